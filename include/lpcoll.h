@@ -78,7 +78,8 @@ typedef enum {
     LPCOLL_OK = 0,
     LPCOLL_ERR_ARG = 1,         /* bad dtype, nranks, or a NULL pointer */
     LPCOLL_ERR_ALIGN = 2,       /* a device pointer not 16-byte aligned */
-    LPCOLL_ERR_UNSUPPORTED = 3, /* block size other than 128 (or 0 where allowed) */
+    LPCOLL_ERR_UNSUPPORTED = 3, /* block size other than 128 (or 0 where allowed),
+                                   or a hidden size above LPCOLL_MAX_HIDDEN */
     LPCOLL_ERR_RANK = 4,        /* NULL entry in a per-rank pointer array */
     LPCOLL_ERR_CUDA = 5         /* the kernel launch failed */
 } lpcoll_status;
@@ -297,6 +298,165 @@ void lpcoll_debug_fail_host_enqueue(long step);
 #define LPCOLL_NOALLOC_MAX_ELEMS (64u * 1024u * 1024u)
 int dda_flat_sim_noalloc(const void *const *in, void *const *out, int nranks,
                          size_t n, lpcoll_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around the collectives of a transformer layer. The pages have no
+ * counterpart: an expert-parallel layer needs them on either side of its
+ * all-to-all and of the allreduce of its row-parallel products.
+ *
+ * Conventions: all of the above, and
+ *   - matrices are row-major without padding: x[ntokens][hidden];
+ *   - a token has topk choices of an expert; slot s = t * topk + k is choice k
+ *     of token t, and ids, weights and slot_row have one entry per slot;
+ *   - two int32 maps tie slots to rows of the experts' side: slot_row[slot] is
+ *     the row of a slot, row_slot[row] the slot of a row, -1 where there is
+ *     none. An entry out of range counts as none: nothing is read or written
+ *     for it;
+ *   - all sums are FP32, in an order that depends on the sizes alone, rounded
+ *     once at the output; the same call gives the same bits again;
+ *   - checks come in the order above; sizes are checked with the dtype
+ *     (LPCOLL_ERR_ARG), and an array of no elements may be NULL.
+ * Limits: rows, slots < 2^31; ntokens * ceil(hidden / 256) < 2^30.
+ * ------------------------------------------------------------------------ */
+#define LPCOLL_MAX_EXPERTS 1024
+#define LPCOLL_MAX_TOPK 32
+#define LPCOLL_MAX_HIDDEN 16384
+
+/* What a gate of residual_norm has one value for. */
+typedef enum {
+    LPCOLL_GATE_NONE = 0,    /* no gate */
+    LPCOLL_GATE_CHANNEL = 1, /* gate[hidden] */
+    LPCOLL_GATE_TOKEN = 2,   /* gate[ntokens] */
+    LPCOLL_GATE_FULL = 3     /* gate[ntokens][hidden] */
+} lpcoll_gate;
+
+/* Router: the topk experts of every token and their weights.
+ *   logits       [ntokens][nexperts] of dtype
+ *   nexperts     1..LPCOLL_MAX_EXPERTS
+ *   topk         1..min(nexperts, LPCOLL_MAX_TOPK)
+ *   renormalize  0: weights = softmax over all experts, at the chosen;
+ *                1: softmax over the chosen only
+ *   ids          out: [ntokens][topk], the largest logits in descending
+ *                order, equal ones lowest index first; an expert with logit
+ *                -infinity is never chosen. Where fewer than topk are left,
+ *                the other entries are -1.
+ *   weights      out: [ntokens][topk] float; 0 where ids is -1
+ * A NaN logit counts as larger than all others. A NaN or +infinity among a
+ * token's logits makes the weights of its chosen experts NaN.               */
+int expert_route(const void *logits, lpcoll_dtype dtype, size_t ntokens, int nexperts,
+                 int topk, int renormalize, int32_t *ids, float *weights, void *stream);
+
+/* Gradient of expert_route's weights.
+ *   ids, weights  as expert_route wrote them for these logits
+ *   dweights      [ntokens][topk] float; not read into the result where ids is -1
+ *   dlogits       out: [ntokens][nexperts] of dtype; may be logits itself
+ * With m = sum_j weights_j dweights_j over the token's choices:
+ *   renormalize 1: weights_j (dweights_j - m) at the chosen, 0 elsewhere
+ *                  (logits is not read and may be NULL);
+ *   renormalize 0: p_e (dweights_e [e chosen] - m), p the softmax of all.   */
+int expert_route_backward(const void *logits, lpcoll_dtype dtype, size_t ntokens,
+                          int nexperts, int topk, int renormalize, const int32_t *ids,
+                          const float *weights, const float *dweights, void *dlogits,
+                          void *stream);
+
+/* Stable sort of the slots by expert.
+ *   ids       [nslots] (ntokens * topk); outside [0, nexperts): no row
+ *   capacity  0: packed. Expert e has the rows [offsets[e], offsets[e+1]),
+ *             its slots in ascending order; there are nslots rows, those from
+ *             offsets[nexperts] on unused.
+ *             C > 0: expert e has the C rows from e * C on (equal chunks, as
+ *             all_to_all_sim moves them); its first C slots get a row, the
+ *             others none. nexperts * C < 2^31 rows.
+ *   slot_row  out: [nslots]       row_slot  out: [rows]
+ *   offsets   out: [nexperts + 1], first row of every expert, then the end
+ *   counts    out: [nexperts], rows that hold a slot
+ *   workspace device memory of expert_sort_workspace_bytes(nslots, nexperts)
+ *             bytes (scratch; 0 bytes up to 2048 slots: may be NULL)          */
+size_t expert_sort_workspace_bytes(size_t nslots, int nexperts);
+int expert_sort(const int32_t *ids, size_t nslots, int nexperts, size_t capacity,
+                int32_t *slot_row, int32_t *row_slot, int32_t *offsets, int32_t *counts,
+                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Tokens to rows: row slot_row[t * topk + k] = x[t], exact or as payload;
+ * rows that row_slot gives no slot are zeros.
+ *   x         [ntokens][hidden] of dtype
+ *   slot_row  [ntokens * topk]   row_slot  [nrows]   (of expert_sort)
+ *   block     0: out [nrows][hidden] of dtype; codes, scales ignored
+ *             128: every row is quantized on its own 128-element blocks into
+ *             codes [nrows][hidden] and scales [nrows][ceil(hidden/128)], with
+ *             lp_quantize's arithmetic; out is ignored. (If hidden is a
+ *             multiple of 128 this is one payload of nrows * hidden elements.)
+ * Its gradient is expert_combine with weights NULL.                         */
+int expert_dispatch(const void *x, size_t ntokens, int topk, size_t nrows, size_t hidden,
+                    lpcoll_dtype dtype, int block, const int32_t *slot_row,
+                    const int32_t *row_slot, void *out, uint8_t *codes, float *scales,
+                    void *stream);
+
+/* Rows back to tokens: out[t] = sum_k weights[t, k] * row slot_row[t, k] in
+ * FP32, k ascending; choices without a row add nothing.
+ *   block     0: rows [nrows][hidden] of dtype; 128: the payload codes, scales
+ *             laid out as expert_dispatch writes it (rows ignored)
+ *   weights   [ntokens * topk] float, or NULL for 1
+ *   out       [ntokens][hidden] of dtype, none of the inputs                 */
+int expert_combine(const void *rows, const uint8_t *codes, const float *scales,
+                   size_t ntokens, int topk, size_t nrows, size_t hidden,
+                   lpcoll_dtype dtype, int block, const int32_t *slot_row,
+                   const float *weights, void *out, void *stream);
+
+/* Gradients of expert_combine (block 0).
+ *   dout      [ntokens][hidden] of dtype
+ *   rows      [nrows][hidden], the rows combined; read only for dweights
+ *   weights   [ntokens * topk] float, or NULL for 1
+ *   drows     out: [nrows][hidden] of dtype, weights[s] * dout[s / topk];
+ *             zeros in rows without a slot; may be rows itself
+ *   dweights  out: [ntokens * topk] float, <rows[slot_row[s]], dout[s / topk]>,
+ *             0 without a row; or NULL if not wanted (then rows may be too)   */
+int expert_combine_backward(const void *dout, const void *rows, size_t ntokens, int topk,
+                            size_t nrows, size_t hidden, lpcoll_dtype dtype,
+                            const int32_t *slot_row, const int32_t *row_slot,
+                            const float *weights, void *drows, float *dweights,
+                            void *stream);
+
+/* End of a block and start of the next, for every token's row:
+ *   h     = sum over r of h[r], FP32 in rank order (the partial products that
+ *           an allreduce would sum; nranks = 1 if it has)
+ *   u     = h / sqrt(mean(h^2) + eps) * w_post       or h if w_post is NULL
+ *   x_out = res_scale * x + branch_scale * gate * u
+ *   n_out = x_out / sqrt(mean(x_out^2) + eps) * w_pre  if w_pre is not NULL
+ * with the unrounded h and x_out going into what follows them.
+ *   h[r], x, x_out, n_out   [ntokens][hidden] of dtype; n_out is ignored if
+ *           w_pre is NULL
+ *   nranks  1..16           hidden  up to LPCOLL_MAX_HIDDEN
+ *   w_post, w_pre           [hidden] of dtype, or NULL
+ *   gate    per gate_kind, of dtype; ignored for LPCOLL_GATE_NONE
+ *   h_sum   out: h rounded to dtype (what the gradient wants), or NULL
+ *   eps     > 0                                                             */
+int residual_norm(const void *const *h, int nranks, const void *x, const void *gate,
+                  int gate_kind, const void *w_post, const void *w_pre, float res_scale,
+                  float branch_scale, float eps, size_t ntokens, size_t hidden,
+                  lpcoll_dtype dtype, void *x_out, void *n_out, void *h_sum, void *stream);
+
+/* Gradients of residual_norm.
+ *   dx_out, dn_out   gradients of the two outputs; dx_out may be NULL (0) if
+ *                    w_pre is given; dn_out is ignored if w_pre is NULL
+ *   h, x_out         the sum h (h_sum, or h[0] of one rank) and the result;
+ *                    the norms' statistics are taken from them again
+ *   dx, dh           out: of x, and of every h[r], [ntokens][hidden] of dtype
+ *   dgate            out: float [hidden] (CHANNEL) or [ntokens] (TOKEN), dtype
+ *                    [ntokens][hidden] (FULL); NULL if not wanted
+ *   dw_post, dw_pre  out: float [hidden]; NULL if not wanted; ignored without
+ *                    their weights
+ *   workspace        residual_norm_backward_workspace_bytes(...) bytes
+ * With ntokens = 0 the sums over tokens are written as zeros.               */
+size_t residual_norm_backward_workspace_bytes(size_t ntokens, size_t hidden,
+                                              lpcoll_dtype dtype);
+int residual_norm_backward(const void *dx_out, const void *dn_out, const void *h,
+                           const void *x_out, const void *gate, int gate_kind,
+                           const void *w_post, const void *w_pre, float res_scale,
+                           float branch_scale, float eps, size_t ntokens, size_t hidden,
+                           lpcoll_dtype dtype, void *dx, void *dh, void *dgate,
+                           float *dw_post, float *dw_pre, void *workspace,
+                           size_t workspace_bytes, void *stream);
 
 /* Bounds checks, a test tool with no counterpart in the method. The
  * bounds-checked build of this library (liblpcoll_debug_bounds.so, compiled

@@ -89,6 +89,7 @@ def _load(path):
               "lp_dequantize_fmt", "lp_reduce_fmt",
               "lpcoll_last_cuda_error", "lpcoll_version"):
         getattr(L, f).restype = ci
+    _declare_layers(L)
     L.lpcoll_status_string.argtypes = [ci]
     L.lpcoll_status_string.restype = ctypes.c_char_p
     L.lpcoll_debug_bounds_errors.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)]
@@ -96,6 +97,30 @@ def _load(path):
     L.lpcoll_debug_bounds_shrink.argtypes = [sz]
     L.lpcoll_debug_bounds_shrink.restype = None
     return L
+
+
+def _declare_layers(L):
+    """C signatures of the operators around the collectives (layers.py)."""
+    vp, sz, ci, cf = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
+    pp = ctypes.POINTER(ctypes.c_void_p)
+    L.expert_route.argtypes = [vp, ci, sz, ci, ci, ci, vp, vp, vp]
+    L.expert_route_backward.argtypes = [vp, ci, sz, ci, ci, ci, vp, vp, vp, vp, vp]
+    L.expert_sort_workspace_bytes.argtypes = [sz, ci]
+    L.expert_sort.argtypes = [vp, sz, ci, sz, vp, vp, vp, vp, vp, sz, vp]
+    L.expert_dispatch.argtypes = [vp, sz, ci, sz, sz, ci, ci, vp, vp, vp, vp, vp, vp]
+    L.expert_combine.argtypes = [vp, vp, vp, sz, ci, sz, sz, ci, ci, vp, vp, vp, vp]
+    L.expert_combine_backward.argtypes = [vp, vp, sz, ci, sz, sz, ci, vp, vp, vp, vp, vp, vp]
+    L.residual_norm.argtypes = [pp, ci, vp, vp, ci, vp, vp, cf, cf, cf, sz, sz, ci, vp, vp, vp,
+                                vp]
+    L.residual_norm_backward_workspace_bytes.argtypes = [sz, sz, ci]
+    L.residual_norm_backward.argtypes = [vp, vp, vp, vp, vp, ci, vp, vp, cf, cf, cf, sz, sz, ci,
+                                         vp, vp, vp, vp, vp, vp, sz, vp]
+    for f in ("expert_route", "expert_route_backward", "expert_sort", "expert_dispatch",
+              "expert_combine", "expert_combine_backward", "residual_norm",
+              "residual_norm_backward"):
+        getattr(L, f).restype = ci
+    for f in ("expert_sort_workspace_bytes", "residual_norm_backward_workspace_bytes"):
+        getattr(L, f).restype = sz
 
 
 def debug_bounds_errors():

@@ -5,13 +5,13 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <initializer_list>
 #ifdef LPCOLL_DEBUG_BOUNDS
 #include <atomic>
 #include <mutex>
 #endif
 
 #include "lpcoll.h"
+#include "lpcoll_checks.h"
 #include "lpcoll_dda.cuh"
 
 namespace lpc {
@@ -37,60 +37,6 @@ cudaError_t launch_all_to_all(const DdaParams &p, int nranks, size_t c, int dtyp
 namespace {
 
 thread_local int g_last_cuda_error = 0;
-
-inline bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
-inline bool bad_dtype(int dtype) { return dtype != LPCOLL_F32 && dtype != LPCOLL_BF16; }
-
-// NULL / alignment check of one per-rank pointer array.
-template <class P>
-int check_rank_array(P const *arr, int nranks)
-{
-    if (arr == nullptr)
-        return LPCOLL_ERR_ARG;
-    for (int r = 0; r < nranks; ++r)
-        if (arr[r] == nullptr)
-            return LPCOLL_ERR_RANK;
-    for (int r = 0; r < nranks; ++r)
-        if (misaligned(arr[r]))
-            return LPCOLL_ERR_ALIGN;
-    return LPCOLL_OK;
-}
-
-int check_ptr(const void *p)
-{
-    if (p == nullptr)
-        return LPCOLL_ERR_ARG;
-    return misaligned(p) ? LPCOLL_ERR_ALIGN : LPCOLL_OK;
-}
-
-int finish(cudaError_t e)
-{
-    if (e == cudaSuccess)
-        return LPCOLL_OK;
-    g_last_cuda_error = static_cast<int>(e);
-    return LPCOLL_ERR_CUDA;
-}
-
-// First non-OK status of a list of checks (NULL before alignment is kept by
-// the order in which callers list them).
-int first_error(std::initializer_list<int> sts)
-{
-    int align = LPCOLL_OK;
-    for (int s : sts) {
-        if (s == LPCOLL_ERR_ALIGN) {
-            if (align == LPCOLL_OK)
-                align = s;
-        } else if (s != LPCOLL_OK) {
-            return s;
-        }
-    }
-    return align;
-}
-
-size_t elem_bytes(int dtype) { return dtype == LPCOLL_F32 ? 4 : 2; }
-
-size_t blocks_of(size_t n, int block) { return (n + block - 1) / block; }
 
 // Bounds-checked build: the buffers of an allreduce-shaped call (inputs read,
 // outputs and wires written, and the tree's shard payload when given).
@@ -510,7 +456,7 @@ const char *lpcoll_status_string(int status)
     case LPCOLL_OK: return "LPCOLL_OK";
     case LPCOLL_ERR_ARG: return "LPCOLL_ERR_ARG: invalid argument or NULL pointer";
     case LPCOLL_ERR_ALIGN: return "LPCOLL_ERR_ALIGN: device pointer not 16-byte aligned";
-    case LPCOLL_ERR_UNSUPPORTED: return "LPCOLL_ERR_UNSUPPORTED: unsupported block size";
+    case LPCOLL_ERR_UNSUPPORTED: return "LPCOLL_ERR_UNSUPPORTED: unsupported block or hidden size";
     case LPCOLL_ERR_RANK: return "LPCOLL_ERR_RANK: NULL pointer in a per-rank array";
     case LPCOLL_ERR_CUDA: return "LPCOLL_ERR_CUDA: kernel launch failed";
     default: return "LPCOLL: unknown status";

@@ -127,8 +127,8 @@ inline void debug_range(const void *, size_t, bool) {}
 // translation unit must copy the buffer list into its own g_debug_ranges, so
 // no two units may share one instantiation of them.
 template <typename... Params, typename... Args>
-static cudaError_t launch_kernel_smem(void (*kernel)(Params...), int grid, size_t smem,
-                                      cudaStream_t stream, Args... args)
+static cudaError_t launch_kernel_block(void (*kernel)(Params...), size_t grid, int threads,
+                                       size_t smem, cudaStream_t stream, Args... args)
 {
 #ifdef LPCOLL_DEBUG_BOUNDS
     const cudaError_t de = cudaMemcpyToSymbolAsync(g_debug_ranges, &debug_pending(),
@@ -142,12 +142,19 @@ static cudaError_t launch_kernel_smem(void (*kernel)(Params...), int grid, size_
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename... Params, typename... Args>
+static cudaError_t launch_kernel_smem(void (*kernel)(Params...), int grid, size_t smem,
+                                      cudaStream_t stream, Args... args)
+{
+    return launch_kernel_block(kernel, static_cast<size_t>(grid), kThreads, smem, stream, args...);
 }
 
 template <typename... Params, typename... Args>

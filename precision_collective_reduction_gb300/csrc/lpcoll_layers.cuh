@@ -1,0 +1,169 @@
+// lpcoll_layers.cuh -- what the kernels around the collectives share (router,
+// sort by expert, dispatch, combine, residual norm): element access at a
+// row's own alignment, sums over a warp and a CTA, and the launchers.
+//
+// Rows of these operators are `hidden` elements long and follow one another
+// without padding, so a row starts on a 16-byte boundary only if its length
+// in bytes is a multiple of 16. Each kernel exists for both cases (VEC): one
+// 16-byte vector per access, or one element.
+#pragma once
+
+#include "lpcoll_device.cuh"
+
+namespace lpc {
+
+// One access of a lane: 16 bytes (VEC) or one element.
+template <int DT, bool VEC> struct Pack {
+    using Raw = uint4;
+    static constexpr int kN = Fmt<DT>::kVec;
+};
+template <> struct Pack<LPCOLL_F32, false> {
+    using Raw = uint32_t;
+    static constexpr int kN = 1;
+};
+template <> struct Pack<LPCOLL_BF16, false> {
+    using Raw = uint16_t;
+    static constexpr int kN = 1;
+};
+
+inline size_t dtype_bytes(int dtype) { return dtype == LPCOLL_F32 ? 4 : 2; }
+
+// Whether rows of `hidden` elements all start on a 16-byte boundary.
+inline bool rows_aligned(size_t hidden, int dtype) { return hidden * dtype_bytes(dtype) % 16 == 0; }
+
+template <int DT, bool VEC>
+__device__ __forceinline__ typename Pack<DT, VEC>::Raw load_pack(const void *base, size_t e0)
+{
+    using Raw = typename Pack<DT, VEC>::Raw;
+    constexpr int kEs = sizeof(Raw) / Pack<DT, VEC>::kN;
+    const Raw *p = reinterpret_cast<const Raw *>(static_cast<const char *>(base) + e0 * kEs);
+    return LPC_READ_OK(p, sizeof(Raw)) ? *p : Raw{};
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void store_pack(void *base, size_t e0, typename Pack<DT, VEC>::Raw v)
+{
+    using Raw = typename Pack<DT, VEC>::Raw;
+    constexpr int kEs = sizeof(Raw) / Pack<DT, VEC>::kN;
+    Raw *p = reinterpret_cast<Raw *>(static_cast<char *>(base) + e0 * kEs);
+    if (LPC_WRITE_OK(p, sizeof(Raw)))
+        *p = v;
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void widen_pack(typename Pack<DT, VEC>::Raw v,
+                                           float (&x)[Pack<DT, VEC>::kN])
+{
+    if constexpr (VEC)
+        widen<DT>(v, x);
+    else if constexpr (DT == LPCOLL_F32)
+        x[0] = __uint_as_float(v);
+    else
+        x[0] = __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ typename Pack<DT, VEC>::Raw
+narrow_pack(const float (&x)[Pack<DT, VEC>::kN])
+{
+    if constexpr (VEC)
+        return narrow<DT>(x);
+    else if constexpr (DT == LPCOLL_F32)
+        return __float_as_uint(x[0]);
+    else
+        return __bfloat16_as_ushort(__float2bfloat16_rn(x[0]));
+}
+
+__device__ __forceinline__ int32_t load_i32(const int32_t *p)
+{
+    return LPC_READ_OK(p, sizeof(int32_t)) ? *p : 0;
+}
+
+__device__ __forceinline__ void store_i32(int32_t *p, int32_t v)
+{
+    if (LPC_WRITE_OK(p, sizeof(int32_t)))
+        *p = v;
+}
+
+__device__ __forceinline__ float load_f32(const float *p)
+{
+    return LPC_READ_OK(p, sizeof(float)) ? *p : 0.0f;
+}
+
+__device__ __forceinline__ void store_f32(float *p, float v)
+{
+    if (LPC_WRITE_OK(p, sizeof(float)))
+        *p = v;
+}
+
+// Sum over the lanes of a warp, the same bits in every lane and run.
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+    return v;
+}
+
+// -- launchers (one translation unit each; called by lpcoll_layers_api.cu) --
+
+struct RouteArgs {
+    const void *logits;
+    int32_t *ids;
+    float *weights;
+    const float *dweights;  // backward
+    void *dlogits;          // backward
+    size_t tokens;
+    int experts, topk, renormalize, dtype;
+};
+cudaError_t launch_route(const RouteArgs &a, cudaStream_t st);
+cudaError_t launch_route_backward(const RouteArgs &a, cudaStream_t st);
+
+struct SortArgs {
+    const int32_t *ids;
+    int32_t *slot_row, *row_slot, *offsets, *counts;
+    int32_t *chunk_counts;  // workspace: [chunks][experts]
+    int slots, experts, capacity, rows;
+    int chunks, chunk_len;
+};
+// Chunks (CTAs) that a sort of `slots` slots runs in; 1 needs no workspace.
+int sort_chunks(size_t slots);
+cudaError_t launch_sort(SortArgs a, cudaStream_t st);
+
+struct RowsArgs {
+    const void *x;       // tokens' side: [tokens, hidden] (dispatch: read, backward: dout)
+    void *out;           // the other side, written
+    const void *rows;    // experts' side, read (combine and its backward)
+    uint8_t *codes;      // experts' side as FP8 payloads
+    float *scales;
+    const float *weights;
+    float *dweights;
+    const int32_t *slot_row, *row_slot;
+    size_t tokens, nrows, hidden;
+    int topk, dtype;
+};
+cudaError_t launch_dispatch(const RowsArgs &a, bool lp, cudaStream_t st);
+cudaError_t launch_combine(const RowsArgs &a, bool lp, cudaStream_t st);
+cudaError_t launch_combine_backward(const RowsArgs &a, cudaStream_t st);
+
+struct NormArgs {
+    const void *h[LPCOLL_MAX_RANKS];
+    int nranks;
+    const void *x, *gate, *w_post, *w_pre;
+    void *x_out, *n_out, *h_sum;
+    // backward: x holds x_out, h[0] the block's output
+    const void *dx_out, *dn_out;
+    void *dx, *dh, *dgate;
+    float *dw_post, *dw_pre;
+    float *partial;  // workspace of the sums over tokens
+    int gate_kind;
+    float res_scale, branch_scale, eps;
+    size_t tokens;
+    int hidden, dtype;
+};
+// Partial sums over tokens that a backward call keeps (CTAs of its row kernel).
+int norm_backward_parts(size_t tokens, size_t hidden, int dtype);
+cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t st);
+cudaError_t launch_residual_norm_backward(const NormArgs &a, cudaStream_t st);
+
+}  // namespace lpc
