@@ -4,74 +4,99 @@
 //
 // Rows of these operators are `hidden` elements long and follow one another
 // without padding, so a row starts on a 16-byte boundary only if its length
-// in bytes is a multiple of 16. Each kernel exists for both cases (VEC): one
-// 16-byte vector per access, or one element.
+// in bytes is a multiple of 16. Each kernel exists for accesses of W = 16
+// bytes, of 4 bytes (FP32 rows of any length, BF16 rows of even length) and
+// of 2 bytes (BF16 rows of odd length).
 #pragma once
 
 #include "lpcoll_device.cuh"
 
 namespace lpc {
 
-// One access of a lane: 16 bytes (VEC) or one element.
-template <int DT, bool VEC> struct Pack {
+// One access of a lane: W bytes.
+template <int DT, int W> struct Pack;
+template <int DT> struct Pack<DT, 16> {
     using Raw = uint4;
     static constexpr int kN = Fmt<DT>::kVec;
 };
-template <> struct Pack<LPCOLL_F32, false> {
+template <int DT> struct Pack<DT, 4> {
     using Raw = uint32_t;
-    static constexpr int kN = 1;
+    static constexpr int kN = Fmt<DT>::kVec / 4;
 };
-template <> struct Pack<LPCOLL_BF16, false> {
+template <> struct Pack<LPCOLL_BF16, 2> {
     using Raw = uint16_t;
     static constexpr int kN = 1;
 };
+// The narrowest access: one element.
+template <int DT> constexpr int kOne = 16 / Fmt<DT>::kVec;
 
 inline size_t dtype_bytes(int dtype) { return dtype == LPCOLL_F32 ? 4 : 2; }
 
-// Whether rows of `hidden` elements all start on a 16-byte boundary.
-inline bool rows_aligned(size_t hidden, int dtype) { return hidden * dtype_bytes(dtype) % 16 == 0; }
-
-template <int DT, bool VEC>
-__device__ __forceinline__ typename Pack<DT, VEC>::Raw load_pack(const void *base, size_t e0)
+// Access width that every row of `hidden` elements allows.
+inline int row_width(size_t hidden, int dtype)
 {
-    using Raw = typename Pack<DT, VEC>::Raw;
-    constexpr int kEs = sizeof(Raw) / Pack<DT, VEC>::kN;
+    const size_t bytes = hidden * dtype_bytes(dtype);
+    return bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
+}
+
+// fn<dtype, width>(...) for a call's dtype and row length.
+#define LPC_BY_ROW(fn, dtype, hidden, ...)                                                   \
+    ((dtype) == LPCOLL_F32                                                                   \
+         ? (row_width(hidden, dtype) == 16 ? fn<LPCOLL_F32, 16>(__VA_ARGS__)                 \
+                                           : fn<LPCOLL_F32, 4>(__VA_ARGS__))                 \
+         : (row_width(hidden, dtype) == 16                                                   \
+                ? fn<LPCOLL_BF16, 16>(__VA_ARGS__)                                           \
+                : (row_width(hidden, dtype) == 4 ? fn<LPCOLL_BF16, 4>(__VA_ARGS__)           \
+                                                 : fn<LPCOLL_BF16, 2>(__VA_ARGS__))))
+
+template <int DT, int W>
+__device__ __forceinline__ typename Pack<DT, W>::Raw load_pack(const void *base, size_t e0)
+{
+    using Raw = typename Pack<DT, W>::Raw;
+    constexpr int kEs = sizeof(Raw) / Pack<DT, W>::kN;
     const Raw *p = reinterpret_cast<const Raw *>(static_cast<const char *>(base) + e0 * kEs);
     return LPC_READ_OK(p, sizeof(Raw)) ? *p : Raw{};
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void store_pack(void *base, size_t e0, typename Pack<DT, VEC>::Raw v)
+template <int DT, int W>
+__device__ __forceinline__ void store_pack(void *base, size_t e0, typename Pack<DT, W>::Raw v)
 {
-    using Raw = typename Pack<DT, VEC>::Raw;
-    constexpr int kEs = sizeof(Raw) / Pack<DT, VEC>::kN;
+    using Raw = typename Pack<DT, W>::Raw;
+    constexpr int kEs = sizeof(Raw) / Pack<DT, W>::kN;
     Raw *p = reinterpret_cast<Raw *>(static_cast<char *>(base) + e0 * kEs);
     if (LPC_WRITE_OK(p, sizeof(Raw)))
         *p = v;
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void widen_pack(typename Pack<DT, VEC>::Raw v,
-                                           float (&x)[Pack<DT, VEC>::kN])
+template <int DT, int W>
+__device__ __forceinline__ void widen_pack(typename Pack<DT, W>::Raw v,
+                                           float (&x)[Pack<DT, W>::kN])
 {
-    if constexpr (VEC)
+    if constexpr (W == 16) {
         widen<DT>(v, x);
-    else if constexpr (DT == LPCOLL_F32)
+    } else if constexpr (DT == LPCOLL_F32) {
         x[0] = __uint_as_float(v);
-    else
+    } else {
         x[0] = __uint_as_float(static_cast<uint32_t>(v) << 16);
+        if constexpr (W == 4)
+            x[1] = __uint_as_float(v & 0xFFFF0000u);
+    }
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ typename Pack<DT, VEC>::Raw
-narrow_pack(const float (&x)[Pack<DT, VEC>::kN])
+template <int DT, int W>
+__device__ __forceinline__ typename Pack<DT, W>::Raw
+narrow_pack(const float (&x)[Pack<DT, W>::kN])
 {
-    if constexpr (VEC)
+    if constexpr (W == 16) {
         return narrow<DT>(x);
-    else if constexpr (DT == LPCOLL_F32)
+    } else if constexpr (DT == LPCOLL_F32) {
         return __float_as_uint(x[0]);
-    else
+    } else if constexpr (W == 4) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[0], x[1]);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
         return __bfloat16_as_ushort(__float2bfloat16_rn(x[0]));
+    }
 }
 
 __device__ __forceinline__ int32_t load_i32(const int32_t *p)

@@ -54,7 +54,7 @@ size_t gate_elems(int gate_kind, size_t ntokens, size_t hidden)
 
 size_t norm_workspace(size_t ntokens, size_t hidden, int dtype)
 {
-    return static_cast<size_t>(3) * norm_backward_parts(ntokens, hidden, dtype) * hidden *
+    return static_cast<size_t>(2) * norm_backward_parts(ntokens, hidden, dtype) * hidden *
            sizeof(float);
 }
 
@@ -388,7 +388,7 @@ int residual_norm_backward(const void *dx_out, const void *dn_out, const void *h
                                                             : check_array(dx_out, count),
                       w_pre != nullptr ? check_array(dn_out, count) : LPCOLL_OK,
                       check_array(h, count), check_array(x_out, count),
-                      gate_kind != LPCOLL_GATE_NONE ? check_array(gate, count) : LPCOLL_OK,
+                      check_array(gate, gate_elems(gate_kind, ntokens, hidden)),
                       check_optional(w_post), check_optional(w_pre), check_array(dx, count),
                       check_array(dh, count), check_optional(dgate), check_optional(dw_post),
                       check_optional(dw_pre), check_array(workspace, need)});

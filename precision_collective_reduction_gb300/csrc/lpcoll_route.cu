@@ -42,7 +42,7 @@ __device__ __forceinline__ void load_logits(const void *logits, size_t t, int ex
         const int e = i * 32 + lane;
         x[i] = -INFINITY;
         if (e < experts) {
-            widen_pack<DT, false>(load_pack<DT, false>(logits, t * experts + e), one);
+            widen_pack<DT, kOne<DT>>(load_pack<DT, kOne<DT>>(logits, t * experts + e), one);
             x[i] = one[0];
         }
     }
@@ -152,10 +152,10 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteArg
                 x[i] = expf(x[i] - m);
                 sum += x[i];
             }
-            sum = warp_sum(sum);
+            const float f = __fdiv_rn(-mean, warp_sum(sum));
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                d[i] = __fmul_rn(-mean, __fdiv_rn(x[i], sum));
+                d[i] = __fmul_rn(f, x[i]);
         }
     }
     for (int j = 0; j < a.topk; ++j) {
@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteArg
         const int e = i * 32 + lane;
         const float one[1] = {d[i]};
         if (e < a.experts)
-            store_pack<DT, false>(a.dlogits, t * a.experts + e, narrow_pack<DT, false>(one));
+            store_pack<DT, kOne<DT>>(a.dlogits, t * a.experts + e,
+                                     narrow_pack<DT, kOne<DT>>(one));
     }
 }
 
@@ -184,8 +185,10 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteArg
 // result does not depend on the order in which anything runs.
 // ---------------------------------------------------------------------------
 
-// A chunk of one CTA: 8 warps of 8 steps of 32 slots.
-constexpr int kSortChunk = 2048;
+// The largest sort of one launch, in one CTA, and the smallest chunk of others:
+// 8 warps of 8, or of 2, steps of 32 slots.
+constexpr int kSortOne = 2048;
+constexpr int kSortChunk = 512;
 constexpr int kSortMaxChunks = 128;
 
 __device__ __forceinline__ int slot_expert(const SortArgs &a, int s)
@@ -375,6 +378,8 @@ cudaError_t launch_route_backward(const RouteArgs &a, cudaStream_t st)
 
 static int sort_chunk_len(size_t slots)
 {
+    if (slots <= kSortOne)
+        return kSortOne;
     const size_t even = (slots + kSortMaxChunks - 1) / kSortMaxChunks;
     const size_t len = (even + kThreads - 1) / kThreads * kThreads;
     return static_cast<int>(len > kSortChunk ? len : kSortChunk);

@@ -20,20 +20,31 @@ MAX_HIDDEN = 16384
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
 torch = None  # imported by the first call, as everywhere in the binding
+_raw_stream = None
 _DTYPE = {}
 
 
 def _device():
     """Index of the current CUDA device, which every call runs on."""
-    global torch
+    global torch, _raw_stream
     if torch is None:
         torch = B._torch()
+        # the current stream's handle without a Stream object around it
+        _raw_stream = torch._C._cuda_getCurrentRawStream
         _DTYPE.update({torch.float32: B.F32, torch.bfloat16: B.BF16})
     return torch.cuda.current_device()
 
 
 def _ptr(t, what, dtype, shape, device):
     """Device pointer of a tensor of that type, shape and device."""
+    # the checks of a good tensor in as few calls as they take: at decode sizes
+    # they cost more than the kernels
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % what)
     if t.dtype != dtype:
@@ -44,9 +55,7 @@ def _ptr(t, what, dtype, shape, device):
     if t.get_device() != device:  # -1 for a host tensor
         raise ValueError("%s must be a CUDA tensor of the current device cuda:%d, is on %s"
                          % (what, device, t.device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % what)
 
 
 def _opt(t, what, dtype, shape, device):
@@ -54,16 +63,23 @@ def _opt(t, what, dtype, shape, device):
 
 
 def _shape(t, dims, what):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % what)
-    if t.dim() != dims:
-        raise ValueError("%s must have %d dimensions, got %s" % (what, dims, tuple(t.shape)))
-    return t.shape
+    try:
+        shape = t.shape
+        if len(shape) == dims:
+            return shape
+    except AttributeError:
+        raise TypeError("%s must be a torch.Tensor" % what) from None
+    raise ValueError("%s must have %d dimensions, got %s" % (what, dims, tuple(shape)))
 
 
 def _code(t):
     code = _DTYPE.get(t.dtype)
     return B.dtype_code(t) if code is None else code
+
+
+def _stream(stream, device):
+    """cudaStream_t of the call; None is the current stream."""
+    return _raw_stream(device) if stream is None else B._stream(stream)
 
 
 def _scratch(workspace, need, stream, device):
@@ -76,8 +92,10 @@ def _scratch(workspace, need, stream, device):
         if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
         else:
-            s = torch.cuda.ExternalStream(B._stream(stream))
-            with torch.cuda.stream(s):
+            if isinstance(stream, int):
+                stream = (torch.cuda.ExternalStream(stream) if stream
+                          else torch.cuda.default_stream())
+            with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
     n = workspace.numel()
     p = _ptr(workspace, "workspace", torch.uint8, (n,), device)
@@ -105,7 +123,7 @@ def expert_route(logits, ids, weights, renormalize=False, stream=None):
     ip = _ptr(ids, "ids", torch.int32, (T, K), dev)
     wp = _ptr(weights, "weights", torch.float32, (T, K), dev)
     B._check(B.lib().expert_route(lp, _code(logits), T, E, K, 1 if renormalize else 0, ip, wp,
-                                  B._stream(stream)), "expert_route")
+                                  _stream(stream, dev)), "expert_route")
     return ids, weights
 
 
@@ -122,7 +140,7 @@ def expert_route_backward(logits, ids, weights, dweights, dlogits, renormalize=F
     gp = _ptr(dweights, "dweights", torch.float32, (T, K), dev)
     op = _ptr(dlogits, "dlogits", logits.dtype, (T, E), dev)
     B._check(B.lib().expert_route_backward(lp, _code(logits), T, E, K, 1 if renormalize else 0,
-                                           ip, wp, gp, op, B._stream(stream)),
+                                           ip, wp, gp, op, _stream(stream, dev)),
              "expert_route_backward")
     return dlogits
 
@@ -153,7 +171,7 @@ def expert_sort(ids, nexperts, slot_row, row_slot, offsets, counts, capacity=0,
     need = L.expert_sort_workspace_bytes(T * K, nexperts)
     wp, wn, _keep = _scratch(workspace, need, stream, dev)
     B._check(L.expert_sort(p[0], T * K, nexperts, capacity, p[1], p[2], p[3], p[4], wp, wn,
-                           B._stream(stream)), "expert_sort")
+                           _stream(stream, dev)), "expert_sort")
     return slot_row, row_slot, offsets, counts
 
 
@@ -182,7 +200,7 @@ def expert_dispatch(x, slot_row, row_slot, out=None, block=0, codes=None, scales
     else:
         op = _ptr(out, "out", x.dtype, (R, H), dev)
     B._check(B.lib().expert_dispatch(xp, T, K, R, H, _code(x), block, sp, rp, op, cp, qp,
-                                     B._stream(stream)), "expert_dispatch")
+                                     _stream(stream, dev)), "expert_dispatch")
     return (codes, scales) if block else out
 
 
@@ -211,7 +229,7 @@ def expert_combine(slot_row, out, rows=None, weights=None, block=0, codes=None, 
         rp = _ptr(rows, "rows", out.dtype, (R, H), dev)
     wp = _opt(weights, "weights", torch.float32, (T, K), dev)
     B._check(B.lib().expert_combine(rp, cp, qp, T, K, R, H, _code(out), block, sp, wp, op,
-                                    B._stream(stream)), "expert_combine")
+                                    _stream(stream, dev)), "expert_combine")
     return out
 
 
@@ -233,26 +251,21 @@ def expert_combine_backward(dout, slot_row, row_slot, drows, rows=None, weights=
          _ptr(drows, "drows", dt, (R, H), dev),
          _opt(dweights, "dweights", torch.float32, (T, K), dev))
     B._check(B.lib().expert_combine_backward(p[0], p[1], T, K, R, H, _code(dout), p[2], p[3],
-                                             p[4], p[5], p[6], B._stream(stream)),
+                                             p[4], p[5], p[6], _stream(stream, dev)),
              "expert_combine_backward")
     return drows, dweights
 
 
 def _gate(gate, dtype, T, H, dev, kind):
-    """(kind, pointer) of a gate of shape [H], [T] or [T, H]. ``kind`` names
-    it where T == H would leave it open."""
+    """(kind, pointer) of a gate of shape [H], [T] or [T, H]. A gate of one
+    dimension is one value per channel if it has H values, whatever T is;
+    ``kind`` says otherwise."""
     if gate is None:
         return GATE_NONE, None
     if not isinstance(gate, torch.Tensor):
         raise TypeError("gate must be a torch.Tensor")
     if kind is None:
-        if gate.dim() == 2:
-            kind = "full"
-        elif T == H:
-            raise ValueError("a gate of %d values may be one per channel or one per token: "
-                             "say gate_kind='channel' or 'token'" % T)
-        else:
-            kind = "token" if gate.shape == (T,) else "channel"
+        kind = "full" if gate.dim() == 2 else "channel" if gate.shape == (H,) else "token"
     if kind not in ("channel", "token", "full"):
         raise ValueError("gate_kind must be 'channel', 'token' or 'full', got %r" % (kind,))
     shape = {"channel": (H,), "token": (T,), "full": (T, H)}[kind]
@@ -266,7 +279,9 @@ def residual_norm(h, x, x_out, n_out=None, gate=None, w_post=None, w_pre=None, r
     16 ranks) is summed and, with ``w_post`` [H], RMS-normed, gated (``gate``
     [H], [T] or [T, H]) and added to the residual x: x_out = res_scale * x +
     branch_scale * gate * u. With ``w_pre`` [H], n_out is the RMS norm of
-    x_out. ``h_sum`` receives the summed h."""
+    x_out. ``h_sum`` receives the summed h. ``gate_kind`` ("channel", "token",
+    "full") names the gate's kind; without it the shape does, and [H] goes
+    before [T] where the two are equal."""
     dev = _device()
     if isinstance(h, torch.Tensor):
         h = (h,)
@@ -286,7 +301,7 @@ def residual_norm(h, x, x_out, n_out=None, gate=None, w_post=None, w_pre=None, r
     sp = _opt(h_sum, "h_sum", dt, (T, H), dev)
     B._check(B.lib().residual_norm(B.ptr_array(hp), len(hp), xp, gp, kind, post, pre, res_scale,
                                    branch_scale, eps, T, H, _code(x), op, np_, sp,
-                                   B._stream(stream)), "residual_norm")
+                                   _stream(stream, dev)), "residual_norm")
     return x_out, n_out
 
 
@@ -328,6 +343,6 @@ def residual_norm_backward(dx_out, dn_out, h, x_out, dx, dh, gate=None, w_post=N
     wp, wn, _keep = _scratch(workspace, need, stream, dev)
     B._check(L.residual_norm_backward(p[0], p[1], p[2], p[3], gp, kind, post, pre, res_scale,
                                       branch_scale, eps, T, H, code, q[0], q[1], q[2], q[3],
-                                      q[4], wp, wn, B._stream(stream)),
+                                      q[4], wp, wn, _stream(stream, dev)),
              "residual_norm_backward")
     return dx, dh

@@ -404,6 +404,17 @@ def test_residual_norm_backward(lib, dt, T, H, kind, post, pre):
     assert torch.equal(both[0], dx) and torch.equal(hh, dh)
 
 
+def test_gate_of_one_dimension_where_both_fit():
+    # as many tokens as channels: per channel, unless the kind says otherwise
+    x = torch.ones(4, 4, device="cuda")
+    gate = torch.arange(4.0, device="cuda")
+    out = torch.empty_like(x)
+    pcr.residual_norm(x, torch.zeros_like(x), out, gate=gate)
+    assert torch.equal(out, gate.expand(4, 4))
+    pcr.residual_norm(x, torch.zeros_like(x), out, gate=gate, gate_kind="token")
+    assert torch.equal(out, gate[:, None].expand(4, 4))
+
+
 def test_norm_gradient_of_no_tokens(lib):
     H = 40
     z = torch.empty(0, H, device="cuda")
@@ -557,7 +568,9 @@ def test_refusals():
     with pytest.raises(ValueError):
         pcr.residual_norm(x, x, x, gate=f(H + 1))
     with pytest.raises(ValueError, match="gate_kind"):
-        pcr.residual_norm(f(8, 8), f(8, 8), f(8, 8), gate=f(8))
+        pcr.residual_norm(x, x, x, gate=f(H), gate_kind="row")
+    with pytest.raises(ValueError):
+        pcr.residual_norm(x, x, x, gate=f(T), gate_kind="channel")
     with pytest.raises(pcr.LpcollError) as e:
         pcr.residual_norm(f(1, 16388), f(1, 16388), f(1, 16388))
     assert e.value.status == 3
