@@ -14,7 +14,11 @@
 //
 // A row belongs to a "team" of whole warps: a part of a CTA for short rows, a
 // CTA, or the CTAs of a cluster, which add up their sums through distributed
-// shared memory. A thread of a team always holds the same columns.
+// shared memory. A thread of a team always holds the same columns, so what
+// the weights and gates of a channel give stays in its registers, and a team
+// goes through its rows one after the other while its next rows are on their
+// way into shared memory (cp.async): each thread copies and reads its own
+// columns only, so no barrier guards them.
 #include "lpcoll_layers.cuh"
 
 namespace lpc {
@@ -23,13 +27,19 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kSms = 152;
-constexpr int kNormThreads = 512;  // largest CTA
-constexpr int kNormWarps = kNormThreads / 32;
+// A thread holds kElems = 8 or 16 columns. An SM holds two CTAs of kThreadsTwo
+// threads, with several teams if the rows are short, or one of kThreadsOne, at
+// 64 or 128 registers a thread.
+template <int kElems> constexpr int kThreadsOne = 8192 / kElems;
+template <int kElems> constexpr int kThreadsTwo = 4096 / kElems;
+constexpr int kMaxWarps = kThreadsOne<8> / 32;
+constexpr int kMaxStages = 4;
 
 // How rows are dealt out: `threads` lanes of each of `cluster` CTAs share a
-// row, `packs` accesses of it per CTA; a CTA has `groups` such teams.
+// row, `packs` accesses of it per CTA; a CTA has `groups` such teams and a
+// ring of `stages` rows for each.
 struct Deal {
-    int threads, groups, cluster, packs;
+    int threads, groups, cluster, packs, stages;
 };
 
 __device__ __forceinline__ unsigned cluster_rank()
@@ -56,179 +66,417 @@ __device__ __forceinline__ float cluster_load(const float *p, unsigned rank)
     return v;
 }
 
+// Waits for the threads of this team: of all CTAs of its cluster, of its CTA,
+// or of its part of a CTA (barriers 1.. of the CTA, one per team).
+__device__ __forceinline__ void team_barrier(const Deal &deal)
+{
+    if (deal.cluster > 1)
+        cluster_barrier();
+    else if (deal.groups == 1)
+        __syncthreads();
+    else if (deal.threads == 32)
+        __syncwarp();
+    else  // at most 8 teams of 64 threads or more
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / deal.threads),
+                     "r"(deal.threads)
+                     : "memory");
+}
+
 // Sums over a team of N <= 8 values per thread, the same bits in every thread
 // of the team and in every run. The lanes first split the values between them
 // (each step halves both the values a lane holds and the lanes that share
 // one), 9 shuffles instead of 5 N; the warps' sums then meet in `red`. The
 // caller alternates between two `red`, so that one barrier is enough.
+// first_warp: the team's first in its CTA.
 template <int N>
-__device__ __forceinline__ void team_sums(float (&v)[N], float (*red)[8], const Deal &deal)
+__device__ __forceinline__ void team_sums(float (&v)[N], float (*red)[8], const Deal &deal,
+                                          int first_warp)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int warps = deal.threads >> 5;
-    float s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        s[i] = i < N ? v[i < N ? i : 0] : 0.0f;
-    // after this lane l holds the sum of value (l & 7) over 4 of the 32 lanes
-#pragma unroll
-    for (int half = 4; half >= 1; half >>= 1) {
-        const bool up = (lane & half) != 0;
-#pragma unroll
-        for (int i = 0; i < half; ++i) {
-            const float give = up ? s[i] : s[i + half];
-            const float keep = up ? s[i + half] : s[i];
-            s[i] = keep + __shfl_xor_sync(kAll, give, half);
+    const bool many = warps > 1 || deal.cluster > 1;
+    if constexpr (N == 1) {
+        float sum = warp_sum(v[0]);
+        if (many) {
+            if (lane == 0)
+                red[warp][0] = sum;
+            team_barrier(deal);
+            sum = 0.0f;
+            if (deal.cluster == 1) {
+                if (lane < warps)
+                    sum = red[first_warp + lane][0];
+            } else if (lane < warps) {
+                for (int c = 0; c < deal.cluster; ++c)
+                    sum += cluster_load(&red[lane][0], c);
+            }
+            sum = warp_sum(sum);
         }
-    }
-    float sum = s[0];
-    sum += __shfl_xor_sync(kAll, sum, 8);
-    sum += __shfl_xor_sync(kAll, sum, 16);
-    const int entries = warps * deal.cluster;
-    if (entries > 1) {
-        if (lane < 8)
-            red[warp][lane] = sum;
-        if (deal.cluster > 1)
-            cluster_barrier();
-        else
-            __syncthreads();
-        const int first = warp / warps * warps;  // of this team in its CTA
-        sum = 0.0f;
-        for (int e = lane >> 3; e < entries; e += 4) {
-            const float *p = &red[first + e % warps][lane & 7];
-            sum += deal.cluster > 1 ? cluster_load(p, e / warps) : *p;
+        v[0] = sum;
+    } else {
+        float s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s[i] = i < N ? v[i < N ? i : 0] : 0.0f;
+        // after this lane l holds the sum of value (l & 7) over 4 of the 32 lanes
+#pragma unroll
+        for (int half = 4; half >= 1; half >>= 1) {
+            const bool up = (lane & half) != 0;
+#pragma unroll
+            for (int i = 0; i < half; ++i) {
+                const float give = up ? s[i] : s[i + half];
+                const float keep = up ? s[i + half] : s[i];
+                s[i] = keep + __shfl_xor_sync(kAll, give, half);
+            }
         }
+        float sum = s[0];
         sum += __shfl_xor_sync(kAll, sum, 8);
         sum += __shfl_xor_sync(kAll, sum, 16);
-    }
+        if (many) {
+            if (lane < 8)
+                red[warp][lane] = sum;
+            team_barrier(deal);
+            sum = 0.0f;
+            if (deal.cluster == 1) {
+                for (int w = lane >> 3; w < warps; w += 4)
+                    sum += red[first_warp + w][lane & 7];
+            } else {
+                for (int c = 0; c < deal.cluster; ++c)
+                    for (int w = lane >> 3; w < warps; w += 4)
+                        sum += cluster_load(&red[w][lane & 7], c);
+            }
+            sum += __shfl_xor_sync(kAll, sum, 8);
+            sum += __shfl_xor_sync(kAll, sum, 16);
+        }
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        v[i] = __shfl_sync(kAll, sum, i);
+        for (int i = 0; i < N; ++i)
+            v[i] = __shfl_sync(kAll, sum, i);
+    }
 }
 
-// 1 / sqrt(mean of squares + eps)
-__device__ __forceinline__ float inv_rms(float sum, int hidden, float eps)
+// 1 / sqrt(mean of squares + eps); rsqrtf is good to 2 ulp.
+__device__ __forceinline__ float inv_rms(float sum, float per_hidden, float eps)
 {
-    return __frsqrt_rn(__fdiv_rn(sum, static_cast<float>(hidden)) + eps);
+    return rsqrtf(fmaf(sum, per_hidden, eps));
+}
+
+// N FP32 values, multiplied and added two at a time where N is even (each
+// lane of a packed operation rounds as the scalar one does).
+template <int N> struct Vec {
+    float v[N];
+};
+
+template <int N> __device__ __forceinline__ Vec<N> splat(float x)
+{
+    Vec<N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        r.v[j] = x;
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ Vec<N> mul(const Vec<N> &a, const Vec<N> &b)
+{
+    Vec<N> r;
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j += 2)
+            asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+                "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+                : "=f"(r.v[j]), "=f"(r.v[j + 1])
+                : "f"(a.v[j]), "f"(a.v[j + 1]), "f"(b.v[j]), "f"(b.v[j + 1]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            r.v[j] = __fmul_rn(a.v[j], b.v[j]);
+    }
+    return r;
+}
+
+template <int N> __device__ __forceinline__ Vec<N> mul(float a, const Vec<N> &b)
+{
+    return mul(splat<N>(a), b);
+}
+
+// a b + c
+template <int N>
+__device__ __forceinline__ Vec<N> fma(const Vec<N> &a, const Vec<N> &b, const Vec<N> &c)
+{
+    Vec<N> r;
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j += 2)
+            asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+                "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+                : "=f"(r.v[j]), "=f"(r.v[j + 1])
+                : "f"(a.v[j]), "f"(a.v[j + 1]), "f"(b.v[j]), "f"(b.v[j + 1]), "f"(c.v[j]),
+                  "f"(c.v[j + 1]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            r.v[j] = __fmaf_rn(a.v[j], b.v[j], c.v[j]);
+    }
+    return r;
+}
+
+template <int N> __device__ __forceinline__ Vec<N> fma(float a, const Vec<N> &b, const Vec<N> &c)
+{
+    return fma(splat<N>(a), b, c);
+}
+
+template <int N> __device__ __forceinline__ Vec<N> add(const Vec<N> &a, const Vec<N> &b)
+{
+    return fma(splat<N>(1.0f), a, b);
+}
+
+// Partial sums of a thread's products: two, or one where values come singly.
+template <int N> using Acc = Vec<N % 2 == 0 ? 2 : 1>;
+
+template <int N>
+__device__ __forceinline__ void add_products(Acc<N> &acc, const Vec<N> &a, const Vec<N> &b)
+{
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j += 2)
+            acc = fma(Vec<2>{{a.v[j], a.v[j + 1]}}, Vec<2>{{b.v[j], b.v[j + 1]}}, acc);
+    } else {
+        acc = fma(a, b, acc);
+    }
+}
+
+__device__ __forceinline__ float fold(const Vec<2> &a) { return a.v[0] + a.v[1]; }
+__device__ __forceinline__ float fold(const Vec<1> &a) { return a.v[0]; }
+
+template <int DT, int W>
+__device__ __forceinline__ Vec<Pack<DT, W>::kN> unpack(typename Pack<DT, W>::Raw raw)
+{
+    Vec<Pack<DT, W>::kN> r;
+    widen_pack<DT, W>(raw, r.v);
+    return r;
+}
+
+template <int DT, int W>
+__device__ __forceinline__ Vec<Pack<DT, W>::kN> load_vec_of(const void *base, size_t e0)
+{
+    return unpack<DT, W>(load_pack<DT, W>(base, e0));
+}
+
+template <int DT, int W>
+__device__ __forceinline__ void store_vec_of(void *base, size_t e0,
+                                             const Vec<Pack<DT, W>::kN> &x)
+{
+    store_pack<DT, W>(base, e0, narrow_pack<DT, W>(x.v));
+}
+
+// W (16 or 4) bytes from global into this thread's place in shared memory.
+template <int W>
+__device__ __forceinline__ void copy_async(void *dst, const void *src)
+{
+    if (!LPC_READ_OK(src, W)) {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i)
+            static_cast<uint16_t *>(dst)[i] = 0;
+        return;
+    }
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (W == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Waits until at most `pending` of this thread's copy groups are under way.
+__device__ __forceinline__ void copy_wait(int pending)
+{
+    static_assert(kMaxStages == 4, "one case per number of stages");
+    if (pending >= 3)
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (pending == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (pending == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <int DT>
 __device__ __forceinline__ float load_one(const void *base, size_t e)
 {
     float one[1];
-    if constexpr (DT == LPCOLL_F32)
-        widen_pack<DT, 4>(load_pack<DT, 4>(base, e), one);
-    else
-        widen_pack<DT, 2>(load_pack<DT, 2>(base, e), one);
+    widen_pack<DT, kOne<DT>>(load_pack<DT, kOne<DT>>(base, e), one);
     return one[0];
 }
 
-// One row per team.
-template <int DT, int W, int NV>
-__global__ void __launch_bounds__(kNormThreads)
-residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal)
+// What a thread of a team works on: its warp's part of a row is kElems * 32
+// consecutive columns, access c of all lanes side by side.
+template <int DT, int W, int kElems> struct Member {
+    static constexpr int kN = Pack<DT, W>::kN;
+    static constexpr int NV = kElems / kN;
+    int group;         // team of the CTA
+    int first_warp;    // of the team
+    int col0;          // first column of the thread
+    int packs;         // accesses from there to the end of the CTA's part of a row
+    size_t t0, step;   // first row of the team, distance to its next
+    int hidden;
+    char *place;       // this thread's place in the team's ring
+    int row_bytes, stage_bytes;
+
+    __device__ __forceinline__ Member(const Deal &deal, int h, int streams, char *smem)
+    {
+        hidden = h;
+        group = static_cast<int>(threadIdx.x) / deal.threads;
+        const int id = static_cast<int>(threadIdx.x) - group * deal.threads;
+        first_warp = group * (deal.threads >> 5);
+        const int part = deal.cluster > 1 ? static_cast<int>(cluster_rank()) * deal.packs : 0;
+        const int p0 = (id >> 5) * NV * 32 + (id & 31);
+        col0 = (part + p0) * kN;
+        packs = min(deal.packs, (h + kN - 1) / kN - part) - p0;
+        step = static_cast<size_t>(gridDim.x / deal.cluster) * deal.groups;
+        t0 = static_cast<size_t>(blockIdx.x / deal.cluster) * deal.groups + group;
+        row_bytes = (deal.packs * W + 15) & ~15;
+        stage_bytes = row_bytes * streams;
+        place = smem + static_cast<size_t>(group) * stage_bytes * deal.stages + p0 * W;
+    }
+    __device__ __forceinline__ bool has(int c) const { return c * 32 < packs; }
+    __device__ __forceinline__ int col(int c) const { return col0 + c * 32 * kN; }
+    // Element of access c of row t.
+    __device__ __forceinline__ size_t elem(size_t t, int c) const
+    {
+        return (t * hidden + col0) + c * 32 * kN;
+    }
+    __device__ __forceinline__ char *at(int stage, int stream, int c) const
+    {
+        return place + stage * stage_bytes + stream * row_bytes + c * 32 * W;
+    }
+    __device__ __forceinline__ Vec<kN> read(int stage, int stream, int c) const
+    {
+        return unpack<DT, W>(
+            *reinterpret_cast<const typename Pack<DT, W>::Raw *>(at(stage, stream, c)));
+    }
+    // Starts the copy of this thread's part of row t.
+    __device__ __forceinline__ void copy(int stage, int stream, const void *base, size_t t) const
+    {
+        using Raw = typename Pack<DT, W>::Raw;
+        const Raw *src = static_cast<const Raw *>(base);
+        if constexpr (W >= 4) {
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+                if (has(c))
+                    copy_async<W>(at(stage, stream, c),
+                                  src + (t * hidden + col0) / kN + c * 32);
+        } else {  // no asynchronous copy of 2 bytes: all loads before the stores
+            Raw v[NV];
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+                if (has(c))
+                    v[c] = load_pack<DT, W>(base, elem(t, c));
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+                if (has(c))
+                    *reinterpret_cast<Raw *>(at(stage, stream, c)) = v[c];
+        }
+    }
+};
+
+// Streams of a row: x, a full gate if there is one, then the ranks' h.
+template <int DT, int W, int kElems>
+__global__ void __launch_bounds__(kThreadsOne<kElems>, 1)
+residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int streams)
 {
     wait_prior_grid();
-    __shared__ float red[2][kNormWarps][8];
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float red[2][kMaxWarps][8];
     constexpr int kN = Pack<DT, W>::kN;
-    using Raw = typename Pack<DT, W>::Raw;
-    const int group = threadIdx.x / deal.threads;
-    const int member = threadIdx.x - group * deal.threads;
-    const unsigned rank = deal.cluster > 1 ? cluster_rank() : 0;
-    const size_t t =
-        static_cast<size_t>(blockIdx.x / deal.cluster) * deal.groups + group;
-    const size_t row = t * a.hidden;
-    const bool live = t < a.tokens;
-    int col[NV];  // first column of each access, or -1
+    constexpr int NV = kElems / kN;
+    const Member<DT, W, kElems> me(deal, a.hidden, streams, reinterpret_cast<char *>(ring_smem));
+    const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+    const bool full = a.gate_kind == LPCOLL_GATE_FULL;
+    const int h0 = full ? 2 : 1;
+    const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
+    const auto fetch = [&](size_t t, int stage) {
+        if (t < a.tokens) {
+            for (int r = 0; r < a.nranks; ++r)
+                me.copy(stage, h0 + r, a.h[r], t);
+            me.copy(stage, 0, a.x, t);
+            if (full)
+                me.copy(stage, 1, a.gate, t);
+        }
+        copy_commit();
+    };
+    for (int s = 0; s < deal.stages; ++s)
+        fetch(me.t0 + s * me.step, s);
+
+    Vec<kN> wq[NV];  // beta w_post, times a channel's gate
+    typename Pack<DT, W>::Raw wp[NV];
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-        const int p = c * deal.threads + member;
-        const int i = (static_cast<int>(rank) * deal.packs + p) * kN;
-        col[c] = live && p < deal.packs && i < a.hidden ? i : -1;
-    }
-    float v[NV][kN];
-    Raw x[NV];
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-#pragma unroll
-        for (int j = 0; j < kN; ++j)
-            v[c][j] = 0.0f;
-        x[c] = Raw{};
-        if (col[c] >= 0) {
-            x[c] = load_pack<DT, W>(a.x, row + col[c]);
-            widen_pack<DT, W>(load_pack<DT, W>(a.h[0], row + col[c]), v[c]);
+        wq[c] = splat<kN>(a.branch_scale);
+        wp[c] = {};
+        if (me.has(c)) {
+            if (post)
+                wq[c] = mul(wq[c], load_vec_of<DT, W>(a.w_post, me.col(c)));
+            if (a.gate_kind == LPCOLL_GATE_CHANNEL)
+                wq[c] = mul(wq[c], load_vec_of<DT, W>(a.gate, me.col(c)));
+            if (pre)
+                wp[c] = load_pack<DT, W>(a.w_pre, me.col(c));
         }
     }
-#pragma unroll 4
-    for (int r = 1; r < a.nranks; ++r) {
+
+    int stage = 0;
+    for (size_t t = me.t0; t - me.group < a.tokens; t += me.step) {
+        const bool live = t < a.tokens;
+        const float gate_t =
+            a.gate_kind == LPCOLL_GATE_TOKEN && live ? load_one<DT>(a.gate, t) : 1.0f;
+        copy_wait(deal.stages - 1);
+        Vec<kN> v[NV];
+        float r1[1] = {1.0f}, r2[1] = {0.0f};
+        Acc<kN> sq = {};
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-            if (col[c] >= 0) {
-                float p[kN];
-                widen_pack<DT, W>(load_pack<DT, W>(a.h[r], row + col[c]), p);
-#pragma unroll
-                for (int j = 0; j < kN; ++j)
-                    v[c][j] += p[j];
-            }
-        }
-    }
-    float r1[1] = {1.0f};
-    if (a.w_post != nullptr) {
-        r1[0] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < NV; ++c)
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                r1[0] = fmaf(v[c][j], v[c][j], r1[0]);
-        team_sums(r1, red[0], deal);
-        r1[0] = inv_rms(r1[0], a.hidden, a.eps);
-    }
-    const float gate_t =
-        a.gate_kind == LPCOLL_GATE_TOKEN && live ? load_one<DT>(a.gate, t) : 1.0f;
-    float r2[1] = {0.0f};
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-        if (col[c] < 0)
-            continue;
-        if (a.h_sum != nullptr)
-            store_pack<DT, W>(a.h_sum, row + col[c], narrow_pack<DT, W>(v[c]));
-        float w[kN], g[kN], xf[kN];
-        if (a.w_post != nullptr) {
-            widen_pack<DT, W>(load_pack<DT, W>(a.w_post, col[c]), w);
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                v[c][j] = __fmul_rn(__fmul_rn(v[c][j], r1[0]), w[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < kN; ++j)
-            g[j] = gate_t;
-        if (a.gate_kind == LPCOLL_GATE_CHANNEL)
-            widen_pack<DT, W>(load_pack<DT, W>(a.gate, col[c]), g);
-        else if (a.gate_kind == LPCOLL_GATE_FULL)
-            widen_pack<DT, W>(load_pack<DT, W>(a.gate, row + col[c]), g);
-        widen_pack<DT, W>(x[c], xf);
-#pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            v[c][j] = fmaf(__fmul_rn(a.branch_scale, g[j]), v[c][j],
-                           __fmul_rn(a.res_scale, xf[j]));
-            r2[0] = fmaf(v[c][j], v[c][j], r2[0]);
-        }
-        store_pack<DT, W>(a.x_out, row + col[c], narrow_pack<DT, W>(v[c]));
-    }
-    if (a.w_pre != nullptr) {
-        team_sums(r2, red[1], deal);
-        r2[0] = inv_rms(r2[0], a.hidden, a.eps);
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            if (col[c] < 0)
+            v[c] = splat<kN>(0.0f);
+            if (!live || !me.has(c))
                 continue;
-            float w[kN];
-            widen_pack<DT, W>(load_pack<DT, W>(a.w_pre, col[c]), w);
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                w[j] = __fmul_rn(__fmul_rn(v[c][j], r2[0]), w[j]);
-            store_pack<DT, W>(a.n_out, row + col[c], narrow_pack<DT, W>(w));
+            v[c] = me.read(stage, h0, c);
+            for (int r = 1; r < a.nranks; ++r)
+                v[c] = add(v[c], me.read(stage, h0 + r, c));
+            if (a.h_sum != nullptr)
+                store_vec_of<DT, W>(a.h_sum, me.elem(t, c), v[c]);
+            add_products(sq, v[c], v[c]);
         }
+        if (post) {
+            r1[0] = fold(sq);
+            team_sums(r1, red[0], deal, me.first_warp);
+            r1[0] = inv_rms(r1[0], per_hidden, a.eps);
+        }
+        const float f = r1[0] * gate_t;
+        sq = {};
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            if (!live || !me.has(c))
+                continue;
+            Vec<kN> u = mul(mul(f, wq[c]), v[c]);
+            if (full)
+                u = mul(u, me.read(stage, 1, c));
+            v[c] = fma(a.res_scale, me.read(stage, 0, c), u);
+            add_products(sq, v[c], v[c]);
+            store_vec_of<DT, W>(a.x_out, me.elem(t, c), v[c]);
+        }
+        fetch(t + deal.stages * me.step, stage);
+        if (pre) {
+            r2[0] = fold(sq);
+            team_sums(r2, red[1], deal, me.first_warp);
+            r2[0] = inv_rms(r2[0], per_hidden, a.eps);
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+                if (live && me.has(c))
+                    store_vec_of<DT, W>(a.n_out, me.elem(t, c),
+                                        mul(mul(r2[0], unpack<DT, W>(wp[c])), v[c]));
+        }
+        if (!(post && pre))
+            team_barrier(deal);  // red is used again only after a barrier
+        stage = stage + 1 == deal.stages ? 0 : stage + 1;
     }
     if (deal.cluster > 1)
         cluster_barrier();  // no CTA leaves while another reads its sums
@@ -241,292 +489,172 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal)
 // a token's own gate) the six sums h^2, x'^2, q x', P dx', P q, P x' of one
 // pass over the row give every factor of the second:
 //   sum(P D) = sum(P dx') + r2 (sum(P q) - c2 sum(P x')).
-// A team goes through its tokens one after the other, its next rows on their
-// way into shared memory (cp.async) meanwhile: each thread copies and reads its
-// own columns only, so that no barrier guards a stage. It keeps the sums over
-// tokens of its columns in registers, S = sum beta r1 h D (times a gate that
-// differs by token) and dw_pre = sum dn x' r2, and the CTA leaves them in the
-// workspace, [2][CTAs][hidden]; a second launch adds those up in order:
-// dw_post = g S and dgate = w_post S for a gate per channel.
+// A thread keeps the sums over tokens of its columns in registers, S = sum
+// beta r1 h D (times a gate that differs by token) and dw_pre = sum dn x' r2,
+// and the CTA leaves them in the workspace, [2][CTAs][hidden]; a second launch
+// adds those up in order: dw_post = g S, and dgate = w_post S for a gate per
+// channel.
 // ---------------------------------------------------------------------------
 
 // Row streams of a stage.
 enum Stream { kH = 0, kDx = 1, kX = 2, kDn = 3, kGate = 4 };
 
-template <int W>
-__device__ __forceinline__ void copy_async(void *dst, const void *src)
-{
-    if (!LPC_READ_OK(src, W)) {
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i)
-            static_cast<uint16_t *>(dst)[i] = 0;
-        return;
-    }
-    if constexpr (W >= 4) {
-        const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-        if constexpr (W == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-        else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
-    } else {
-        *static_cast<uint16_t *>(dst) = *static_cast<const uint16_t *>(src);
-    }
-}
-
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-// Waits until at most `pending` of this thread's copy groups are under way.
-__device__ __forceinline__ void copy_wait(int pending)
-{
-    if (pending >= 2)
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (pending == 1)
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-
-template <int DT, int W, int NV>
-__global__ void __launch_bounds__(kNormThreads, NV * Pack<DT, W>::kN <= 8 ? 2 : 1)
-residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal deal, int stages,
-                              int streams)
+template <int DT, int W, int kElems>
+__global__ void __launch_bounds__(kThreadsOne<kElems>, 1)
+residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal deal, int streams)
 {
     wait_prior_grid();
-    extern __shared__ uint4 stage_smem[];
-    __shared__ float red[2][kNormWarps][8];
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float red[2][kMaxWarps][8];
     constexpr int kN = Pack<DT, W>::kN;
-    constexpr size_t kEs = sizeof(typename Pack<DT, W>::Raw) / kN;
-    using Raw = typename Pack<DT, W>::Raw;
-    const int group = threadIdx.x / deal.threads;
-    const int member = threadIdx.x - group * deal.threads;
-    const unsigned rank = deal.cluster > 1 ? cluster_rank() : 0;
+    constexpr int NV = kElems / kN;
+    const Member<DT, W, kElems> me(deal, a.hidden, streams, reinterpret_cast<char *>(ring_smem));
     const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr, given = a.dx_out != nullptr;
     const bool full = a.gate_kind == LPCOLL_GATE_FULL;
     const int H = a.hidden;
-    // shared memory: [stage][group][stream][packs], a stream's part padded to 16 bytes
-    const int stream_bytes = (deal.packs * W + 15) & ~15;
-    const int group_bytes = stream_bytes * streams;
-    char *const mine = reinterpret_cast<char *>(stage_smem) + group * group_bytes;
-    const int stage_bytes = group_bytes * deal.groups;
-
-    int col[NV];          // first column of each access, or -1
-    float wq[NV][kN];     // w_post times a channel's gate
-    Raw wp[NV];           // w_pre
-    float S[NV][kN], s_pre[NV][kN];
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-        const int p = c * deal.threads + member;
-        const int i = (static_cast<int>(rank) * deal.packs + p) * kN;
-        col[c] = p < deal.packs && i < H ? i : -1;
-        wp[c] = Raw{};
-#pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            S[c][j] = s_pre[c][j] = 0.0f;
-            wq[c][j] = 1.0f;
-        }
-        if (col[c] >= 0) {
-            if (post)
-                widen_pack<DT, W>(load_pack<DT, W>(a.w_post, i), wq[c]);
-            if (pre)
-                wp[c] = load_pack<DT, W>(a.w_pre, i);
-            if (a.gate_kind == LPCOLL_GATE_CHANNEL) {
-                float g[kN];
-                widen_pack<DT, W>(load_pack<DT, W>(a.gate, i), g);
-#pragma unroll
-                for (int j = 0; j < kN; ++j)
-                    wq[c][j] = __fmul_rn(wq[c][j], g[j]);
-            }
-        }
-    }
-
-    const size_t step = static_cast<size_t>(gridDim.x / deal.cluster) * deal.groups;
-    const size_t t0 = static_cast<size_t>(blockIdx.x / deal.cluster) * deal.groups + group;
+    const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(H));
     const auto fetch = [&](size_t t, int stage) {
         if (t < a.tokens) {
-            const size_t row = t * H;
-            char *dst = mine + stage * stage_bytes;
-#pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                if (col[c] < 0)
-                    continue;
-                char *d = dst + (c * deal.threads + member) * W;
-                const size_t off = (row + col[c]) * kEs;
-                copy_async<W>(d, static_cast<const char *>(a.h[0]) + off);
-                if (given)
-                    copy_async<W>(d + kDx * stream_bytes, static_cast<const char *>(a.dx_out) + off);
-                if (pre) {
-                    copy_async<W>(d + kX * stream_bytes, static_cast<const char *>(a.x) + off);
-                    copy_async<W>(d + kDn * stream_bytes, static_cast<const char *>(a.dn_out) + off);
-                }
-                if (full)
-                    copy_async<W>(d + kGate * stream_bytes, static_cast<const char *>(a.gate) + off);
+            me.copy(stage, kH, a.h[0], t);
+            if (given)
+                me.copy(stage, kDx, a.dx_out, t);
+            if (pre) {
+                me.copy(stage, kX, a.x, t);
+                me.copy(stage, kDn, a.dn_out, t);
             }
+            if (full)
+                me.copy(stage, kGate, a.gate, t);
         }
         copy_commit();
     };
-    for (int s = 0; s < stages; ++s)
-        fetch(t0 + s * step, s);
+    for (int s = 0; s < deal.stages; ++s)
+        fetch(me.t0 + s * me.step, s);
+
+    Vec<kN> wq[NV];                    // w_post times a channel's gate
+    typename Pack<DT, W>::Raw wp[NV];  // w_pre
+    Vec<kN> S[NV], s_pre[NV];
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        S[c] = s_pre[c] = splat<kN>(0.0f);
+        wq[c] = splat<kN>(1.0f);
+        wp[c] = {};
+        if (me.has(c)) {
+            if (post)
+                wq[c] = load_vec_of<DT, W>(a.w_post, me.col(c));
+            if (a.gate_kind == LPCOLL_GATE_CHANNEL)
+                wq[c] = mul(wq[c], load_vec_of<DT, W>(a.gate, me.col(c)));
+            if (pre)
+                wp[c] = load_pack<DT, W>(a.w_pre, me.col(c));
+        }
+    }
 
     int stage = 0, turn = 0;
-    // the same number of turns for all teams of the CTA and of the cluster
-    for (size_t t = t0; t - group < a.tokens; t += step, turn ^= 1) {
-        copy_wait(stages - 1);
+    for (size_t t = me.t0; t - me.group < a.tokens; t += me.step, turn ^= 1) {
         const bool live = t < a.tokens;
-        const char *src = mine + stage * stage_bytes;
-        const auto read = [&](int stream, int c, float (&out)[kN]) {
-            widen_pack<DT, W>(*reinterpret_cast<const Raw *>(
-                                  src + stream * stream_bytes + (c * deal.threads + member) * W),
-                              out);
-        };
-        float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            if (!live || col[c] < 0)
-                continue;
-            float h[kN], p[kN];
-            read(kH, c, h);
-#pragma unroll
-            for (int j = 0; j < kN; ++j) {
-                p[j] = __fmul_rn(wq[c][j], h[j]);
-                s[0] = fmaf(h[j], h[j], s[0]);
-            }
-            if (full) {
-                float g[kN];
-                read(kGate, c, g);
-#pragma unroll
-                for (int j = 0; j < kN; ++j)
-                    p[j] = __fmul_rn(p[j], g[j]);
-            }
-            if (given) {
-                float d[kN];
-                read(kDx, c, d);
-#pragma unroll
-                for (int j = 0; j < kN; ++j)
-                    s[3] = fmaf(p[j], d[j], s[3]);
-            }
-            if (pre) {
-                float x[kN], q[kN], w[kN];
-                read(kX, c, x);
-                read(kDn, c, q);
-                widen_pack<DT, W>(wp[c], w);
-#pragma unroll
-                for (int j = 0; j < kN; ++j) {
-                    q[j] = __fmul_rn(q[j], w[j]);
-                    s[1] = fmaf(x[j], x[j], s[1]);
-                    s[2] = fmaf(q[j], x[j], s[2]);
-                    s[4] = fmaf(p[j], q[j], s[4]);
-                    s[5] = fmaf(p[j], x[j], s[5]);
-                }
-            }
-        }
-        team_sums(s, red[turn], deal);
         const float gate_t =
             a.gate_kind == LPCOLL_GATE_TOKEN && live ? load_one<DT>(a.gate, t) : 1.0f;
-        const float r1 = post ? inv_rms(s[0], H, a.eps) : 1.0f;
-        const float r2 = pre ? inv_rms(s[1], H, a.eps) : 0.0f;
-        const float c2 = pre ? __fdiv_rn(r2 * r2 * s[2], static_cast<float>(H)) : 0.0f;
+        copy_wait(deal.stages - 1);
+        float s[6];
+        {
+            Acc<kN> v[6] = {};
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                if (!live || !me.has(c))
+                    continue;
+                const Vec<kN> h = me.read(stage, kH, c);
+                Vec<kN> p = mul(wq[c], h);
+                add_products(v[0], h, h);
+                if (full)
+                    p = mul(p, me.read(stage, kGate, c));
+                if (given)
+                    add_products(v[3], p, me.read(stage, kDx, c));
+                if (pre) {
+                    const Vec<kN> x = me.read(stage, kX, c);
+                    const Vec<kN> q = mul(me.read(stage, kDn, c), unpack<DT, W>(wp[c]));
+                    add_products(v[1], x, x);
+                    add_products(v[2], q, x);
+                    add_products(v[4], p, q);
+                    add_products(v[5], p, x);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+                s[i] = fold(v[i]);
+        }
+        team_sums(s, red[turn], deal, me.first_warp);
+        const float r1 = post ? inv_rms(s[0], per_hidden, a.eps) : 1.0f;
+        const float r2 = pre ? inv_rms(s[1], per_hidden, a.eps) : 0.0f;
+        const float c2 = pre ? r2 * r2 * s[2] * per_hidden : 0.0f;
         const float pd = fmaf(r2, fmaf(-c2, s[5], s[4]), s[3]);
         const float bt = a.branch_scale * gate_t;
         // dh = f1 wq g D - f2 h;  S += f1 g h D
         const float f1 = r1 * bt;
-        const float f2 = post ? r1 * __fdiv_rn(r1 * r1 * bt * pd, static_cast<float>(H)) : 0.0f;
-        if (a.gate_kind == LPCOLL_GATE_TOKEN && a.dgate != nullptr && live && member == 0 &&
-            rank == 0)
+        const float f2 = post ? r1 * (r1 * r1 * bt * pd * per_hidden) : 0.0f;
+        if (a.gate_kind == LPCOLL_GATE_TOKEN && a.dgate != nullptr && live && me.col0 == 0)
             store_f32(static_cast<float *>(a.dgate) + t, a.branch_scale * r1 * pd);
-        const size_t row = t * H;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-            if (!live || col[c] < 0)
+            if (!live || !me.has(c))
                 continue;
-            float d[kN], o[kN], h[kN];
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                d[j] = 0.0f;
+            Vec<kN> d = splat<kN>(0.0f);
             if (given)
-                read(kDx, c, d);
+                d = me.read(stage, kDx, c);
             if (pre) {
-                float x[kN], q[kN], w[kN];
-                read(kX, c, x);
-                read(kDn, c, q);
-                widen_pack<DT, W>(wp[c], w);
-#pragma unroll
-                for (int j = 0; j < kN; ++j) {
-                    s_pre[c][j] = fmaf(__fmul_rn(q[j], r2), x[j], s_pre[c][j]);
-                    d[j] = fmaf(r2, fmaf(-c2, x[j], __fmul_rn(q[j], w[j])), d[j]);
-                }
+                const Vec<kN> x = me.read(stage, kX, c), dn = me.read(stage, kDn, c);
+                const Vec<kN> q = mul(dn, unpack<DT, W>(wp[c]));
+                s_pre[c] = fma(mul(r2, dn), x, s_pre[c]);
+                d = fma(r2, fma(-c2, x, q), d);
             }
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                o[j] = __fmul_rn(a.res_scale, d[j]);
-            store_pack<DT, W>(a.dx, row + col[c], narrow_pack<DT, W>(o));
-            read(kH, c, h);
+            store_vec_of<DT, W>(a.dx, me.elem(t, c), mul(a.res_scale, d));
+            const Vec<kN> h = me.read(stage, kH, c);
             if (full) {
-                float g[kN];
-                read(kGate, c, g);
-                if (a.dgate != nullptr) {
-#pragma unroll
-                    for (int j = 0; j < kN; ++j)
-                        o[j] = __fmul_rn(__fmul_rn(__fmul_rn(f1, wq[c][j]), h[j]), d[j]);
-                    store_pack<DT, W>(a.dgate, row + col[c], narrow_pack<DT, W>(o));
-                }
-#pragma unroll
-                for (int j = 0; j < kN; ++j)
-                    d[j] = __fmul_rn(d[j], g[j]);
+                if (a.dgate != nullptr)
+                    store_vec_of<DT, W>(a.dgate, me.elem(t, c),
+                                        mul(mul(mul(f1, wq[c]), h), d));
+                d = mul(d, me.read(stage, kGate, c));
             }
-#pragma unroll
-            for (int j = 0; j < kN; ++j) {
-                S[c][j] = fmaf(__fmul_rn(f1, h[j]), d[j], S[c][j]);
-                o[j] = fmaf(__fmul_rn(f1, wq[c][j]), d[j], -__fmul_rn(f2, h[j]));
-            }
-            store_pack<DT, W>(a.dh, row + col[c], narrow_pack<DT, W>(o));
+            const Vec<kN> e = mul(f1, d);
+            S[c] = fma(h, e, S[c]);
+            store_vec_of<DT, W>(a.dh, me.elem(t, c), fma(wq[c], e, mul(-f2, h)));
         }
-        fetch(t + stages * step, stage);
-        stage = stage + 1 == stages ? 0 : stage + 1;
+        fetch(t + deal.stages * me.step, stage);
+        stage = stage + 1 == deal.stages ? 0 : stage + 1;
     }
     copy_wait(0);
     if (deal.cluster > 1)
         cluster_barrier();  // no CTA leaves while another reads its sums
 
     // The CTA's sums over its tokens: the groups add theirs in order in shared
-    // memory (the stages are free), then the CTA writes one row per gradient.
+    // memory (the rows are done with), then the CTA writes one row per gradient.
     if (a.partial == nullptr)
         return;
     const size_t part = static_cast<size_t>(gridDim.x / deal.cluster) * H;
     float *const out = a.partial + static_cast<size_t>(blockIdx.x / deal.cluster) * H;
-    float *const sums = reinterpret_cast<float *>(stage_smem);
-    for (int g = 0; g + 1 < deal.groups; ++g) {
+    float *const sums = reinterpret_cast<float *>(ring_smem);
+    for (int g = 0; g < deal.groups; ++g) {
         __syncthreads();
-        if (group == g) {
-#pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                if (col[c] < 0)
-                    continue;
-#pragma unroll
-                for (int j = 0; j < kN; ++j) {
-                    float *p = sums + 2 * (col[c] + j);
-                    p[0] = g > 0 ? p[0] + s_pre[c][j] : s_pre[c][j];
-                    p[1] = g > 0 ? p[1] + S[c][j] : S[c][j];
-                }
-            }
-        }
-    }
-    __syncthreads();
-    if (group != deal.groups - 1)
-        return;
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-        if (col[c] < 0)
+        if (me.group != g)
             continue;
 #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            const int i = col[c] + j;
-            float v0 = s_pre[c][j], v1 = S[c][j];
-            if (deal.groups > 1) {
-                v0 = sums[2 * i] + v0;
-                v1 = sums[2 * i + 1] + v1;
+        for (int c = 0; c < NV; ++c) {
+            if (!me.has(c))
+                continue;
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                const int i = me.col(c) + j;
+                float v0 = s_pre[c].v[j], v1 = S[c].v[j];
+                if (g > 0) {
+                    v0 = sums[2 * i] + v0;
+                    v1 = sums[2 * i + 1] + v1;
+                }
+                if (g + 1 < deal.groups) {
+                    sums[2 * i] = v0;
+                    sums[2 * i + 1] = v1;
+                } else {
+                    store_f32(out + i, v0);
+                    store_f32(out + part + i, v1);
+                }
             }
-            store_f32(out + i, v0);
-            store_f32(out + part + i, v1);
         }
     }
 }
@@ -578,85 +706,94 @@ norm_column_sums_kernel(const __grid_constant__ NormArgs a, int parts, int colum
 
 int round_up(int n, int to) { return (n + to - 1) / to * to; }
 
-// Accesses per thread of the backward kernel: 8 elements where a CTA then
-// holds the row, else 16 (and up to 4 CTAs of a cluster for the longest rows).
-template <int DT, int W> constexpr int kFew = 8 / Pack<DT, W>::kN;
-template <int DT, int W> constexpr int kMany = 16 / Pack<DT, W>::kN;
-
-// Team of `nv` accesses per thread for a row, over `cluster` CTAs.
-Deal deal_row(int hidden, int kn, int nv, int cluster, int most_threads)
-{
-    Deal d;
-    d.cluster = cluster;
-    d.packs = ((hidden + kn - 1) / kn + cluster - 1) / cluster;
-    d.threads = round_up((d.packs + nv - 1) / nv, 32);
-    d.groups = cluster > 1 || d.threads * 2 > most_threads ? 1 : most_threads / d.threads;
-    return d;
-}
-
-struct BackwardPlan {
+struct Plan {
     Deal deal;
-    bool few;
-    int parts;  // CTAs, or clusters of them
+    int elems;    // columns of a thread
+    int ctas;     // CTAs, or clusters of them, that share the rows
+    size_t smem;  // dynamic shared memory of a CTA
 };
 
-BackwardPlan backward_plan(size_t tokens, int hidden, int dtype)
+// Shared memory of the rings of a CTA, for one or two CTAs per SM.
+constexpr size_t kSmemOne = 224 * 1024, kSmemTwo = 110 * 1024;
+
+// A row is one CTA's, or, from 8193 columns on or where there are few tokens,
+// a cluster's. 16 columns a thread halve what a row costs besides its columns
+// (sums, addresses): 8192 columns in BF16 took 147 instead of 239 us for the
+// gradients of 8192 tokens, 193 instead of 256 us for 16384 tokens forward. 8
+// columns are faster where latency counts (32 tokens: 5.6 against 6.1 us) and
+// for the shortest rows (128 columns: 7.2 against 9.0 us).
+Plan make_plan(size_t tokens, int hidden, int dtype, int streams, size_t sums_smem)
 {
     const int width = row_width(hidden, dtype);
     const int kn = width / static_cast<int>(dtype_bytes(dtype));
-    BackwardPlan p;
-    p.few = hidden <= 8 * kNormThreads;
-    const int per_cta = 16 * kNormThreads;
-    const int cluster = hidden > per_cta ? 2 : 1;
-    p.deal = deal_row(hidden, kn, (p.few ? 8 : 16) / kn, cluster, kNormThreads);
-    const size_t steps = (tokens + p.deal.groups - 1) / p.deal.groups;
-    const size_t most = static_cast<size_t>(kSms) * (p.few ? 2 : 1) / cluster;
-    p.parts = static_cast<int>(steps < most ? steps : most);
+    // few tokens: a row over up to 8 CTAs, while there are SMs left and a CTA
+    // keeps two warps
+    constexpr int kRow = 8192;  // columns of the largest CTA
+    int cluster = hidden > kRow ? 2 : 1;
+    while (cluster < 8 && tokens * cluster * 2 <= kSms && hidden >= 512 * cluster * 2)
+        cluster *= 2;
+    // many ranks: until a row of all streams fits the shared memory
+    while (cluster < 8 && (static_cast<size_t>(hidden) * width / kn / cluster + 16 * kn) * streams >
+                              kSmemOne)
+        cluster *= 2;
+    Plan p;
+    p.elems = hidden <= 256 || tokens <= kSms ? 8 : 16;
+    Deal &d = p.deal;
+    d.cluster = cluster;
+    d.packs = ((hidden + kn - 1) / kn + cluster - 1) / cluster;
+    d.threads = round_up((d.packs + p.elems / kn - 1) / (p.elems / kn), 32);
+    const int share = p.elems == 8 ? kThreadsTwo<8> : kThreadsTwo<16>;
+    d.groups = cluster > 1 || d.threads * 2 > share ? 1 : share / d.threads;
+    const bool two = d.threads * d.groups <= share;
+    const size_t steps = (tokens + d.groups - 1) / d.groups;
+    const size_t most = static_cast<size_t>(kSms) * (two ? 2 : 1) / cluster;
+    p.ctas = static_cast<int>(steps < most ? steps : most);
+    const size_t stage = static_cast<size_t>(round_up(d.packs * width, 16)) * streams * d.groups;
+    const size_t fit = (two ? kSmemTwo : kSmemOne) / stage;
+    d.stages = static_cast<int>(fit > kMaxStages ? kMaxStages : (fit < 1 ? 1 : fit));
+    const size_t sums = d.groups > 1 ? sums_smem : 0;
+    p.smem = d.stages * stage > sums ? d.stages * stage : sums;
     return p;
 }
 
-template <int DT, int W, int NV>
-cudaError_t backward_nv(const NormArgs &a, const BackwardPlan &p, cudaStream_t st)
+template <class Kernel>
+cudaError_t launch_plan(Kernel kernel, const NormArgs &a, const Plan &p, int streams,
+                        cudaStream_t st)
 {
-    // shared memory of a CTA beside its static part, for one or two CTAs per SM
-    constexpr size_t kLimit = 225 * 1024, kHalf = 112 * 1024;
-    const int streams = a.gate_kind == LPCOLL_GATE_FULL ? 5 : 4;
-    const size_t stage = static_cast<size_t>(round_up(p.deal.packs * W, 16)) * streams * p.deal.groups;
-    // the sums that the groups of a CTA add up at the end
-    const size_t sums = p.deal.groups > 1 ? static_cast<size_t>(a.hidden) * 2 * sizeof(float) : 0;
-    const size_t room = p.few ? kHalf : kLimit;
-    int stages = static_cast<int>(room / stage);
-    stages = stages > 3 ? 3 : (stages < 1 ? 1 : stages);
-    const size_t smem = stages * stage > sums ? stages * stage : sums;
-    auto kernel = residual_norm_backward_kernel<DT, W, NV>;
     // always the same value: calls of several threads must not undo each other's
     const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLimit));
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemOne));
     if (e != cudaSuccess)
         return e;
-    return launch_kernel_cluster(kernel, static_cast<size_t>(p.parts) * p.deal.cluster,
-                                 p.deal.threads * p.deal.groups, p.deal.cluster, smem, st, a,
-                                 p.deal, stages, streams);
+    return launch_kernel_cluster(kernel, static_cast<size_t>(p.ctas) * p.deal.cluster,
+                                 p.deal.threads * p.deal.groups, p.deal.cluster, p.smem, st, a,
+                                 p.deal, streams);
+}
+
+Plan backward_plan(size_t tokens, int hidden, int dtype, int gate_kind)
+{
+    const int streams = gate_kind == LPCOLL_GATE_FULL ? 5 : 4;
+    // the groups of a CTA add up their sums in shared memory
+    return make_plan(tokens, hidden, dtype, streams,
+                     static_cast<size_t>(hidden) * 2 * sizeof(float));
 }
 
 template <int DT, int W>
-cudaError_t backward_dt(const NormArgs &a, const BackwardPlan &p, cudaStream_t st)
+cudaError_t backward_dt(const NormArgs &a, const Plan &p, cudaStream_t st)
 {
-    return p.few ? backward_nv<DT, W, kFew<DT, W>>(a, p, st)
-                 : backward_nv<DT, W, kMany<DT, W>>(a, p, st);
+    return launch_plan(p.elems == 8 ? residual_norm_backward_kernel<DT, W, 8>
+                                    : residual_norm_backward_kernel<DT, W, 16>,
+                       a, p, a.gate_kind == LPCOLL_GATE_FULL ? 5 : 4, st);
 }
 
 template <int DT, int W>
 cudaError_t forward_dt(const NormArgs &a, cudaStream_t st)
 {
-    constexpr int kN = Pack<DT, W>::kN;
-    const bool few = a.hidden <= 8 * kNormThreads;
-    const int cluster = a.hidden > 16 * kNormThreads ? 2 : 1;
-    const Deal d = deal_row(a.hidden, kN, few ? kFew<DT, W> : kMany<DT, W>, cluster, 256);
-    const size_t grid = (a.tokens + d.groups - 1) / d.groups * cluster;
-    return launch_kernel_cluster(few ? residual_norm_kernel<DT, W, kFew<DT, W>>
-                                     : residual_norm_kernel<DT, W, kMany<DT, W>>,
-                                 grid, d.threads * d.groups, cluster, 0, st, a, d);
+    const int streams = a.nranks + 1 + (a.gate_kind == LPCOLL_GATE_FULL ? 1 : 0);
+    const Plan p = make_plan(a.tokens, a.hidden, a.dtype, streams, 0);
+    return launch_plan(p.elems == 8 ? residual_norm_kernel<DT, W, 8>
+                                    : residual_norm_kernel<DT, W, 16>,
+                       a, p, streams, st);
 }
 
 }  // namespace
@@ -665,7 +802,7 @@ int norm_backward_parts(size_t tokens, size_t hidden, int dtype)
 {
     return hidden == 0 || tokens == 0
                ? 0
-               : backward_plan(tokens, static_cast<int>(hidden), dtype).parts;
+               : backward_plan(tokens, static_cast<int>(hidden), dtype, LPCOLL_GATE_NONE).ctas;
 }
 
 cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t st)
@@ -682,8 +819,8 @@ cudaError_t launch_residual_norm_backward(const NormArgs &args, cudaStream_t st)
         a.partial = nullptr;
     int parts = 0;
     if (a.tokens > 0) {
-        const BackwardPlan p = backward_plan(a.tokens, a.hidden, a.dtype);
-        parts = p.parts;
+        const Plan p = backward_plan(a.tokens, a.hidden, a.dtype, a.gate_kind);
+        parts = p.ctas;
         const cudaError_t e =
             LPC_BY_ROW(backward_dt, a.dtype, static_cast<size_t>(a.hidden), a, p, st);
         if (e != cudaSuccess)

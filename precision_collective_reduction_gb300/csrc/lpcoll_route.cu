@@ -2,10 +2,15 @@
 // the K largest of each token, and the gradient) and the stable counting sort
 // of the (token, choice) slots by expert.
 //
-// Router: one warp per token. A lane holds the logits of experts lane,
-// lane + 32, ... as order-preserving 32-bit keys; a choice is the largest key
-// of the warp and, among the experts that hold it, the lowest index: two
-// warp-wide integer reductions. Every sum is FP32 in a fixed order.
+// Router: one warp per token, lane l holding the logits of experts l, l + 32,
+// ... as order-preserving integers. Instructions bound it, not the logits'
+// traffic, so a choice is one warp-wide integer maximum: 22 bits of the logit
+// and 10 of the expert's index make one unsigned number whose order is that
+// of the logits, lower index first. For BF16 the 22 bits hold the whole logit;
+// for FP32 a token in which two neighbours of the choice agree in them, and
+// not in the rest, is chosen again with both parts apart. A lane sorts its
+// numbers once, and the winner of a choice moves up its list. Every sum is
+// FP32 in a fixed order.
 #include "lpcoll_layers.cuh"
 
 namespace lpc {
@@ -48,24 +53,62 @@ __device__ __forceinline__ void load_logits(const void *logits, size_t t, int ex
     }
 }
 
-template <int DT, int PER>
-__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a)
+// Descending order of v[LO .. LO + N) (Batcher's odd-even merge sort); merge_down
+// does it for the elements R apart, whose halves are in order.
+template <int P, int Q, int PER> __device__ __forceinline__ void order(uint32_t (&v)[PER])
 {
-    wait_prior_grid();
-    const int lane = threadIdx.x & 31;
-    const size_t t = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    if (t >= a.tokens)
-        return;
+    const uint32_t hi = max(v[P], v[Q]);
+    v[Q] = min(v[P], v[Q]);
+    v[P] = hi;
+}
+
+template <int LO, int END, int STEP, int R, int PER>
+__device__ __forceinline__ void order_each(uint32_t (&v)[PER])
+{
+    if constexpr (LO + R < END) {
+        order<LO, LO + R>(v);
+        order_each<LO + STEP, END, STEP, R>(v);
+    }
+}
+
+template <int LO, int N, int R, int PER>
+__device__ __forceinline__ void merge_down(uint32_t (&v)[PER])
+{
+    if constexpr (2 * R < N) {
+        merge_down<LO, N, 2 * R>(v);
+        merge_down<LO + R, N, 2 * R>(v);
+        order_each<LO + R, LO + N, 2 * R, R>(v);
+    } else {
+        order<LO, LO + R>(v);
+    }
+}
+
+template <int LO, int N, int PER> __device__ __forceinline__ void sort_down(uint32_t (&v)[PER])
+{
+    if constexpr (N > 1) {
+        sort_down<LO, N / 2>(v);
+        sort_down<LO + N / 2, N / 2>(v);
+        merge_down<LO, N, 1>(v);
+    }
+}
+
+constexpr uint32_t kIndexBits = 0x3FFu;
+static_assert(LPCOLL_MAX_EXPERTS == kIndexBits + 1, "an expert's index has 10 bits");
+
+// The topk choices by logit and index apart: expert in lane j, -1 from the
+// first lane on that finds none left.
+template <int DT, int PER>
+__device__ __noinline__ int choose_apart(const void *logits, size_t t, int experts, int topk,
+                                         int lane)
+{
     float x[PER];
     uint32_t key[PER];
-    load_logits<DT, PER>(a.logits, t, a.experts, lane, x);
+    load_logits<DT, PER>(logits, t, experts, lane, x);
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         key[i] = logit_key(x[i]);
-
     int my_id = -1;
-    uint32_t my_key = 0, top = 0;
-    for (int j = 0; j < a.topk; ++j) {
+    for (int j = 0; j < topk; ++j) {
         uint32_t best = 0;
         int at = 0;
 #pragma unroll
@@ -77,24 +120,75 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a)
         const uint32_t most = __reduce_max_sync(kAll, best);
         if (most <= kKeyNone)
             break;
-        const int mine = best == most ? at * 32 + lane : INT32_MAX;
-        const int id = __reduce_min_sync(kAll, mine);
-        if (j == 0)
-            top = most;
-        if (lane == j) {
+        const int id = __reduce_min_sync(kAll, best == most ? at * 32 + lane : INT32_MAX);
+        if (lane == j)
             my_id = id;
-            my_key = most;
-        }
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (i * 32 + lane == id)
                 key[i] = 0;
     }
+    return my_id;
+}
+
+template <int DT, int PER>
+__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a)
+{
+    wait_prior_grid();
+    const int lane = threadIdx.x & 31;
+    const size_t t = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+    if (t >= a.tokens)
+        return;
+    float x[PER];
+    load_logits<DT, PER>(a.logits, t, a.experts, lane, x);
+
+    uint32_t list[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const uint32_t key = logit_key(x[i]);
+        list[i] = key > kKeyNone ? (key & ~kIndexBits) | (kIndexBits - (i * 32 + lane)) : 0u;
+    }
+    sort_down<0, PER>(list);
+    uint32_t mine = 0, most = 0;
+    for (int j = 0; j < a.topk; ++j) {
+        most = __reduce_max_sync(kAll, list[0]);
+        if (most == 0)
+            break;
+        if (lane == j)
+            mine = most;
+        const bool won = list[0] == most;
+#pragma unroll
+        for (int i = 0; i + 1 < PER; ++i)
+            list[i] = won ? list[i + 1] : list[i];
+        list[PER - 1] = won ? 0u : list[PER - 1];
+    }
+    int my_id = mine != 0 ? static_cast<int>(kIndexBits - (mine & kIndexBits)) : -1;
+    const auto logit_of = [&](int id) {
+        float one[1] = {-INFINITY};
+        if (id >= 0)
+            widen_pack<DT, kOne<DT>>(load_pack<DT, kOne<DT>>(a.logits, t * a.experts + id), one);
+        return one[0];
+    };
+    float z = logit_of(my_id);
+    if constexpr (DT == LPCOLL_F32) {
+        // neighbours in the order, the last choice and the next one among them
+        const uint32_t next = __reduce_max_sync(kAll, list[0]);
+        const uint32_t before = __shfl_up_sync(kAll, mine, 1);
+        const float z_before = __shfl_up_sync(kAll, z, 1);
+        const bool unsure =
+            (lane > 0 && mine != 0 && (mine ^ before) <= kIndexBits &&
+             logit_key(z) != logit_key(z_before)) ||
+            (lane == a.topk - 1 && mine != 0 && next != 0 && (mine ^ next) <= kIndexBits);
+        if (__any_sync(kAll, unsure)) {
+            my_id = choose_apart<DT, PER>(a.logits, t, a.experts, a.topk, lane);
+            z = logit_of(my_id);
+        }
+    }
 
     float w = 0.0f;
-    if (top > kKeyNone) {  // the same in all lanes
-        const float m = key_logit(top);
-        w = my_id >= 0 ? expf(key_logit(my_key) - m) : 0.0f;
+    if (__any_sync(kAll, my_id >= 0)) {
+        const float m = __shfl_sync(kAll, z, 0);
+        w = my_id >= 0 ? expf(z - m) : 0.0f;
         float sum = w;
         if (!a.renormalize) {
             sum = 0.0f;
@@ -111,15 +205,24 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a)
 }
 
 // dl_e = [e chosen as j] w_j dw_j - p_e sum_j w_j dw_j, with p = w at the
-// chosen and 0 elsewhere when the weights were renormalised.
+// chosen and 0 elsewhere when the weights were renormalised. The chosen
+// experts' terms go through a row in shared memory.
 template <int DT, int PER>
 __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteArgs a)
 {
     wait_prior_grid();
+    __shared__ float chosen_all[kWarpsPerCta][PER * 32];
+    float *const chosen = chosen_all[threadIdx.x >> 5];
     const int lane = threadIdx.x & 31;
     const size_t t = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
     if (t >= a.tokens)
         return;
+    float x[PER];
+    if (!a.renormalize)
+        load_logits<DT, PER>(a.logits, t, a.experts, lane, x);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        chosen[i * 32 + lane] = 0.0f;
     int id = -1;
     float w = 0.0f, g = 0.0f;
     if (lane < a.topk) {
@@ -130,15 +233,15 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteArg
         }
     }
     const float mean = warp_sum(g);
+    __syncwarp();
+    if (id >= 0 && id < a.experts)
+        chosen[id] = a.renormalize ? fmaf(-w, mean, g) : g;
+    __syncwarp();
     float d[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        d[i] = 0.0f;
-    if (a.renormalize) {
-        g = fmaf(-w, mean, g);
-    } else {
-        float x[PER];
-        load_logits<DT, PER>(a.logits, t, a.experts, lane, x);
+        d[i] = chosen[i * 32 + lane];
+    if (!a.renormalize) {
         uint32_t most = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
@@ -155,16 +258,8 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteArg
             const float f = __fdiv_rn(-mean, warp_sum(sum));
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                d[i] = __fmul_rn(f, x[i]);
+                d[i] = fmaf(f, x[i], d[i]);
         }
-    }
-    for (int j = 0; j < a.topk; ++j) {
-        const int e = __shfl_sync(kAll, id, j);
-        const float v = __shfl_sync(kAll, g, j);
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (i * 32 + lane == e)
-                d[i] += v;
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
