@@ -529,6 +529,17 @@ __device__ __forceinline__ void dequantize_lane(Codes<DT> c, float s,
     }
 }
 
+// One thread's bulk copy of `bytes` from shared to global memory; its
+// completion is tracked with commit / wait groups.
+__device__ __forceinline__ void bulk_store(void *gdst, const void *ssrc, uint32_t bytes)
+{
+    if (!LPC_WRITE_OK(gdst, bytes))
+        return;
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst),
+                 "r"(static_cast<uint32_t>(__cvta_generic_to_shared(ssrc))), "r"(bytes)
+                 : "memory");
+}
+
 // Number of valid elements of a lane whose first element is e0.
 template <int DT>
 __device__ __forceinline__ int lane_count(size_t n, size_t e0)

@@ -147,7 +147,7 @@ cudaError_t launch_route_backward(const RouteArgs &a, cudaStream_t st);
 struct SortArgs {
     const int32_t *ids;
     int32_t *slot_row, *row_slot, *offsets, *counts;
-    int32_t *chunk_counts;  // workspace: [chunks][experts]
+    int32_t *chunk_counts;  // workspace: [experts][chunks]
     int slots, experts, capacity, rows;
     int chunks, chunk_len;
 };

@@ -34,6 +34,7 @@ template <int kElems> constexpr int kThreadsOne = 8192 / kElems;
 template <int kElems> constexpr int kThreadsTwo = 4096 / kElems;
 constexpr int kMaxWarps = kThreadsOne<8> / 32;
 constexpr int kMaxStages = 4;
+constexpr int kMaxCluster = 8;
 
 // How rows are dealt out: `threads` lanes of each of `cluster` CTAs share a
 // row, `packs` accesses of it per CTA; a CTA has `groups` such teams and a
@@ -67,90 +68,79 @@ __device__ __forceinline__ float cluster_load(const float *p, unsigned rank)
 }
 
 // Waits for the threads of this team: of all CTAs of its cluster, of its CTA,
-// or of its part of a CTA (barriers 1.. of the CTA, one per team).
+// or of its part of a CTA (barrier 1 + team of the CTA).
 __device__ __forceinline__ void team_barrier(const Deal &deal)
 {
     if (deal.cluster > 1)
         cluster_barrier();
     else if (deal.groups == 1)
         __syncthreads();
-    else if (deal.threads == 32)
-        __syncwarp();
-    else  // at most 8 teams of 64 threads or more
+    else  // teams of 64 threads or more, 8 of them at most
         asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / deal.threads),
                      "r"(deal.threads)
                      : "memory");
 }
 
+template <int N> constexpr int kSplit = N == 1 ? 1 : (N == 2 ? 2 : 8);
+
 // Sums over a team of N <= 8 values per thread, the same bits in every thread
-// of the team and in every run. The lanes first split the values between them
-// (each step halves both the values a lane holds and the lanes that share
-// one), 9 shuffles instead of 5 N; the warps' sums then meet in `red`. The
-// caller alternates between two `red`, so that one barrier is enough.
-// first_warp: the team's first in its CTA.
+// of the team and in every run. The lanes of a warp split the values between
+// them (each step halves both the values a lane holds and the lanes that share
+// one: 9 shuffles for 6 values instead of 30); the warps' sums then meet in
+// `red`. The caller alternates between two `red`, so that one barrier per sum
+// is enough. first_warp: the team's first in its CTA.
 template <int N>
 __device__ __forceinline__ void team_sums(float (&v)[N], float (*red)[8], const Deal &deal,
                                           int first_warp)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int P = kSplit<N>;
+    const int lane = threadIdx.x & 31;
     const int warps = deal.threads >> 5;
-    const bool many = warps > 1 || deal.cluster > 1;
-    if constexpr (N == 1) {
-        float sum = warp_sum(v[0]);
-        if (many) {
-            if (lane == 0)
-                red[warp][0] = sum;
-            team_barrier(deal);
-            sum = 0.0f;
-            if (deal.cluster == 1) {
-                if (lane < warps)
-                    sum = red[first_warp + lane][0];
-            } else if (lane < warps) {
-                for (int c = 0; c < deal.cluster; ++c)
-                    sum += cluster_load(&red[lane][0], c);
-            }
-            sum = warp_sum(sum);
+    float s[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        s[i] = i < N ? v[i < N ? i : 0] : 0.0f;
+#pragma unroll
+    for (int half = P / 2; half >= 1; half >>= 1) {
+        const bool up = (lane & half) != 0;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float give = up ? s[i] : s[i + half];
+            const float keep = up ? s[i + half] : s[i];
+            s[i] = keep + __shfl_xor_sync(kAll, give, half);
         }
-        v[0] = sum;
-    } else {
-        float s[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s[i] = i < N ? v[i < N ? i : 0] : 0.0f;
-        // after this lane l holds the sum of value (l & 7) over 4 of the 32 lanes
-#pragma unroll
-        for (int half = 4; half >= 1; half >>= 1) {
-            const bool up = (lane & half) != 0;
-#pragma unroll
-            for (int i = 0; i < half; ++i) {
-                const float give = up ? s[i] : s[i + half];
-                const float keep = up ? s[i + half] : s[i];
-                s[i] = keep + __shfl_xor_sync(kAll, give, half);
-            }
-        }
-        float sum = s[0];
-        sum += __shfl_xor_sync(kAll, sum, 8);
-        sum += __shfl_xor_sync(kAll, sum, 16);
-        if (many) {
-            if (lane < 8)
-                red[warp][lane] = sum;
-            team_barrier(deal);
-            sum = 0.0f;
-            if (deal.cluster == 1) {
-                for (int w = lane >> 3; w < warps; w += 4)
-                    sum += red[first_warp + w][lane & 7];
-            } else {
-                for (int c = 0; c < deal.cluster; ++c)
-                    for (int w = lane >> 3; w < warps; w += 4)
-                        sum += cluster_load(&red[w][lane & 7], c);
-            }
-            sum += __shfl_xor_sync(kAll, sum, 8);
-            sum += __shfl_xor_sync(kAll, sum, 16);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] = __shfl_sync(kAll, sum, i);
     }
+    float sum = s[0];
+#pragma unroll
+    for (int m = P; m < 32; m <<= 1)
+        sum += __shfl_xor_sync(kAll, sum, m);
+    if (warps > 1 || deal.cluster > 1) {
+        if (lane < P)
+            red[threadIdx.x >> 5][lane] = sum;
+        __syncwarp();
+        team_barrier(deal);
+        sum = 0.0f;
+        if (deal.cluster == 1) {
+            for (int w = lane / P; w < warps; w += 32 / P)
+                sum += red[first_warp + w][lane % P];
+        } else {
+            for (int w = lane / P; w < warps; w += 32 / P) {
+                float far[kMaxCluster];
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c)
+                    far[c] = c < deal.cluster ? cluster_load(&red[w][lane % P], c) : 0.0f;
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c)
+                    sum += far[c];
+            }
+        }
+#pragma unroll
+        for (int m = P; m < 32; m <<= 1)
+            sum += __shfl_xor_sync(kAll, sum, m);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = P == 1 ? sum : __shfl_sync(kAll, sum, i);
 }
 
 // 1 / sqrt(mean of squares + eps); rsqrtf is good to 2 ulp.
@@ -311,7 +301,7 @@ __device__ __forceinline__ float load_one(const void *base, size_t e)
 
 // What a thread of a team works on: its warp's part of a row is kElems * 32
 // consecutive columns, access c of all lanes side by side.
-template <int DT, int W, int kElems> struct Member {
+template <int DT, int W, int kElems, bool kPlain> struct Member {
     static constexpr int kN = Pack<DT, W>::kN;
     static constexpr int NV = kElems / kN;
     int group;         // team of the CTA
@@ -339,7 +329,7 @@ template <int DT, int W, int kElems> struct Member {
         stage_bytes = row_bytes * streams;
         place = smem + static_cast<size_t>(group) * stage_bytes * deal.stages + p0 * W;
     }
-    __device__ __forceinline__ bool has(int c) const { return c * 32 < packs; }
+    __device__ __forceinline__ bool has(int c) const { return kPlain || c * 32 < packs; }
     __device__ __forceinline__ int col(int c) const { return col0 + c * 32 * kN; }
     // Element of access c of row t.
     __device__ __forceinline__ size_t elem(size_t t, int c) const
@@ -354,6 +344,30 @@ template <int DT, int W, int kElems> struct Member {
     {
         return unpack<DT, W>(
             *reinterpret_cast<const typename Pack<DT, W>::Raw *>(at(stage, stream, c)));
+    }
+    // FP32 values in the place of an access and, if its elements are shorter,
+    // of the next stream's.
+    __device__ __forceinline__ void keep(int stage, int stream, int c, const Vec<kN> &x) const
+    {
+        using Raw = typename Pack<DT, W>::Raw;
+        constexpr int kParts = kN * 4 / W;
+        Raw raw[kParts];
+        memcpy(raw, x.v, sizeof(x.v));
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+            *reinterpret_cast<Raw *>(at(stage, stream + i, c)) = raw[i];
+    }
+    __device__ __forceinline__ Vec<kN> kept(int stage, int stream, int c) const
+    {
+        using Raw = typename Pack<DT, W>::Raw;
+        constexpr int kParts = kN * 4 / W;
+        Raw raw[kParts];
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+            raw[i] = *reinterpret_cast<const Raw *>(at(stage, stream + i, c));
+        Vec<kN> x;
+        memcpy(x.v, raw, sizeof(x.v));
+        return x;
     }
     // Starts the copy of this thread's part of row t.
     __device__ __forceinline__ void copy(int stage, int stream, const void *base, size_t t) const
@@ -380,8 +394,13 @@ template <int DT, int W, int kElems> struct Member {
     }
 };
 
+// Both kernels exist a second time for the plain case, in which every thread
+// has all its columns, both norms are there, one rank's h, no full gate and, in
+// the gradient, dx_out: without the conditions around every access the compiler
+// interleaves a thread's accesses. Measured: see make_plan.
+
 // Streams of a row: x, a full gate if there is one, then the ranks' h.
-template <int DT, int W, int kElems>
+template <int DT, int W, int kElems, bool kPlain>
 __global__ void __launch_bounds__(kThreadsOne<kElems>, 1)
 residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int streams)
 {
@@ -390,14 +409,15 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
     __shared__ float red[2][kMaxWarps][8];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems> me(deal, a.hidden, streams, reinterpret_cast<char *>(ring_smem));
-    const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
-    const bool full = a.gate_kind == LPCOLL_GATE_FULL;
-    const int h0 = full ? 2 : 1;
+    const Member<DT, W, kElems, kPlain> me(deal, a.hidden, streams, reinterpret_cast<char *>(ring_smem));
+    const bool post = kPlain || a.w_post != nullptr, pre = kPlain || a.w_pre != nullptr;
+    const bool full = !kPlain && a.gate_kind == LPCOLL_GATE_FULL;
+    const int h0 = full ? 2 : 1, nranks = kPlain ? 1 : a.nranks;
+    void *const h_sum = kPlain ? nullptr : a.h_sum;
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
     const auto fetch = [&](size_t t, int stage) {
         if (t < a.tokens) {
-            for (int r = 0; r < a.nranks; ++r)
+            for (int r = 0; r < nranks; ++r)
                 me.copy(stage, h0 + r, a.h[r], t);
             me.copy(stage, 0, a.x, t);
             if (full)
@@ -424,38 +444,51 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
         }
     }
 
-    int stage = 0;
-    for (size_t t = me.t0; t - me.group < a.tokens; t += me.step) {
-        const bool live = t < a.tokens;
-        const float gate_t =
-            a.gate_kind == LPCOLL_GATE_TOKEN && live ? load_one<DT>(a.gate, t) : 1.0f;
-        copy_wait(deal.stages - 1);
-        Vec<kN> v[NV];
-        float r1[1] = {1.0f}, r2[1] = {0.0f};
+    // The ranks' sum for the row in `stage`, left in FP32 in the place of the
+    // first ranks' values, and this thread's part of the sum of its squares.
+    const auto sum_ranks = [&](int stage) {
         Acc<kN> sq = {};
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-            v[c] = splat<kN>(0.0f);
-            if (!live || !me.has(c))
+            if (!me.has(c))
                 continue;
-            v[c] = me.read(stage, h0, c);
-            for (int r = 1; r < a.nranks; ++r)
-                v[c] = add(v[c], me.read(stage, h0 + r, c));
-            if (a.h_sum != nullptr)
-                store_vec_of<DT, W>(a.h_sum, me.elem(t, c), v[c]);
-            add_products(sq, v[c], v[c]);
+            Vec<kN> h = me.read(stage, h0, c);
+            if (nranks > 1) {
+#pragma unroll 4
+                for (int r = 1; r < nranks; ++r)
+                    h = add(h, me.read(stage, h0 + r, c));
+                me.keep(stage, h0, c, h);
+            }
+            add_products(sq, h, h);
         }
+        return fold(sq);
+    };
+
+    // Each turn ends row t and takes the next row's sum of squares of h with
+    // its own of x', so that there is one barrier per row.
+    int stage = 0, turn = 0;
+    float r1 = 1.0f;
+    copy_wait(deal.stages - 1);
+    const bool summed = post || nranks > 1;
+    if (summed) {
+        float s[1] = {me.t0 < a.tokens ? sum_ranks(0) : 0.0f};
         if (post) {
-            r1[0] = fold(sq);
-            team_sums(r1, red[0], deal, me.first_warp);
-            r1[0] = inv_rms(r1[0], per_hidden, a.eps);
+            team_sums(s, red[1], deal, me.first_warp);
+            r1 = inv_rms(s[0], per_hidden, a.eps);
         }
-        const float f = r1[0] * gate_t;
-        sq = {};
+    }
+    for (size_t t = me.t0; t < a.tokens; t += me.step, turn ^= 1) {
+        const float gate_t = a.gate_kind == LPCOLL_GATE_TOKEN ? load_one<DT>(a.gate, t) : 1.0f;
+        const float f = r1 * gate_t;
+        Vec<kN> v[NV];
+        Acc<kN> sq = {};
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-            if (!live || !me.has(c))
+            if (!me.has(c))
                 continue;
+            v[c] = nranks > 1 ? me.kept(stage, h0, c) : me.read(stage, h0, c);
+            if (h_sum != nullptr)
+                store_vec_of<DT, W>(h_sum, me.elem(t, c), v[c]);
             Vec<kN> u = mul(mul(f, wq[c]), v[c]);
             if (full)
                 u = mul(u, me.read(stage, 1, c));
@@ -464,19 +497,20 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
             store_vec_of<DT, W>(a.x_out, me.elem(t, c), v[c]);
         }
         fetch(t + deal.stages * me.step, stage);
+        stage = stage + 1 == deal.stages ? 0 : stage + 1;
+        copy_wait(deal.stages - 1);
+        float s[2] = {fold(sq), summed && t + me.step < a.tokens ? sum_ranks(stage) : 0.0f};
+        if (post || pre)
+            team_sums(s, red[turn], deal, me.first_warp);
+        r1 = post ? inv_rms(s[1], per_hidden, a.eps) : 1.0f;
         if (pre) {
-            r2[0] = fold(sq);
-            team_sums(r2, red[1], deal, me.first_warp);
-            r2[0] = inv_rms(r2[0], per_hidden, a.eps);
+            const float r2 = inv_rms(s[0], per_hidden, a.eps);
 #pragma unroll
             for (int c = 0; c < NV; ++c)
-                if (live && me.has(c))
+                if (me.has(c))
                     store_vec_of<DT, W>(a.n_out, me.elem(t, c),
-                                        mul(mul(r2[0], unpack<DT, W>(wp[c])), v[c]));
+                                        mul(mul(r2, unpack<DT, W>(wp[c])), v[c]));
         }
-        if (!(post && pre))
-            team_barrier(deal);  // red is used again only after a barrier
-        stage = stage + 1 == deal.stages ? 0 : stage + 1;
     }
     if (deal.cluster > 1)
         cluster_barrier();  // no CTA leaves while another reads its sums
@@ -499,7 +533,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
 // Row streams of a stage.
 enum Stream { kH = 0, kDx = 1, kX = 2, kDn = 3, kGate = 4 };
 
-template <int DT, int W, int kElems>
+template <int DT, int W, int kElems, bool kPlain>
 __global__ void __launch_bounds__(kThreadsOne<kElems>, 1)
 residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal deal, int streams)
 {
@@ -508,9 +542,10 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
     __shared__ float red[2][kMaxWarps][8];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems> me(deal, a.hidden, streams, reinterpret_cast<char *>(ring_smem));
-    const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr, given = a.dx_out != nullptr;
-    const bool full = a.gate_kind == LPCOLL_GATE_FULL;
+    const Member<DT, W, kElems, kPlain> me(deal, a.hidden, streams, reinterpret_cast<char *>(ring_smem));
+    const bool post = kPlain || a.w_post != nullptr, pre = kPlain || a.w_pre != nullptr;
+    const bool given = kPlain || a.dx_out != nullptr;
+    const bool full = !kPlain && a.gate_kind == LPCOLL_GATE_FULL;
     const int H = a.hidden;
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(H));
     const auto fetch = [&](size_t t, int stage) {
@@ -548,39 +583,40 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
         }
     }
 
+    // a thread's part of the six sums of row t
+    const auto row_sums = [&](int stage, float (&s)[6]) {
+        Acc<kN> v[6] = {};
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            if (!me.has(c))
+                continue;
+            const Vec<kN> h = me.read(stage, kH, c);
+            Vec<kN> p = mul(wq[c], h);
+            add_products(v[0], h, h);
+            if (full)
+                p = mul(p, me.read(stage, kGate, c));
+            if (given)
+                add_products(v[3], p, me.read(stage, kDx, c));
+            if (pre) {
+                const Vec<kN> x = me.read(stage, kX, c);
+                const Vec<kN> q = mul(me.read(stage, kDn, c), unpack<DT, W>(wp[c]));
+                add_products(v[1], x, x);
+                add_products(v[2], q, x);
+                add_products(v[4], p, q);
+                add_products(v[5], p, x);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            s[i] = fold(v[i]);
+    };
+
     int stage = 0, turn = 0;
-    for (size_t t = me.t0; t - me.group < a.tokens; t += me.step, turn ^= 1) {
-        const bool live = t < a.tokens;
-        const float gate_t =
-            a.gate_kind == LPCOLL_GATE_TOKEN && live ? load_one<DT>(a.gate, t) : 1.0f;
+    for (size_t t = me.t0; t < a.tokens; t += me.step, turn ^= 1) {
+        const float gate_t = a.gate_kind == LPCOLL_GATE_TOKEN ? load_one<DT>(a.gate, t) : 1.0f;
         copy_wait(deal.stages - 1);
         float s[6];
-        {
-            Acc<kN> v[6] = {};
-#pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                if (!live || !me.has(c))
-                    continue;
-                const Vec<kN> h = me.read(stage, kH, c);
-                Vec<kN> p = mul(wq[c], h);
-                add_products(v[0], h, h);
-                if (full)
-                    p = mul(p, me.read(stage, kGate, c));
-                if (given)
-                    add_products(v[3], p, me.read(stage, kDx, c));
-                if (pre) {
-                    const Vec<kN> x = me.read(stage, kX, c);
-                    const Vec<kN> q = mul(me.read(stage, kDn, c), unpack<DT, W>(wp[c]));
-                    add_products(v[1], x, x);
-                    add_products(v[2], q, x);
-                    add_products(v[4], p, q);
-                    add_products(v[5], p, x);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 6; ++i)
-                s[i] = fold(v[i]);
-        }
+        row_sums(stage, s);
         team_sums(s, red[turn], deal, me.first_warp);
         const float r1 = post ? inv_rms(s[0], per_hidden, a.eps) : 1.0f;
         const float r2 = pre ? inv_rms(s[1], per_hidden, a.eps) : 0.0f;
@@ -590,11 +626,11 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
         // dh = f1 wq g D - f2 h;  S += f1 g h D
         const float f1 = r1 * bt;
         const float f2 = post ? r1 * (r1 * r1 * bt * pd * per_hidden) : 0.0f;
-        if (a.gate_kind == LPCOLL_GATE_TOKEN && a.dgate != nullptr && live && me.col0 == 0)
+        if (a.gate_kind == LPCOLL_GATE_TOKEN && a.dgate != nullptr && me.col0 == 0)
             store_f32(static_cast<float *>(a.dgate) + t, a.branch_scale * r1 * pd);
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-            if (!live || !me.has(c))
+            if (!me.has(c))
                 continue;
             Vec<kN> d = splat<kN>(0.0f);
             if (given)
@@ -709,6 +745,7 @@ int round_up(int n, int to) { return (n + to - 1) / to * to; }
 struct Plan {
     Deal deal;
     int elems;    // columns of a thread
+    bool even;    // every thread has all its columns
     int ctas;     // CTAs, or clusters of them, that share the rows
     size_t smem;  // dynamic shared memory of a CTA
 };
@@ -718,11 +755,12 @@ constexpr size_t kSmemOne = 224 * 1024, kSmemTwo = 110 * 1024;
 
 // A row is one CTA's, or, from 8193 columns on or where there are few tokens,
 // a cluster's. 16 columns a thread halve what a row costs besides its columns
-// (sums, addresses): 8192 columns in BF16 took 147 instead of 239 us for the
-// gradients of 8192 tokens, 193 instead of 256 us for 16384 tokens forward. 8
-// columns are faster where latency counts (32 tokens: 5.6 against 6.1 us) and
-// for the shortest rows (128 columns: 7.2 against 9.0 us).
-Plan make_plan(size_t tokens, int hidden, int dtype, int streams, size_t sums_smem)
+// (sums, addresses), 8 columns give twice the warps. 8192 columns in BF16: the
+// gradients of 8192 tokens take 134 us with 16 and 177 with 8, the forward pass
+// of 16384 tokens 183 and 160 (of 8 ranks at 4096 columns 121 and 125). 8 are
+// also faster where latency counts (32 tokens: 5.6 against 6.1 us) and for the
+// shortest rows (128 columns: 7.2 against 9.0 us).
+Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
 {
     const int width = row_width(hidden, dtype);
     const int kn = width / static_cast<int>(dtype_bytes(dtype));
@@ -730,20 +768,23 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, size_t sums_sm
     // keeps two warps
     constexpr int kRow = 8192;  // columns of the largest CTA
     int cluster = hidden > kRow ? 2 : 1;
-    while (cluster < 8 && tokens * cluster * 2 <= kSms && hidden >= 512 * cluster * 2)
+    while (cluster < kMaxCluster && tokens * cluster * 2 <= kSms && hidden >= 512 * cluster * 2)
         cluster *= 2;
     // many ranks: until a row of all streams fits the shared memory
-    while (cluster < 8 && (static_cast<size_t>(hidden) * width / kn / cluster + 16 * kn) * streams >
+    while (cluster < kMaxCluster && (static_cast<size_t>(hidden) * width / kn / cluster + 16 * kn) * streams >
                               kSmemOne)
         cluster *= 2;
     Plan p;
-    p.elems = hidden <= 256 || tokens <= kSms ? 8 : 16;
+    const bool light = !gradient && streams <= 2 && hidden <= kRow;
+    p.elems = hidden <= 256 || tokens <= kSms || light ? 8 : 16;
     Deal &d = p.deal;
     d.cluster = cluster;
     d.packs = ((hidden + kn - 1) / kn + cluster - 1) / cluster;
     d.threads = round_up((d.packs + p.elems / kn - 1) / (p.elems / kn), 32);
     const int share = p.elems == 8 ? kThreadsTwo<8> : kThreadsTwo<16>;
     d.groups = cluster > 1 || d.threads * 2 > share ? 1 : share / d.threads;
+    p.even = width == 16 && hidden % kn == 0 && d.packs * cluster * kn == hidden &&
+             d.packs % (32 * (p.elems / kn)) == 0;
     const bool two = d.threads * d.groups <= share;
     const size_t steps = (tokens + d.groups - 1) / d.groups;
     const size_t most = static_cast<size_t>(kSms) * (two ? 2 : 1) / cluster;
@@ -751,7 +792,8 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, size_t sums_sm
     const size_t stage = static_cast<size_t>(round_up(d.packs * width, 16)) * streams * d.groups;
     const size_t fit = (two ? kSmemTwo : kSmemOne) / stage;
     d.stages = static_cast<int>(fit > kMaxStages ? kMaxStages : (fit < 1 ? 1 : fit));
-    const size_t sums = d.groups > 1 ? sums_smem : 0;
+    // the groups of a CTA add up their sums over tokens in shared memory
+    const size_t sums = gradient && d.groups > 1 ? static_cast<size_t>(hidden) * 2 * sizeof(float) : 0;
     p.smem = d.stages * stage > sums ? d.stages * stage : sums;
     return p;
 }
@@ -773,26 +815,40 @@ cudaError_t launch_plan(Kernel kernel, const NormArgs &a, const Plan &p, int str
 Plan backward_plan(size_t tokens, int hidden, int dtype, int gate_kind)
 {
     const int streams = gate_kind == LPCOLL_GATE_FULL ? 5 : 4;
-    // the groups of a CTA add up their sums in shared memory
-    return make_plan(tokens, hidden, dtype, streams,
-                     static_cast<size_t>(hidden) * 2 * sizeof(float));
+    return make_plan(tokens, hidden, dtype, streams, true);
 }
 
 template <int DT, int W>
 cudaError_t backward_dt(const NormArgs &a, const Plan &p, cudaStream_t st)
 {
-    return launch_plan(p.elems == 8 ? residual_norm_backward_kernel<DT, W, 8>
-                                    : residual_norm_backward_kernel<DT, W, 16>,
-                       a, p, a.gate_kind == LPCOLL_GATE_FULL ? 5 : 4, st);
+    const bool full = a.gate_kind == LPCOLL_GATE_FULL;
+    const int streams = full ? 5 : 4;
+    if constexpr (W == 16) {
+        if (p.even && !full && a.w_post != nullptr && a.w_pre != nullptr && a.dx_out != nullptr)
+            return launch_plan(p.elems == 8 ? residual_norm_backward_kernel<DT, W, 8, true>
+                                            : residual_norm_backward_kernel<DT, W, 16, true>,
+                               a, p, streams, st);
+    }
+    return launch_plan(p.elems == 8 ? residual_norm_backward_kernel<DT, W, 8, false>
+                                    : residual_norm_backward_kernel<DT, W, 16, false>,
+                       a, p, streams, st);
 }
 
 template <int DT, int W>
 cudaError_t forward_dt(const NormArgs &a, cudaStream_t st)
 {
-    const int streams = a.nranks + 1 + (a.gate_kind == LPCOLL_GATE_FULL ? 1 : 0);
-    const Plan p = make_plan(a.tokens, a.hidden, a.dtype, streams, 0);
-    return launch_plan(p.elems == 8 ? residual_norm_kernel<DT, W, 8>
-                                    : residual_norm_kernel<DT, W, 16>,
+    const bool full = a.gate_kind == LPCOLL_GATE_FULL;
+    const int streams = a.nranks + 1 + (full ? 1 : 0);
+    const Plan p = make_plan(a.tokens, a.hidden, a.dtype, streams, false);
+    if constexpr (W == 16) {
+        if (p.even && !full && a.w_post != nullptr && a.w_pre != nullptr && a.nranks == 1 &&
+            a.h_sum == nullptr)
+            return launch_plan(p.elems == 8 ? residual_norm_kernel<DT, W, 8, true>
+                                            : residual_norm_kernel<DT, W, 16, true>,
+                               a, p, streams, st);
+    }
+    return launch_plan(p.elems == 8 ? residual_norm_kernel<DT, W, 8, false>
+                                    : residual_norm_kernel<DT, W, 16, false>,
                        a, p, streams, st);
 }
 

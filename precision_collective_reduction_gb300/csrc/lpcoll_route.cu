@@ -2,8 +2,8 @@
 // the K largest of each token, and the gradient) and the stable counting sort
 // of the (token, choice) slots by expert.
 //
-// Router: one warp per token, lane l holding the logits of experts l, l + 32,
-// ... as order-preserving integers. Instructions bound it, not the logits'
+// Router: one warp per token, the logits of a lane's experts as
+// order-preserving integers. Instructions bound it, not the logits'
 // traffic, so a choice is one warp-wide integer maximum: 22 bits of the logit
 // and 10 of the expert's index make one unsigned number whose order is that
 // of the logits, lower index first. For BF16 the 22 bits hold the whole logit;
@@ -20,34 +20,89 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 // Keys up to this one are "no expert": -infinity, a choice taken, padding.
 constexpr uint32_t kKeyNone = 0x007FFFFFu;
-constexpr uint32_t kKeyNan = 0xFFFFFFFFu;
 
-// Order-preserving key of a logit: -0 equals +0, a NaN is above +infinity.
+// Order-preserving key of a logit: -0 equals +0, and every NaN is the largest
+// key, since an addition returns all of them as 0x7FFFFFFF.
 __device__ __forceinline__ uint32_t logit_key(float x)
 {
-    if (isnan(x))
-        return kKeyNan;
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    return b ^ ((b >> 31) != 0 ? 0xFFFFFFFFu : 0x80000000u);
+    const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ float key_logit(uint32_t k)
 {
-    return k == kKeyNan ? __uint_as_float(0x7FC00000u)
-                        : __uint_as_float(k ^ ((k >> 31) != 0 ? 0x80000000u : 0xFFFFFFFFu));
+    return __uint_as_float(k ^ ((k >> 31) != 0 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// 2^x, 2 ulp; results below the normal range are 0.
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A term e^d of a softmax's sum, d <= 0: the rounding of the product moves it
+// by |d| 2^-24 of itself, at most 2^-25 of the sum's largest term.
+__device__ __forceinline__ float exp_term(float d)
+{
+    return exp2_fast(__fmul_rn(d, 1.44269504f));
+}
+
+// The PER experts of a lane come in runs of kRun consecutive ones, run r at
+// (r * 32 + lane) * kRun, so that a run is one access where rows of logits
+// are a multiple of a run.
+template <int DT, int PER> constexpr int kRun = PER < Fmt<DT>::kVec ? PER : Fmt<DT>::kVec;
+
+template <int DT, int PER> __device__ __forceinline__ int expert_of(int i, int lane)
+{
+    constexpr int R = kRun<DT, PER>;
+    return (i / R * 32 + lane) * R + i % R;
+}
+
+template <int BYTES> struct RunBytes;
+template <> struct RunBytes<4> {
+    using Raw = uint32_t;
+};
+template <> struct RunBytes<8> {
+    using Raw = uint2;
+};
+template <> struct RunBytes<16> {
+    using Raw = uint4;
+};
+
+// -infinity where there is no expert.
 template <int DT, int PER>
 __device__ __forceinline__ void load_logits(const void *logits, size_t t, int experts, int lane,
                                             float (&x)[PER])
 {
-    float one[1];
+    constexpr int R = kRun<DT, PER>;
+    constexpr int kEs = kOne<DT>;
+    using Raw = typename RunBytes<R * kEs>::Raw;
+    const char *row = static_cast<const char *>(logits) + t * experts * kEs;
+    if (experts % R == 0) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 + lane;
-        x[i] = -INFINITY;
-        if (e < experts) {
-            widen_pack<DT, kOne<DT>>(load_pack<DT, kOne<DT>>(logits, t * experts + e), one);
+        for (int r = 0; r < PER / R; ++r) {
+            const int e = (r * 32 + lane) * R;
+            typename Pack<DT, kEs>::Raw v[R];
+            if (e < experts && LPC_READ_OK(row + e * kEs, R * kEs)) {
+                const Raw raw = *reinterpret_cast<const Raw *>(row + e * kEs);
+                memcpy(v, &raw, sizeof(raw));
+            }
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                float one[1];
+                widen_pack<DT, kEs>(v[j], one);
+                x[r * R + j] = e < experts ? one[0] : -INFINITY;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = expert_of<DT, PER>(i, lane);
+            float one[1] = {-INFINITY};
+            if (e < experts)
+                widen_pack<DT, kEs>(load_pack<DT, kEs>(row, e), one);
             x[i] = one[0];
         }
     }
@@ -115,17 +170,17 @@ __device__ __noinline__ int choose_apart(const void *logits, size_t t, int exper
         for (int i = 0; i < PER; ++i)
             if (key[i] > best) {
                 best = key[i];
-                at = i;
+                at = expert_of<DT, PER>(i, lane);
             }
         const uint32_t most = __reduce_max_sync(kAll, best);
         if (most <= kKeyNone)
             break;
-        const int id = __reduce_min_sync(kAll, best == most ? at * 32 + lane : INT32_MAX);
+        const int id = __reduce_min_sync(kAll, best == most ? at : INT32_MAX);
         if (lane == j)
             my_id = id;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (i * 32 + lane == id)
+            if (expert_of<DT, PER>(i, lane) == id)
                 key[i] = 0;
     }
     return my_id;
@@ -145,14 +200,15 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a)
     uint32_t list[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const uint32_t key = logit_key(x[i]);
-        list[i] = key > kKeyNone ? (key & ~kIndexBits) | (kIndexBits - (i * 32 + lane)) : 0u;
+        // a number of -infinity, of an expert that is not there too, stays
+        // below kKeyNone
+        list[i] = (logit_key(x[i]) & ~kIndexBits) | (kIndexBits - expert_of<DT, PER>(i, lane));
     }
     sort_down<0, PER>(list);
     uint32_t mine = 0, most = 0;
     for (int j = 0; j < a.topk; ++j) {
         most = __reduce_max_sync(kAll, list[0]);
-        if (most == 0)
+        if (most <= kKeyNone)
             break;
         if (lane == j)
             mine = most;
@@ -178,7 +234,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a)
         const bool unsure =
             (lane > 0 && mine != 0 && (mine ^ before) <= kIndexBits &&
              logit_key(z) != logit_key(z_before)) ||
-            (lane == a.topk - 1 && mine != 0 && next != 0 && (mine ^ next) <= kIndexBits);
+            (lane == a.topk - 1 && mine != 0 && next > kKeyNone &&
+             (mine ^ next) <= kIndexBits);
         if (__any_sync(kAll, unsure)) {
             my_id = choose_apart<DT, PER>(a.logits, t, a.experts, a.topk, lane);
             z = logit_of(my_id);
@@ -194,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a)
             sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                sum += expf(x[i] - m);
+                sum += exp_term(x[i] - m);
         }
         w = __fdiv_rn(w, warp_sum(sum));
     }
@@ -204,6 +261,9 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a)
     }
 }
 
+// Tokens of a warp of the gradient kernel, whose logits it loads together.
+template <int PER> constexpr int kPairs = PER <= 8 ? 2 : 1;
+
 // dl_e = [e chosen as j] w_j dw_j - p_e sum_j w_j dw_j, with p = w at the
 // chosen and 0 elsewhere when the weights were renormalised. The chosen
 // experts' terms go through a row in shared memory.
@@ -211,63 +271,110 @@ template <int DT, int PER>
 __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteArgs a)
 {
     wait_prior_grid();
-    __shared__ float chosen_all[kWarpsPerCta][PER * 32];
+    constexpr int R = kRun<DT, PER>;
+    constexpr int kEs = kOne<DT>;
+    using Raw = typename RunBytes<R * kEs>::Raw;
+    __shared__ __align__(16) float chosen_all[kWarpsPerCta][PER * 32];
     float *const chosen = chosen_all[threadIdx.x >> 5];
     const int lane = threadIdx.x & 31;
-    const size_t t = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    if (t >= a.tokens)
-        return;
-    float x[PER];
-    if (!a.renormalize)
-        load_logits<DT, PER>(a.logits, t, a.experts, lane, x);
+    const size_t t0 =
+        ((static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5) * kPairs<PER>;
+    float x[kPairs<PER>][PER], w[kPairs<PER>], g[kPairs<PER>];
+    int id[kPairs<PER>];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        chosen[i * 32 + lane] = 0.0f;
-    int id = -1;
-    float w = 0.0f, g = 0.0f;
-    if (lane < a.topk) {
-        id = load_i32(a.ids + t * a.topk + lane);
-        if (id >= 0 && id < a.experts) {
-            w = load_f32(a.weights + t * a.topk + lane);
-            g = __fmul_rn(w, load_f32(a.dweights + t * a.topk + lane));
+    for (int q = 0; q < kPairs<PER>; ++q) {
+        id[q] = -1;
+        w[q] = g[q] = 0.0f;
+        const size_t t = t0 + q;
+        if (t < a.tokens) {
+            if (!a.renormalize)
+                load_logits<DT, PER>(a.logits, t, a.experts, lane, x[q]);
+            if (lane < a.topk) {
+                id[q] = load_i32(a.ids + t * a.topk + lane);
+                w[q] = load_f32(a.weights + t * a.topk + lane);
+                g[q] = load_f32(a.dweights + t * a.topk + lane);
+            }
         }
     }
-    const float mean = warp_sum(g);
-    __syncwarp();
-    if (id >= 0 && id < a.experts)
-        chosen[id] = a.renormalize ? fmaf(-w, mean, g) : g;
-    __syncwarp();
-    float d[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        d[i] = chosen[i * 32 + lane];
-    if (!a.renormalize) {
-        uint32_t most = 0;
+    for (int q = 0; q < kPairs<PER>; ++q) {
+        const size_t t = t0 + q;
+        if (t >= a.tokens)
+            return;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            most = max(most, logit_key(x[i]));
-        most = __reduce_max_sync(kAll, most);
-        if (most > kKeyNone) {
-            const float m = key_logit(most);
+            chosen[i * 32 + lane] = 0.0f;
+        const bool there = id[q] >= 0 && id[q] < a.experts;
+        g[q] = there ? __fmul_rn(w[q], g[q]) : 0.0f;
+        const float mean = warp_sum(g[q]);
+        __syncwarp();
+        if (there)
+            chosen[id[q]] = a.renormalize ? fmaf(-w[q], mean, g[q]) : g[q];
+        __syncwarp();
+        float d[PER];
+#pragma unroll
+        for (int r = 0; r < PER / R; ++r) {
+            const float *p = chosen + (r * 32 + lane) * R;
+            if constexpr (R % 4 == 0) {
+#pragma unroll
+                for (int j = 0; j < R; j += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(p + j);
+                    d[r * R + j] = v.x;
+                    d[r * R + j + 1] = v.y;
+                    d[r * R + j + 2] = v.z;
+                    d[r * R + j + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    d[r * R + j] = p[j];
+            }
+        }
+        __syncwarp();
+        if (!a.renormalize) {
+            // a NaN logit does not reach the maximum, but makes the sum NaN
+            float most = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                most = fmaxf(most, x[q][i]);
+            const uint32_t key = __reduce_max_sync(kAll, logit_key(most));
+            const float m = key > kKeyNone ? key_logit(key) : 0.0f;
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                x[i] = expf(x[i] - m);
-                sum += x[i];
+                x[q][i] = exp_term(x[q][i] - m);
+                sum += x[q][i];
             }
-            const float f = __fdiv_rn(-mean, warp_sum(sum));
+            sum = warp_sum(sum);
+            if (sum != 0.0f) {  // else no expert is left: zeros
+                const float f = __fdiv_rn(-mean, sum);
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                d[i] = fmaf(f, x[i], d[i]);
+                for (int i = 0; i < PER; ++i)
+                    d[i] = fmaf(f, x[q][i], d[i]);
+            }
         }
-    }
+        char *row = static_cast<char *>(a.dlogits) + t * a.experts * kEs;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 + lane;
-        const float one[1] = {d[i]};
-        if (e < a.experts)
-            store_pack<DT, kOne<DT>>(a.dlogits, t * a.experts + e,
-                                     narrow_pack<DT, kOne<DT>>(one));
+        for (int r = 0; r < PER / R; ++r) {
+            const int e = (r * 32 + lane) * R;
+            typename Pack<DT, kEs>::Raw v[R];
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                const float one[1] = {d[r * R + j]};
+                v[j] = narrow_pack<DT, kEs>(one);
+            }
+            if (a.experts % R == 0) {
+                Raw raw;
+                memcpy(&raw, v, sizeof(raw));
+                if (e < a.experts && LPC_WRITE_OK(row + e * kEs, R * kEs))
+                    *reinterpret_cast<Raw *>(row + e * kEs) = raw;
+            } else {
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    if (e + j < a.experts)
+                        store_pack<DT, kEs>(row, e + j, v[j]);
+            }
+        }
     }
 }
 
@@ -308,14 +415,15 @@ __global__ void __launch_bounds__(kThreads) sort_count_kernel(const SortArgs a)
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += kThreads)
-        store_i32(a.chunk_counts + static_cast<size_t>(blockIdx.x) * a.experts + e, hist[e]);
+        store_i32(a.chunk_counts + static_cast<size_t>(e) * a.chunks + blockIdx.x, hist[e]);
 }
 
 __global__ void __launch_bounds__(kThreads) sort_place_kernel(const SortArgs a)
 {
     // next[w][e]: rank within expert e of warp w's next slot
     __shared__ int next[kWarpsPerCta][LPCOLL_MAX_EXPERTS];
-    __shared__ int first[LPCOLL_MAX_EXPERTS];  // first row of an expert
+    // first row of an expert; before that, its slots in the chunks before
+    __shared__ int first[LPCOLL_MAX_EXPERTS];
     __shared__ int total[LPCOLL_MAX_EXPERTS];  // slots of an expert
     __shared__ int warp_total[kWarpsPerCta];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -338,24 +446,50 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(const SortArgs a)
             atomicAdd(&next[warp][e], 1);
     }
     __syncthreads();
-    for (int e = tid; e < E; e += kThreads) {
-        int sum = 0, before = 0;
-        if (a.chunks > 1) {
-#pragma unroll 8
-            for (int c = 0; c < a.chunks; ++c) {
-                const int v = load_i32(a.chunk_counts + static_cast<size_t>(c) * E + e);
-                sum += v;
-                before += c < static_cast<int>(blockIdx.x) ? v : 0;
+    if (a.chunks > 1) {
+        // slots of each expert in all chunks, and in those before this one: a
+        // warp for kAhead experts at a time, a lane per chunk
+        constexpr int kAhead = 4, kSteps = kSortMaxChunks / 32;
+        for (int e0 = warp * kAhead; e0 < E; e0 += kWarpsPerCta * kAhead) {
+            int v[kAhead][kSteps];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const int c = i * 32 + lane;
+                    v[q][i] = e0 + q < E && c < a.chunks
+                                  ? load_i32(a.chunk_counts +
+                                             static_cast<size_t>(e0 + q) * a.chunks + c)
+                                  : 0;
+                }
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                int sum = 0, before = 0;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    sum += v[q][i];
+                    before += i * 32 + lane < static_cast<int>(blockIdx.x) ? v[q][i] : 0;
+                }
+                sum = __reduce_add_sync(kAll, sum);
+                before = __reduce_add_sync(kAll, before);
+                if (lane == 0 && e0 + q < E) {
+                    total[e0 + q] = sum;
+                    first[e0 + q] = before;
+                }
             }
         }
-        int run = before;
+        __syncthreads();
+    }
+    for (int e = tid; e < E; e += kThreads) {
+        int run = a.chunks > 1 ? first[e] : 0;
 #pragma unroll
         for (int w = 0; w < kWarpsPerCta; ++w) {
             const int v = next[w][e];
             next[w][e] = run;
             run += v;
         }
-        total[e] = a.chunks > 1 ? sum : run;
+        if (a.chunks == 1)
+            total[e] = run;
     }
     __syncthreads();
 
@@ -433,13 +567,19 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(const SortArgs a)
     }
 }
 
-size_t token_ctas(size_t tokens) { return (tokens + kWarpsPerCta - 1) / kWarpsPerCta; }
+size_t token_ctas(size_t tokens, int per_warp)
+{
+    const size_t per_cta = static_cast<size_t>(kWarpsPerCta) * per_warp;
+    return (tokens + per_cta - 1) / per_cta;
+}
 
 template <int DT, int PER>
 cudaError_t route_per(const RouteArgs &a, bool backward, cudaStream_t st)
 {
-    return launch_kernel_block(backward ? route_backward_kernel<DT, PER> : route_kernel<DT, PER>,
-                               token_ctas(a.tokens), kThreads, 0, st, a);
+    if (backward)
+        return launch_kernel_block(route_backward_kernel<DT, PER>,
+                                   token_ctas(a.tokens, kPairs<PER>), kThreads, 0, st, a);
+    return launch_kernel_block(route_kernel<DT, PER>, token_ctas(a.tokens, 1), kThreads, 0, st, a);
 }
 
 // Logits per lane: the smallest power of two that holds the experts.
