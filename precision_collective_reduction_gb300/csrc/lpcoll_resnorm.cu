@@ -299,6 +299,16 @@ __device__ __forceinline__ float load_one(const void *base, size_t e)
     return one[0];
 }
 
+// Shared memory of a warp's part of an odd row, of kElems columns per lane: its
+// words, and one more.
+__host__ __device__ constexpr int odd_warp_bytes(int elems) { return elems * 32 * 2 + 16; }
+
+// Shared memory of a CTA's part of a row, a multiple of 16 bytes.
+__host__ __device__ constexpr int row_part_bytes(int width, int packs, int threads, int elems)
+{
+    return width == 2 ? threads / 32 * odd_warp_bytes(elems) : (packs * width + 15) & ~15;
+}
+
 // What a thread of a team works on: its warp's part of a row is kElems * 32
 // consecutive columns, access c of all lanes side by side.
 template <int DT, int W, int kElems, bool kPlain> struct Member {
@@ -312,22 +322,34 @@ template <int DT, int W, int kElems, bool kPlain> struct Member {
     int hidden;
     char *place;       // this thread's place in the team's ring
     int row_bytes, stage_bytes;
+    // Rows of an odd number of BF16 elements (W = 2): a warp copies the aligned
+    // words that its columns lie in, lane for lane, and reads them from the
+    // element on that the row begins with; `end` is the tensors' end.
+    int warp_col;
+    size_t end;
 
-    __device__ __forceinline__ Member(const Deal &deal, int h, int streams, char *smem)
+    __device__ __forceinline__ Member(const Deal &deal, const NormArgs &a, int streams, char *smem)
     {
-        hidden = h;
+        hidden = a.hidden;
         group = static_cast<int>(threadIdx.x) / deal.threads;
         const int id = static_cast<int>(threadIdx.x) - group * deal.threads;
         first_warp = group * (deal.threads >> 5);
         const int part = deal.cluster > 1 ? static_cast<int>(cluster_rank()) * deal.packs : 0;
         const int p0 = (id >> 5) * NV * 32 + (id & 31);
         col0 = (part + p0) * kN;
-        packs = min(deal.packs, (h + kN - 1) / kN - part) - p0;
+        packs = min(deal.packs, (hidden + kN - 1) / kN - part) - p0;
         step = static_cast<size_t>(gridDim.x / deal.cluster) * deal.groups;
         t0 = static_cast<size_t>(blockIdx.x / deal.cluster) * deal.groups + group;
-        row_bytes = (deal.packs * W + 15) & ~15;
+        row_bytes = row_part_bytes(W, deal.packs, deal.threads, kElems);
         stage_bytes = row_bytes * streams;
-        place = smem + static_cast<size_t>(group) * stage_bytes * deal.stages + p0 * W;
+        place = smem + static_cast<size_t>(group) * stage_bytes * deal.stages;
+        if constexpr (W == 2) {
+            warp_col = part + (id >> 5) * NV * 32;
+            end = a.tokens * hidden;
+            place += (id >> 5) * odd_warp_bytes(kElems) + (id & 31) * W;
+        } else {
+            place += p0 * W;
+        }
     }
     __device__ __forceinline__ bool has(int c) const { return kPlain || c * 32 < packs; }
     __device__ __forceinline__ int col(int c) const { return col0 + c * 32 * kN; }
@@ -336,18 +358,51 @@ template <int DT, int W, int kElems, bool kPlain> struct Member {
     {
         return (t * hidden + col0) + c * 32 * kN;
     }
-    __device__ __forceinline__ char *at(int stage, int stream, int c) const
+    // Where access c of row t is, in its stage and stream.
+    __device__ __forceinline__ char *at(size_t t, int stage, int stream, int c) const
     {
-        return place + stage * stage_bytes + stream * row_bytes + c * 32 * W;
+        char *p = place + stage * stage_bytes + stream * row_bytes + c * 32 * W;
+        if constexpr (W == 2)
+            p += (t * hidden + warp_col) % 2 * W;
+        return p;
     }
-    __device__ __forceinline__ Vec<kN> read(int stage, int stream, int c) const
+    __device__ __forceinline__ Vec<kN> read(size_t t, int stage, int stream, int c) const
     {
         return unpack<DT, W>(
-            *reinterpret_cast<const typename Pack<DT, W>::Raw *>(at(stage, stream, c)));
+            *reinterpret_cast<const typename Pack<DT, W>::Raw *>(at(t, stage, stream, c)));
+    }
+    // wq = f w_post gate and wp = w_pre of this thread's columns, as far as they
+    // are there. All loads go out before the first value is used.
+    __device__ __forceinline__ void weights(const NormArgs &a, bool post, bool channel, bool pre,
+                                            float f, Vec<kN> (&wq)[NV],
+                                            typename Pack<DT, W>::Raw (&wp)[NV]) const
+    {
+        typename Pack<DT, W>::Raw rw[NV], rg[NV];
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            rw[c] = rg[c] = wp[c] = {};
+            if (has(c)) {
+                if (post)
+                    rw[c] = load_pack<DT, W>(a.w_post, col(c));
+                if (channel)
+                    rg[c] = load_pack<DT, W>(a.gate, col(c));
+                if (pre)
+                    wp[c] = load_pack<DT, W>(a.w_pre, col(c));
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            wq[c] = splat<kN>(f);
+            if (post)
+                wq[c] = mul(wq[c], unpack<DT, W>(rw[c]));
+            if (channel)
+                wq[c] = mul(wq[c], unpack<DT, W>(rg[c]));
+        }
     }
     // FP32 values in the place of an access and, if its elements are shorter,
     // of the next stream's.
-    __device__ __forceinline__ void keep(int stage, int stream, int c, const Vec<kN> &x) const
+    __device__ __forceinline__ void keep(size_t t, int stage, int stream, int c,
+                                         const Vec<kN> &x) const
     {
         using Raw = typename Pack<DT, W>::Raw;
         constexpr int kParts = kN * 4 / W;
@@ -355,16 +410,16 @@ template <int DT, int W, int kElems, bool kPlain> struct Member {
         memcpy(raw, x.v, sizeof(x.v));
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
-            *reinterpret_cast<Raw *>(at(stage, stream + i, c)) = raw[i];
+            *reinterpret_cast<Raw *>(at(t, stage, stream + i, c)) = raw[i];
     }
-    __device__ __forceinline__ Vec<kN> kept(int stage, int stream, int c) const
+    __device__ __forceinline__ Vec<kN> kept(size_t t, int stage, int stream, int c) const
     {
         using Raw = typename Pack<DT, W>::Raw;
         constexpr int kParts = kN * 4 / W;
         Raw raw[kParts];
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
-            raw[i] = *reinterpret_cast<const Raw *>(at(stage, stream + i, c));
+            raw[i] = *reinterpret_cast<const Raw *>(at(t, stage, stream + i, c));
         Vec<kN> x;
         memcpy(x.v, raw, sizeof(x.v));
         return x;
@@ -372,25 +427,37 @@ template <int DT, int W, int kElems, bool kPlain> struct Member {
     // Starts the copy of this thread's part of row t.
     __device__ __forceinline__ void copy(int stage, int stream, const void *base, size_t t) const
     {
-        using Raw = typename Pack<DT, W>::Raw;
-        const Raw *src = static_cast<const Raw *>(base);
         if constexpr (W >= 4) {
+            using Raw = typename Pack<DT, W>::Raw;
+            const Raw *src = static_cast<const Raw *>(base) + (t * hidden + col0) / kN;
 #pragma unroll
             for (int c = 0; c < NV; ++c)
                 if (has(c))
-                    copy_async<W>(at(stage, stream, c),
-                                  src + (t * hidden + col0) / kN + c * 32);
-        } else {  // no asynchronous copy of 2 bytes: all loads before the stores
-            Raw v[NV];
-#pragma unroll
-            for (int c = 0; c < NV; ++c)
-                if (has(c))
-                    v[c] = load_pack<DT, W>(base, elem(t, c));
-#pragma unroll
-            for (int c = 0; c < NV; ++c)
-                if (has(c))
-                    *reinterpret_cast<Raw *>(at(stage, stream, c)) = v[c];
+                    copy_async<W>(at(t, stage, stream, c), src + c * 32);
+        } else {
+            const int lane = static_cast<int>(threadIdx.x) & 31;
+            const int n = min(packs + lane, NV * 32);  // columns of the warp
+            const size_t e0 = t * hidden + warp_col, first = e0 & ~static_cast<size_t>(1);
+            const int words = n > 0 ? static_cast<int>(e0 - first + n + 1) / 2 : 0;
+            const uint16_t *src = static_cast<const uint16_t *>(base) + first;
+            uint16_t *dst = reinterpret_cast<uint16_t *>(place + stage * stage_bytes +
+                                                         stream * row_bytes) - lane;
+            __syncwarp();  // the words' last readers are done
+            for (int w = lane; w < words; w += 32) {
+                if (first + 2 * w + 1 < end)
+                    copy_async<4>(dst + 2 * w, src + 2 * w);
+                else  // the tensor's last element, alone in its word
+                    dst[2 * w] = load_pack<DT, 2>(src, 2 * w);
+            }
         }
+    }
+    // Waits for a row's copies, this thread's or, where they share them, the
+    // warp's.
+    __device__ __forceinline__ void ready(int pending) const
+    {
+        copy_wait(pending);
+        if constexpr (W == 2)
+            __syncwarp();
     }
 };
 
@@ -409,7 +476,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
     __shared__ float red[2][kMaxWarps][8];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems, kPlain> me(deal, a.hidden, streams, reinterpret_cast<char *>(ring_smem));
+    const Member<DT, W, kElems, kPlain> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
     const bool post = kPlain || a.w_post != nullptr, pre = kPlain || a.w_pre != nullptr;
     const bool full = !kPlain && a.gate_kind == LPCOLL_GATE_FULL;
     const int h0 = full ? 2 : 1, nranks = kPlain ? 1 : a.nranks;
@@ -430,34 +497,22 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
 
     Vec<kN> wq[NV];  // beta w_post, times a channel's gate
     typename Pack<DT, W>::Raw wp[NV];
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-        wq[c] = splat<kN>(a.branch_scale);
-        wp[c] = {};
-        if (me.has(c)) {
-            if (post)
-                wq[c] = mul(wq[c], load_vec_of<DT, W>(a.w_post, me.col(c)));
-            if (a.gate_kind == LPCOLL_GATE_CHANNEL)
-                wq[c] = mul(wq[c], load_vec_of<DT, W>(a.gate, me.col(c)));
-            if (pre)
-                wp[c] = load_pack<DT, W>(a.w_pre, me.col(c));
-        }
-    }
+    me.weights(a, post, a.gate_kind == LPCOLL_GATE_CHANNEL, pre, a.branch_scale, wq, wp);
 
     // The ranks' sum for the row in `stage`, left in FP32 in the place of the
     // first ranks' values, and this thread's part of the sum of its squares.
-    const auto sum_ranks = [&](int stage) {
+    const auto sum_ranks = [&](size_t t, int stage) {
         Acc<kN> sq = {};
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             if (!me.has(c))
                 continue;
-            Vec<kN> h = me.read(stage, h0, c);
+            Vec<kN> h = me.read(t, stage, h0, c);
             if (nranks > 1) {
 #pragma unroll 4
                 for (int r = 1; r < nranks; ++r)
-                    h = add(h, me.read(stage, h0 + r, c));
-                me.keep(stage, h0, c, h);
+                    h = add(h, me.read(t, stage, h0 + r, c));
+                me.keep(t, stage, h0, c, h);
             }
             add_products(sq, h, h);
         }
@@ -468,10 +523,10 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
     // its own of x', so that there is one barrier per row.
     int stage = 0, turn = 0;
     float r1 = 1.0f;
-    copy_wait(deal.stages - 1);
+    me.ready(deal.stages - 1);
     const bool summed = post || nranks > 1;
     if (summed) {
-        float s[1] = {me.t0 < a.tokens ? sum_ranks(0) : 0.0f};
+        float s[1] = {me.t0 < a.tokens ? sum_ranks(me.t0, 0) : 0.0f};
         if (post) {
             team_sums(s, red[1], deal, me.first_warp);
             r1 = inv_rms(s[0], per_hidden, a.eps);
@@ -486,20 +541,20 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
         for (int c = 0; c < NV; ++c) {
             if (!me.has(c))
                 continue;
-            v[c] = nranks > 1 ? me.kept(stage, h0, c) : me.read(stage, h0, c);
+            v[c] = nranks > 1 ? me.kept(t, stage, h0, c) : me.read(t, stage, h0, c);
             if (h_sum != nullptr)
                 store_vec_of<DT, W>(h_sum, me.elem(t, c), v[c]);
             Vec<kN> u = mul(mul(f, wq[c]), v[c]);
             if (full)
-                u = mul(u, me.read(stage, 1, c));
-            v[c] = fma(a.res_scale, me.read(stage, 0, c), u);
+                u = mul(u, me.read(t, stage, 1, c));
+            v[c] = fma(a.res_scale, me.read(t, stage, 0, c), u);
             add_products(sq, v[c], v[c]);
             store_vec_of<DT, W>(a.x_out, me.elem(t, c), v[c]);
         }
         fetch(t + deal.stages * me.step, stage);
         stage = stage + 1 == deal.stages ? 0 : stage + 1;
-        copy_wait(deal.stages - 1);
-        float s[2] = {fold(sq), summed && t + me.step < a.tokens ? sum_ranks(stage) : 0.0f};
+        me.ready(deal.stages - 1);
+        float s[2] = {fold(sq), summed && t + me.step < a.tokens ? sum_ranks(t + me.step, stage) : 0.0f};
         if (post || pre)
             team_sums(s, red[turn], deal, me.first_warp);
         r1 = post ? inv_rms(s[1], per_hidden, a.eps) : 1.0f;
@@ -542,7 +597,7 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
     __shared__ float red[2][kMaxWarps][8];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems, kPlain> me(deal, a.hidden, streams, reinterpret_cast<char *>(ring_smem));
+    const Member<DT, W, kElems, kPlain> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
     const bool post = kPlain || a.w_post != nullptr, pre = kPlain || a.w_pre != nullptr;
     const bool given = kPlain || a.dx_out != nullptr;
     const bool full = !kPlain && a.gate_kind == LPCOLL_GATE_FULL;
@@ -568,38 +623,28 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
     Vec<kN> wq[NV];                    // w_post times a channel's gate
     typename Pack<DT, W>::Raw wp[NV];  // w_pre
     Vec<kN> S[NV], s_pre[NV];
+    me.weights(a, post, a.gate_kind == LPCOLL_GATE_CHANNEL, pre, 1.0f, wq, wp);
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
+    for (int c = 0; c < NV; ++c)
         S[c] = s_pre[c] = splat<kN>(0.0f);
-        wq[c] = splat<kN>(1.0f);
-        wp[c] = {};
-        if (me.has(c)) {
-            if (post)
-                wq[c] = load_vec_of<DT, W>(a.w_post, me.col(c));
-            if (a.gate_kind == LPCOLL_GATE_CHANNEL)
-                wq[c] = mul(wq[c], load_vec_of<DT, W>(a.gate, me.col(c)));
-            if (pre)
-                wp[c] = load_pack<DT, W>(a.w_pre, me.col(c));
-        }
-    }
 
-    // a thread's part of the six sums of row t
-    const auto row_sums = [&](int stage, float (&s)[6]) {
+    // a thread's part of the six sums of the row in `stage`
+    const auto row_sums = [&](size_t t, int stage, float (&s)[6]) {
         Acc<kN> v[6] = {};
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             if (!me.has(c))
                 continue;
-            const Vec<kN> h = me.read(stage, kH, c);
+            const Vec<kN> h = me.read(t, stage, kH, c);
             Vec<kN> p = mul(wq[c], h);
             add_products(v[0], h, h);
             if (full)
-                p = mul(p, me.read(stage, kGate, c));
+                p = mul(p, me.read(t, stage, kGate, c));
             if (given)
-                add_products(v[3], p, me.read(stage, kDx, c));
+                add_products(v[3], p, me.read(t, stage, kDx, c));
             if (pre) {
-                const Vec<kN> x = me.read(stage, kX, c);
-                const Vec<kN> q = mul(me.read(stage, kDn, c), unpack<DT, W>(wp[c]));
+                const Vec<kN> x = me.read(t, stage, kX, c);
+                const Vec<kN> q = mul(me.read(t, stage, kDn, c), unpack<DT, W>(wp[c]));
                 add_products(v[1], x, x);
                 add_products(v[2], q, x);
                 add_products(v[4], p, q);
@@ -614,9 +659,9 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
     int stage = 0, turn = 0;
     for (size_t t = me.t0; t < a.tokens; t += me.step, turn ^= 1) {
         const float gate_t = a.gate_kind == LPCOLL_GATE_TOKEN ? load_one<DT>(a.gate, t) : 1.0f;
-        copy_wait(deal.stages - 1);
+        me.ready(deal.stages - 1);
         float s[6];
-        row_sums(stage, s);
+        row_sums(t, stage, s);
         team_sums(s, red[turn], deal, me.first_warp);
         const float r1 = post ? inv_rms(s[0], per_hidden, a.eps) : 1.0f;
         const float r2 = pre ? inv_rms(s[1], per_hidden, a.eps) : 0.0f;
@@ -634,20 +679,20 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
                 continue;
             Vec<kN> d = splat<kN>(0.0f);
             if (given)
-                d = me.read(stage, kDx, c);
+                d = me.read(t, stage, kDx, c);
             if (pre) {
-                const Vec<kN> x = me.read(stage, kX, c), dn = me.read(stage, kDn, c);
+                const Vec<kN> x = me.read(t, stage, kX, c), dn = me.read(t, stage, kDn, c);
                 const Vec<kN> q = mul(dn, unpack<DT, W>(wp[c]));
                 s_pre[c] = fma(mul(r2, dn), x, s_pre[c]);
                 d = fma(r2, fma(-c2, x, q), d);
             }
             store_vec_of<DT, W>(a.dx, me.elem(t, c), mul(a.res_scale, d));
-            const Vec<kN> h = me.read(stage, kH, c);
+            const Vec<kN> h = me.read(t, stage, kH, c);
             if (full) {
                 if (a.dgate != nullptr)
                     store_vec_of<DT, W>(a.dgate, me.elem(t, c),
                                         mul(mul(mul(f1, wq[c]), h), d));
-                d = mul(d, me.read(stage, kGate, c));
+                d = mul(d, me.read(t, stage, kGate, c));
             }
             const Vec<kN> e = mul(f1, d);
             S[c] = fma(h, e, S[c]);
@@ -695,36 +740,43 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
     }
 }
 
-// Column sums of the workspace: a CTA adds 32 columns of one of the two sums,
-// 8 threads per column that each take every 8th CTA's part, in order.
+// Column sums of the workspace: a CTA adds 32 columns of one of the two sums.
+// 32 threads per column take every 32nd CTA's part, all in flight at once (up to
+// kColumnParts), and a warp adds up a column's 32.
+constexpr int kColumnParts = 2 * kSms / 32 + 1;
+
 template <int DT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(1024)
 norm_column_sums_kernel(const __grid_constant__ NormArgs a, int parts, int column_ctas)
 {
     wait_prior_grid();
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     const int which = blockIdx.x / column_ctas;
     const bool channel = a.gate_kind == LPCOLL_GATE_CHANNEL;
     float *const dgate = channel ? static_cast<float *>(a.dgate) : nullptr;
     if (which == 0 ? a.dw_pre == nullptr : a.dw_post == nullptr && dgate == nullptr)
         return;
-    const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
-    const int col = (blockIdx.x % column_ctas) * 32 + lane;
-    float sum = 0.0f;
-    if (col < a.hidden) {
-        const float *p = a.partial + static_cast<size_t>(which) * parts * a.hidden + col;
-#pragma unroll 8
-        for (int q = group; q < parts; q += 8)
-            sum += load_f32(p + static_cast<size_t>(q) * a.hidden);
-    }
-    red[group][lane] = sum;
-    __syncthreads();
-    if (group != 0 || col >= a.hidden)
-        return;
-    sum = 0.0f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first = (blockIdx.x % column_ctas) * 32;
+    const float *p = a.partial + static_cast<size_t>(which) * parts * a.hidden + first + lane;
+    float v[kColumnParts];
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-        sum += red[q][lane];
+    for (int i = 0; i < kColumnParts; ++i) {
+        const int q = i * 32 + warp;
+        v[i] = q < parts && first + lane < a.hidden
+                   ? load_f32(p + static_cast<size_t>(q) * a.hidden)
+                   : 0.0f;
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kColumnParts; ++i)
+        sum += v[i];
+    red[warp][lane] = sum;
+    __syncthreads();
+    sum = warp_sum(red[lane][warp]);
+    const int col = first + warp;
+    if (lane != 0 || col >= a.hidden)
+        return;
     if (which == 0 || parts == 0) {  // no tokens: zeros, whatever the weights hold
         if (which == 0)
             store_f32(a.dw_pre + col, sum);
@@ -771,7 +823,7 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
     while (cluster < kMaxCluster && tokens * cluster * 2 <= kSms && hidden >= 512 * cluster * 2)
         cluster *= 2;
     // many ranks: until a row of all streams fits the shared memory
-    while (cluster < kMaxCluster && (static_cast<size_t>(hidden) * width / kn / cluster + 16 * kn) * streams >
+    while (cluster < kMaxCluster && (static_cast<size_t>(hidden) * width / kn / cluster + 2048) * streams >
                               kSmemOne)
         cluster *= 2;
     Plan p;
@@ -789,7 +841,9 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
     const size_t steps = (tokens + d.groups - 1) / d.groups;
     const size_t most = static_cast<size_t>(kSms) * (two ? 2 : 1) / cluster;
     p.ctas = static_cast<int>(steps < most ? steps : most);
-    const size_t stage = static_cast<size_t>(round_up(d.packs * width, 16)) * streams * d.groups;
+    const size_t stage =
+        static_cast<size_t>(row_part_bytes(width, d.packs, d.threads, p.elems)) * streams *
+        d.groups;
     const size_t fit = (two ? kSmemTwo : kSmemOne) / stage;
     d.stages = static_cast<int>(fit > kMaxStages ? kMaxStages : (fit < 1 ? 1 : fit));
     // the groups of a CTA add up their sums over tokens in shared memory
@@ -887,7 +941,7 @@ cudaError_t launch_residual_norm_backward(const NormArgs &args, cudaStream_t st)
     const int ctas = (a.hidden + 31) / 32;
     return launch_kernel_block(a.dtype == LPCOLL_F32 ? norm_column_sums_kernel<LPCOLL_F32>
                                                      : norm_column_sums_kernel<LPCOLL_BF16>,
-                               static_cast<size_t>(2) * ctas, kThreads, 0, st, a, parts, ctas);
+                               static_cast<size_t>(2) * ctas, 1024, 0, st, a, parts, ctas);
 }
 
 }  // namespace lpc

@@ -35,7 +35,7 @@ def _device():
     return torch.cuda.current_device()
 
 
-def _ptr(t, what, dtype, shape, device):
+def _ptr(t, what, dtype, shape, device, rank=None):
     """Device pointer of a tensor of that type, shape and device."""
     # the checks of a good tensor in as few calls as they take: at decode sizes
     # they cost more than the kernels
@@ -45,6 +45,8 @@ def _ptr(t, what, dtype, shape, device):
             return t.data_ptr()
     except AttributeError:
         pass
+    if rank is not None:
+        what = "%s[%d]" % (what, rank)
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % what)
     if t.dtype != dtype:
@@ -287,7 +289,7 @@ def residual_norm(h, x, x_out, n_out=None, gate=None, w_post=None, w_pre=None, r
         h = (h,)
     T, H = _shape(x, 2, "x")
     dt = x.dtype
-    hp = [_ptr(t, "h[%d]" % r, dt, (T, H), dev) for r, t in enumerate(h)]
+    hp = [_ptr(t, "h", dt, (T, H), dev, r) for r, t in enumerate(h)]
     if not hp:
         raise ValueError("need at least one rank")
     kind, gp = _gate(gate, dt, T, H, dev, gate_kind)

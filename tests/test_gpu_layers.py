@@ -127,6 +127,23 @@ def test_route_nan_and_infinity(lib, dt, renorm):
     within(w[3:], (ww[3:], wb[3:]), "weights beside")
 
 
+@pytest.mark.parametrize("E", [8, 100, 256, 300, 1024])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_of_logits_that_agree_in_their_first_bits(lib, E, renorm):
+    # FP32 logits one ulp apart, equal ones among them, in any order
+    g = rng(E, 17)
+    z = (1.0 + g.integers(0, 24, size=(60, E)) * 2.0 ** -23).astype(np.float32)
+    z[20:40] *= -1
+    z[40:] = np.where(g.random((20, E)) < 0.5, z[40:], g.normal(size=(20, E)))
+    K = min(E, 9)
+    ids = torch.empty(60, K, dtype=torch.int32, device="cuda")
+    w = torch.empty(60, K, device="cuda")
+    pcr.expert_route(dev(z), ids, w, renormalize=renorm)
+    wi, ww, wb = ref.route(z, K, renorm)
+    assert np.array_equal(ids.cpu().numpy(), wi)
+    within(w, (ww, wb), "weights")
+
+
 # -- sort ---------------------------------------------------------------------
 
 def maps(T, K, E, capacity):
@@ -175,7 +192,7 @@ def test_sort_of_nothing(lib):
 
 # -- dispatch and combine -----------------------------------------------------
 
-SIZES = [(1, 1, 1, 1), (1, 8, 16, 8192), (3, 2, 4, 7), (5, 4, 6, 130), (9, 3, 8, 96),
+SIZES = [(1, 1, 1, 1), (1500, 2, 5, 512), (1300, 1, 3, 1024), (1, 8, 16, 8192), (3, 2, 4, 7), (5, 4, 6, 130), (9, 3, 8, 96),
          (20, 8, 32, 257), (33, 5, 7, 1000), (64, 32, 64, 128), (130, 2, 3, 2050), (11, 6, 8, 4100)]
 
 
@@ -413,6 +430,39 @@ def test_gate_of_one_dimension_where_both_fit():
     assert torch.equal(out, gate.expand(4, 4))
     pcr.residual_norm(x, torch.zeros_like(x), out, gate=gate, gate_kind="token")
     assert torch.equal(out, gate[:, None].expand(4, 4))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H", [(700, 1025), (1300, 130), (400, 1024), (310, 8704), (160, 16384),
+                                 (5000, 64), (311, 2051)])
+@pytest.mark.parametrize("kind,post,pre", [("channel", True, True), ("token", False, True)])
+def test_norms_of_many_tokens(lib, dt, T, H, kind, post, pre):
+    # several rows per team, in a part of a CTA, a CTA and a cluster
+    test_residual_norm(lib, dt, T, H, kind, post, pre)
+    test_residual_norm_backward(lib, dt, T, H, kind, post, pre)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H", [(3, 8192), (200, 4096), (40, 777), (2, 16384)])
+@pytest.mark.parametrize("kind", [None, "full"])
+def test_residual_norm_of_16_ranks(lib, dt, T, H, kind):
+    a, b, eps = (float(np.float32(v)) for v in (0.9, 0.7, 1e-5))
+    g, hs, x, gate, wq, wp = norm_case(T, H, dt, kind, True, True, 16)
+    out = Out()
+    xo, n, hsum = (out(T, H, dtype=DT[dt]) for _ in range(3))
+    kw = dict(gate=gate, w_post=wq, w_pre=wp, res_scale=a, branch_scale=b, eps=eps, gate_kind=kind)
+    pcr.residual_norm(hs, x, xo, n, h_sum=hsum, **kw)
+    want = ref.residual_norm([f64(t) for t in hs], f64(x), opt64(gate), kind, opt64(wq), opt64(wp),
+                             a, b, eps, dt)
+    for got, w, what in zip((xo, n, hsum), want, ("x_out", "n_out", "h_sum")):
+        within(got, w, what)
+    assert out.intact()
+    # h_sum is what the allreduce of the partial products gives, before rounding
+    # to BF16 equal in FP32: the same sum in the same order
+    total = torch.empty_like(x)
+    pcr.dda_flat_sim([t.view(-1) for t in hs], [torch.empty_like(t).view(-1) for t in hs[1:]]
+                     + [total.view(-1)], block=0)
+    assert torch.equal(total, hsum)
 
 
 def test_norm_gradient_of_no_tokens(lib):
