@@ -628,6 +628,11 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
     for (int c = 0; c < NV; ++c)
         S[c] = s_pre[c] = splat<kN>(0.0f);
 
+    // a token's gate, read a row ahead
+    const auto gate_of = [&](size_t t) {
+        return a.gate_kind == LPCOLL_GATE_TOKEN && t < a.tokens ? load_one<DT>(a.gate, t) : 1.0f;
+    };
+
     // a thread's part of the six sums of the row in `stage`
     const auto row_sums = [&](size_t t, int stage, float (&s)[6]) {
         Acc<kN> v[6] = {};
@@ -657,8 +662,10 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
     };
 
     int stage = 0, turn = 0;
+    float gate_next = gate_of(me.t0);
     for (size_t t = me.t0; t < a.tokens; t += me.step, turn ^= 1) {
-        const float gate_t = a.gate_kind == LPCOLL_GATE_TOKEN ? load_one<DT>(a.gate, t) : 1.0f;
+        const float gate_t = gate_next;
+        gate_next = gate_of(t + me.step);
         me.ready(deal.stages - 1);
         float s[6];
         row_sums(t, stage, s);
@@ -686,7 +693,7 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
                 s_pre[c] = fma(mul(r2, dn), x, s_pre[c]);
                 d = fma(r2, fma(-c2, x, q), d);
             }
-            store_vec_of<DT, W>(a.dx, me.elem(t, c), mul(a.res_scale, d));
+            const Vec<kN> dx = mul(a.res_scale, d);
             const Vec<kN> h = me.read(t, stage, kH, c);
             if (full) {
                 if (a.dgate != nullptr)
@@ -696,6 +703,7 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
             }
             const Vec<kN> e = mul(f1, d);
             S[c] = fma(h, e, S[c]);
+            store_vec_of<DT, W>(a.dx, me.elem(t, c), dx);
             store_vec_of<DT, W>(a.dh, me.elem(t, c), fma(wq[c], e, mul(-f2, h)));
         }
         fetch(t + deal.stages * me.step, stage);

@@ -12,12 +12,17 @@ Results go into tensors that the caller provides; scratch memory is taken from
 the caller's ``workspace`` or, without one, from torch's allocator on the
 call's stream.
 """
+import ctypes
+
 from . import _binding as B
 
 MAX_EXPERTS = 1024
 MAX_TOPK = 32
 MAX_HIDDEN = 16384
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+
+# host arrays of 0..16 device pointers
+_POINTERS = [ctypes.c_void_p * n for n in range(B.MAX_RANKS + 1)]
 
 torch = None  # imported by the first call, as everywhere in the binding
 _raw_stream = None
@@ -290,8 +295,8 @@ def residual_norm(h, x, x_out, n_out=None, gate=None, w_post=None, w_pre=None, r
     T, H = _shape(x, 2, "x")
     dt = x.dtype
     hp = [_ptr(t, "h", dt, (T, H), dev, r) for r, t in enumerate(h)]
-    if not hp:
-        raise ValueError("need at least one rank")
+    if not 1 <= len(hp) <= B.MAX_RANKS:
+        raise ValueError("need 1 to %d ranks, got %d" % (B.MAX_RANKS, len(hp)))
     kind, gp = _gate(gate, dt, T, H, dev, gate_kind)
     if w_pre is not None and n_out is None:
         raise ValueError("w_pre needs n_out")
@@ -301,7 +306,7 @@ def residual_norm(h, x, x_out, n_out=None, gate=None, w_post=None, w_pre=None, r
     op = _ptr(x_out, "x_out", dt, (T, H), dev)
     np_ = _ptr(n_out, "n_out", dt, (T, H), dev) if w_pre is not None else None
     sp = _opt(h_sum, "h_sum", dt, (T, H), dev)
-    B._check(B.lib().residual_norm(B.ptr_array(hp), len(hp), xp, gp, kind, post, pre, res_scale,
+    B._check(B.lib().residual_norm(_POINTERS[len(hp)](*hp), len(hp), xp, gp, kind, post, pre, res_scale,
                                    branch_scale, eps, T, H, _code(x), op, np_, sp,
                                    _stream(stream, dev)), "residual_norm")
     return x_out, n_out
