@@ -32,7 +32,19 @@ constexpr int kSms = 152;
 // 64 or 128 registers a thread.
 template <int kElems> constexpr int kThreadsOne = 8192 / kElems;
 template <int kElems> constexpr int kThreadsTwo = 4096 / kElems;
-constexpr int kMaxWarps = kThreadsOne<8> / 32;
+constexpr int kWideThreads = 1024;
+constexpr int kMaxWarps = kWideThreads / 32;
+
+// Forms of both kernels. kPlain is for calls in which every thread has all its
+// columns, both norms are there, one rank's h, no full gate and, in the
+// gradient, dx_out: without the conditions around every access the compiler
+// interleaves a thread's accesses (gradient of 8192 x 8192 BF16 143 -> 134 us).
+// kWide is for the forward pass of rows of more than 8192 columns, in a CTA of
+// 1024 threads with 16 columns each at 64 registers a thread, the weights from
+// L1 each time (8192 x 12288 BF16: 166 us, 241 with a cluster of two CTAs and the
+// weights in registers; the gradient, which keeps its sums too, 268 against 174).
+enum Mode { kGeneral, kPlain, kWide };
+
 constexpr int kMaxStages = 4;
 constexpr int kMaxCluster = 8;
 
@@ -311,7 +323,7 @@ __host__ __device__ constexpr int row_part_bytes(int width, int packs, int threa
 
 // What a thread of a team works on: its warp's part of a row is kElems * 32
 // consecutive columns, access c of all lanes side by side.
-template <int DT, int W, int kElems, bool kPlain> struct Member {
+template <int DT, int W, int kElems, int kMode> struct Member {
     static constexpr int kN = Pack<DT, W>::kN;
     static constexpr int NV = kElems / kN;
     int group;         // team of the CTA
@@ -351,7 +363,7 @@ template <int DT, int W, int kElems, bool kPlain> struct Member {
             place += p0 * W;
         }
     }
-    __device__ __forceinline__ bool has(int c) const { return kPlain || c * 32 < packs; }
+    __device__ __forceinline__ bool has(int c) const { return kMode == kPlain || c * 32 < packs; }
     __device__ __forceinline__ int col(int c) const { return col0 + c * 32 * kN; }
     // Element of access c of row t.
     __device__ __forceinline__ size_t elem(size_t t, int c) const
@@ -371,8 +383,19 @@ template <int DT, int W, int kElems, bool kPlain> struct Member {
         return unpack<DT, W>(
             *reinterpret_cast<const typename Pack<DT, W>::Raw *>(at(t, stage, stream, c)));
     }
-    // wq = f w_post gate and wp = w_pre of this thread's columns, as far as they
-    // are there. All loads go out before the first value is used.
+    // f w_post gate and w_pre of access c.
+    __device__ __forceinline__ Vec<kN> scale(const NormArgs &a, bool post, bool channel, float f,
+                                             int c) const
+    {
+        Vec<kN> q = splat<kN>(f);
+        if (post)
+            q = mul(q, load_vec_of<DT, W>(a.w_post, col(c)));
+        if (channel)
+            q = mul(q, load_vec_of<DT, W>(a.gate, col(c)));
+        return q;
+    }
+    // Both for all of this thread's columns, as far as they are there. All loads
+    // go out before the first value is used.
     __device__ __forceinline__ void weights(const NormArgs &a, bool post, bool channel, bool pre,
                                             float f, Vec<kN> (&wq)[NV],
                                             typename Pack<DT, W>::Raw (&wp)[NV]) const
@@ -461,14 +484,9 @@ template <int DT, int W, int kElems, bool kPlain> struct Member {
     }
 };
 
-// Both kernels exist a second time for the plain case, in which every thread
-// has all its columns, both norms are there, one rank's h, no full gate and, in
-// the gradient, dx_out: without the conditions around every access the compiler
-// interleaves a thread's accesses. Measured: see make_plan.
-
 // Streams of a row: x, a full gate if there is one, then the ranks' h.
-template <int DT, int W, int kElems, bool kPlain>
-__global__ void __launch_bounds__(kThreadsOne<kElems>, 1)
+template <int DT, int W, int kElems, int kMode>
+__global__ void __launch_bounds__(kMode == kWide ? kWideThreads : kThreadsOne<kElems>, 1)
 residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int streams)
 {
     wait_prior_grid();
@@ -476,11 +494,12 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
     __shared__ float red[2][kMaxWarps][8];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems, kPlain> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
-    const bool post = kPlain || a.w_post != nullptr, pre = kPlain || a.w_pre != nullptr;
-    const bool full = !kPlain && a.gate_kind == LPCOLL_GATE_FULL;
-    const int h0 = full ? 2 : 1, nranks = kPlain ? 1 : a.nranks;
-    void *const h_sum = kPlain ? nullptr : a.h_sum;
+    const Member<DT, W, kElems, kMode> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
+    const bool post = kMode == kPlain || a.w_post != nullptr;
+    const bool pre = kMode == kPlain || a.w_pre != nullptr;
+    const bool full = kMode != kPlain && a.gate_kind == LPCOLL_GATE_FULL;
+    const int h0 = full ? 2 : 1, nranks = kMode == kPlain ? 1 : a.nranks;
+    void *const h_sum = kMode == kPlain ? nullptr : a.h_sum;
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
     const auto fetch = [&](size_t t, int stage) {
         if (t < a.tokens) {
@@ -497,7 +516,15 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
 
     Vec<kN> wq[NV];  // beta w_post, times a channel's gate
     typename Pack<DT, W>::Raw wp[NV];
-    me.weights(a, post, a.gate_kind == LPCOLL_GATE_CHANNEL, pre, a.branch_scale, wq, wp);
+    const bool channel = a.gate_kind == LPCOLL_GATE_CHANNEL;
+    if constexpr (kMode != kWide)
+        me.weights(a, post, channel, pre, a.branch_scale, wq, wp);
+    const auto scale = [&](int c) {
+        return kMode == kWide ? me.scale(a, post, channel, a.branch_scale, c) : wq[c];
+    };
+    const auto w_pre = [&](int c) {
+        return kMode == kWide ? load_vec_of<DT, W>(a.w_pre, me.col(c)) : unpack<DT, W>(wp[c]);
+    };
 
     // The ranks' sum for the row in `stage`, left in FP32 in the place of the
     // first ranks' values, and this thread's part of the sum of its squares.
@@ -544,7 +571,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
             v[c] = nranks > 1 ? me.kept(t, stage, h0, c) : me.read(t, stage, h0, c);
             if (h_sum != nullptr)
                 store_vec_of<DT, W>(h_sum, me.elem(t, c), v[c]);
-            Vec<kN> u = mul(mul(f, wq[c]), v[c]);
+            Vec<kN> u = mul(mul(f, scale(c)), v[c]);
             if (full)
                 u = mul(u, me.read(t, stage, 1, c));
             v[c] = fma(a.res_scale, me.read(t, stage, 0, c), u);
@@ -564,7 +591,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
             for (int c = 0; c < NV; ++c)
                 if (me.has(c))
                     store_vec_of<DT, W>(a.n_out, me.elem(t, c),
-                                        mul(mul(r2, unpack<DT, W>(wp[c])), v[c]));
+                                        mul(mul(r2, w_pre(c)), v[c]));
         }
     }
     if (deal.cluster > 1)
@@ -588,7 +615,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
 // Row streams of a stage.
 enum Stream { kH = 0, kDx = 1, kX = 2, kDn = 3, kGate = 4 };
 
-template <int DT, int W, int kElems, bool kPlain>
+template <int DT, int W, int kElems, int kMode>
 __global__ void __launch_bounds__(kThreadsOne<kElems>, 1)
 residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal deal, int streams)
 {
@@ -597,10 +624,11 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
     __shared__ float red[2][kMaxWarps][8];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems, kPlain> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
-    const bool post = kPlain || a.w_post != nullptr, pre = kPlain || a.w_pre != nullptr;
-    const bool given = kPlain || a.dx_out != nullptr;
-    const bool full = !kPlain && a.gate_kind == LPCOLL_GATE_FULL;
+    const Member<DT, W, kElems, kMode> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
+    const bool post = kMode == kPlain || a.w_post != nullptr;
+    const bool pre = kMode == kPlain || a.w_pre != nullptr;
+    const bool given = kMode == kPlain || a.dx_out != nullptr;
+    const bool full = kMode != kPlain && a.gate_kind == LPCOLL_GATE_FULL;
     const int H = a.hidden;
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(H));
     const auto fetch = [&](size_t t, int stage) {
@@ -751,7 +779,7 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
 // Column sums of the workspace: a CTA adds 32 columns of one of the two sums.
 // 32 threads per column take every 32nd CTA's part, all in flight at once (up to
 // kColumnParts), and a warp adds up a column's 32.
-constexpr int kColumnParts = 2 * kSms / 32 + 1;
+constexpr int kColumnParts = 2 * kSms / 32 + 1;  // of at most 2 CTAs per SM
 
 template <int DT>
 __global__ void __launch_bounds__(1024)
@@ -806,6 +834,7 @@ struct Plan {
     Deal deal;
     int elems;    // columns of a thread
     bool even;    // every thread has all its columns
+    bool wide;    // kWide (forward only)
     int ctas;     // CTAs, or clusters of them, that share the rows
     size_t smem;  // dynamic shared memory of a CTA
 };
@@ -813,28 +842,30 @@ struct Plan {
 // Shared memory of the rings of a CTA, for one or two CTAs per SM.
 constexpr size_t kSmemOne = 224 * 1024, kSmemTwo = 110 * 1024;
 
-// A row is one CTA's, or, from 8193 columns on or where there are few tokens,
-// a cluster's. 16 columns a thread halve what a row costs besides its columns
-// (sums, addresses), 8 columns give twice the warps. 8192 columns in BF16: the
-// gradients of 8192 tokens take 134 us with 16 and 177 with 8, the forward pass
-// of 16384 tokens 183 and 160 (of 8 ranks at 4096 columns 121 and 125). 8 are
-// also faster where latency counts (32 tokens: 5.6 against 6.1 us) and for the
-// shortest rows (128 columns: 7.2 against 9.0 us).
+// A row is one CTA's, or, where there are few tokens or the row does not fit
+// one, a cluster's. 16 columns a thread halve what a row costs besides its
+// columns (sums, addresses), 8 columns give twice the warps. 8192 columns in
+// BF16: the gradients of 8192 tokens take 134 us with 16 and 177 with 8, the
+// forward pass of 16384 tokens 183 and 160 (of 8 ranks at 4096 columns 121 and
+// 125). 8 are also faster where latency counts (32 tokens: 5.6 against 6.1 us)
+// and for the shortest rows (128 columns: 7.2 against 9.0 us).
 Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
 {
     const int width = row_width(hidden, dtype);
     const int kn = width / static_cast<int>(dtype_bytes(dtype));
+    constexpr int kRow = 8192;  // columns of the largest CTA but kWide's
+    Plan p;
+    p.wide = !gradient && width == 16 && hidden > kRow && tokens > kSms &&
+             static_cast<size_t>(hidden) * width / kn * streams <= kSmemOne;
+    int cluster = hidden > kRow && !p.wide ? 2 : 1;
     // few tokens: a row over up to 8 CTAs, while there are SMs left and a CTA
     // keeps two warps
-    constexpr int kRow = 8192;  // columns of the largest CTA
-    int cluster = hidden > kRow ? 2 : 1;
     while (cluster < kMaxCluster && tokens * cluster * 2 <= kSms && hidden >= 512 * cluster * 2)
         cluster *= 2;
     // many ranks: until a row of all streams fits the shared memory
-    while (cluster < kMaxCluster && (static_cast<size_t>(hidden) * width / kn / cluster + 2048) * streams >
-                              kSmemOne)
+    while (!p.wide && cluster < kMaxCluster &&
+           (static_cast<size_t>(hidden) * width / kn / cluster + 2048) * streams > kSmemOne)
         cluster *= 2;
-    Plan p;
     const bool light = !gradient && streams <= 2 && hidden <= kRow;
     p.elems = hidden <= 256 || tokens <= kSms || light ? 8 : 16;
     Deal &d = p.deal;
@@ -852,10 +883,15 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
     const size_t stage =
         static_cast<size_t>(row_part_bytes(width, d.packs, d.threads, p.elems)) * streams *
         d.groups;
-    const size_t fit = (two ? kSmemTwo : kSmemOne) / stage;
-    d.stages = static_cast<int>(fit > kMaxStages ? kMaxStages : (fit < 1 ? 1 : fit));
+    // as many rows under way as fit, and no more than a team has
+    size_t stages = (two ? kSmemTwo : kSmemOne) / stage;
+    const size_t rows = (steps + p.ctas - 1) / p.ctas;
+    stages = stages > kMaxStages ? kMaxStages : stages;
+    stages = stages > rows ? rows : stages;
+    d.stages = stages < 1 ? 1 : static_cast<int>(stages);
     // the groups of a CTA add up their sums over tokens in shared memory
-    const size_t sums = gradient && d.groups > 1 ? static_cast<size_t>(hidden) * 2 * sizeof(float) : 0;
+    const size_t sums =
+        gradient && d.groups > 1 ? static_cast<size_t>(hidden) * 2 * sizeof(float) : 0;
     p.smem = d.stages * stage > sums ? d.stages * stage : sums;
     return p;
 }
@@ -864,11 +900,13 @@ template <class Kernel>
 cudaError_t launch_plan(Kernel kernel, const NormArgs &a, const Plan &p, int streams,
                         cudaStream_t st)
 {
-    // always the same value: calls of several threads must not undo each other's
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemOne));
-    if (e != cudaSuccess)
-        return e;
+    if (p.smem > 48 * 1024) {
+        // always the same value: calls of several threads must not undo each other's
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemOne));
+        if (e != cudaSuccess)
+            return e;
+    }
     return launch_kernel_cluster(kernel, static_cast<size_t>(p.ctas) * p.deal.cluster,
                                  p.deal.threads * p.deal.groups, p.deal.cluster, p.smem, st, a,
                                  p.deal, streams);
@@ -887,12 +925,12 @@ cudaError_t backward_dt(const NormArgs &a, const Plan &p, cudaStream_t st)
     const int streams = full ? 5 : 4;
     if constexpr (W == 16) {
         if (p.even && !full && a.w_post != nullptr && a.w_pre != nullptr && a.dx_out != nullptr)
-            return launch_plan(p.elems == 8 ? residual_norm_backward_kernel<DT, W, 8, true>
-                                            : residual_norm_backward_kernel<DT, W, 16, true>,
+            return launch_plan(p.elems == 8 ? residual_norm_backward_kernel<DT, W, 8, kPlain>
+                                            : residual_norm_backward_kernel<DT, W, 16, kPlain>,
                                a, p, streams, st);
     }
-    return launch_plan(p.elems == 8 ? residual_norm_backward_kernel<DT, W, 8, false>
-                                    : residual_norm_backward_kernel<DT, W, 16, false>,
+    return launch_plan(p.elems == 8 ? residual_norm_backward_kernel<DT, W, 8, kGeneral>
+                                    : residual_norm_backward_kernel<DT, W, 16, kGeneral>,
                        a, p, streams, st);
 }
 
@@ -903,14 +941,16 @@ cudaError_t forward_dt(const NormArgs &a, cudaStream_t st)
     const int streams = a.nranks + 1 + (full ? 1 : 0);
     const Plan p = make_plan(a.tokens, a.hidden, a.dtype, streams, false);
     if constexpr (W == 16) {
+        if (p.wide)
+            return launch_plan(residual_norm_kernel<DT, W, 16, kWide>, a, p, streams, st);
         if (p.even && !full && a.w_post != nullptr && a.w_pre != nullptr && a.nranks == 1 &&
             a.h_sum == nullptr)
-            return launch_plan(p.elems == 8 ? residual_norm_kernel<DT, W, 8, true>
-                                            : residual_norm_kernel<DT, W, 16, true>,
+            return launch_plan(p.elems == 8 ? residual_norm_kernel<DT, W, 8, kPlain>
+                                            : residual_norm_kernel<DT, W, 16, kPlain>,
                                a, p, streams, st);
     }
-    return launch_plan(p.elems == 8 ? residual_norm_kernel<DT, W, 8, false>
-                                    : residual_norm_kernel<DT, W, 16, false>,
+    return launch_plan(p.elems == 8 ? residual_norm_kernel<DT, W, 8, kGeneral>
+                                    : residual_norm_kernel<DT, W, 16, kGeneral>,
                        a, p, streams, st);
 }
 
@@ -918,9 +958,13 @@ cudaError_t forward_dt(const NormArgs &a, cudaStream_t st)
 
 int norm_backward_parts(size_t tokens, size_t hidden, int dtype)
 {
-    return hidden == 0 || tokens == 0
-               ? 0
-               : backward_plan(tokens, static_cast<int>(hidden), dtype, LPCOLL_GATE_NONE).ctas;
+    if (hidden == 0 || tokens == 0)
+        return 0;
+    // the same workspace for every kind of gate
+    const int h = static_cast<int>(hidden);
+    const int some = backward_plan(tokens, h, dtype, LPCOLL_GATE_NONE).ctas;
+    const int full = backward_plan(tokens, h, dtype, LPCOLL_GATE_FULL).ctas;
+    return some > full ? some : full;
 }
 
 cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t st)
