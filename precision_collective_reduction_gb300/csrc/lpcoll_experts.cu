@@ -195,28 +195,100 @@ dispatch_bulk_kernel(const RowsArgs a, unsigned row_bytes, unsigned segs, unsign
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// 16 elements of a row from element i on (missing ones read 0).
+// N words from byte address p on, of any alignment, by aligned words; the bytes
+// from `end` on read 0. p and `end` lie in one buffer that starts on a word.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t *p, const uint8_t *end, uint32_t (&w)[N])
+{
+    const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 3u);
+    const uint8_t *base = p - off;
+    uint32_t v[N + 1];
+    if (base + 4 * (N + 1) <= end && LPC_READ_OK(base, 4 * (N + 1))) {
+#pragma unroll
+        for (int k = 0; k <= N; ++k)
+            v[k] = reinterpret_cast<const uint32_t *>(base)[k];
+    } else {
+#pragma unroll
+        for (int k = 0; k <= N; ++k) {
+            v[k] = 0u;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (base + 4 * k + b < end && LPC_READ_OK(base + 4 * k + b, 1))
+                    v[k] |= static_cast<uint32_t>(base[4 * k + b]) << (8 * b);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        w[k] = __funnelshift_r(v[k], v[k + 1], 8 * off);
+}
+
+// 16 elements of row `row` of a [rows][hidden] matrix from element i on (missing
+// ones read 0).
 template <int DT, int W>
-__device__ __forceinline__ void load_row16(const void *base, size_t row, size_t hidden, size_t i,
-                                           float (&x)[kWideElems])
+__device__ __forceinline__ void load_row16(const void *base, size_t rows, size_t row,
+                                           size_t hidden, size_t i, float (&x)[kWideElems])
 {
     constexpr int V = Fmt<DT>::kVec;
     uint4 raw[kWideElems / V];
+    if constexpr (W == 16) {
 #pragma unroll
-    for (int j = 0; j < kWideElems / V; ++j) {
-        const int cnt = lane_count<DT>(hidden, i + j * V);
-        raw[j] = cnt > 0 ? load_vec<DT>(base, row * hidden + i + j * V,
-                                        access_count<DT>(cnt, W == 16))
-                         : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < kWideElems / V; ++j) {
+            const int cnt = lane_count<DT>(hidden, i + j * V);
+            raw[j] = cnt > 0 ? load_vec<DT>(base, row * hidden + i + j * V, cnt)
+                             : make_uint4(0u, 0u, 0u, 0u);
+        }
+    } else {
+        constexpr int kEs = 16 / V;
+        const uint8_t *first = static_cast<const uint8_t *>(base);
+        uint32_t w[kWideElems * kEs / 4];
+        load_words(first + (row * hidden + i) * kEs, first + rows * hidden * kEs, w);
+        // elements of the next row are not this one's
+#pragma unroll
+        for (int j = 0; j < kWideElems * kEs / 4; ++j) {
+            if (i + (j + 1) * 4 / kEs > hidden)
+                w[j] = i + j * 4 / kEs < hidden ? w[j] & 0xFFFFu : 0u;
+        }
+        memcpy(raw, w, sizeof(w));
     }
     wide_widen<DT>(raw, x);
+}
+
+// Stores the 16 codes of every lane of a warp at p (of any alignment, lane after
+// lane; n of them are the row's) in aligned words: a lane's last word takes the
+// bytes it misses from the next lane.
+__device__ __forceinline__ void store_codes16(uint8_t *p, int n, const uint32_t (&w)[4], int lane)
+{
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3u);
+    const int head = (4 - off) & 3;  // bytes before the lane's first aligned word
+    const uint32_t next = __shfl_down_sync(kAll, w[0], 1);
+    const int n_next = __shfl_down_sync(kAll, n, 1);
+    const auto byte = [&](int b) {
+        if (LPC_WRITE_OK(p + b, 1))
+            p[b] = static_cast<uint8_t>(w[b / 4] >> (8 * (b % 4)));
+    };
+    // bytes that go out one by one: the head, unless the lane before takes it,
+    // and what no whole word holds
+    const int first = lane > 0 && n >= head ? head : 0;
+    const bool shared = head == 0 || (lane < 31 && n_next >= head);
+    int words = n < head ? 0 : (n - head) / 4;
+    if (n == kWideElems && shared)
+        words = 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t v = __funnelshift_r(w[k], k < 3 ? w[k < 3 ? k + 1 : 3] : next, 8 * head);
+        if (k < words && LPC_WRITE_OK(p + head + 4 * k, 4))
+            *reinterpret_cast<uint32_t *>(p + head + 4 * k) = v;
+    }
+#pragma unroll
+    for (int b = 0; b < kWideElems; ++b)
+        if (b < n && b >= first && (b < head || b >= head + 4 * words))
+            byte(b);
 }
 
 __device__ __forceinline__ size_t row_blocks(size_t hidden) { return (hidden + kBlock - 1) / kBlock; }
 
 // Low precision: a lane quantizes 16 consecutive elements, 8 lanes a block of
-// 128, once per token, and writes codes and scales into the K rows. codes are
-// stored 16 at a time where rows of codes start on 16 bytes.
+// 128, once per token, and writes codes and scales into the K rows.
 template <int DT, int W>
 __global__ void __launch_bounds__(kThreads)
 dispatch_lp_kernel(const RowsArgs a, const Cut cut, unsigned clear)
@@ -245,7 +317,7 @@ dispatch_lp_kernel(const RowsArgs a, const Cut cut, unsigned clear)
     const int rows = lane_row(a, t, lane);
     float x[kWideElems];
     if (i < a.hidden) {
-        load_row16<DT, W>(a.x, t, a.hidden, i, x);
+        load_row16<DT, W>(a.x, a.tokens, t, a.hidden, i, x);
     } else {
 #pragma unroll
         for (int j = 0; j < kWideElems; ++j)
@@ -254,12 +326,20 @@ dispatch_lp_kernel(const RowsArgs a, const Cut cut, unsigned clear)
     uint32_t w[4];
     float s;
     wide_quantize(x, w, s);  // all 32 lanes take part
+    const bool aligned = a.hidden % kWideElems == 0;
+    const int n = i >= a.hidden ? 0
+                                : static_cast<int>(a.hidden - i < kWideElems ? a.hidden - i
+                                                                             : kWideElems);
     for (int k = 0; k < a.topk; ++k) {
         const int row = __shfl_sync(kAll, rows, k);
-        if (!has_row(row, a) || i >= a.hidden)
+        if (!has_row(row, a))
             continue;
-        wide_store_codes(a.codes + static_cast<size_t>(row) * a.hidden, a.hidden, i, w);
-        if (lane % kWideGroup == 0)
+        uint8_t *const codes = a.codes + static_cast<size_t>(row) * a.hidden;
+        if (!aligned)
+            store_codes16(codes + i, n, w, lane);
+        else if (n > 0)
+            wide_store_codes(codes, a.hidden, i, w);
+        if (n > 0 && lane % kWideGroup == 0)
             store_scale(a.scales + row * nb + i / kBlock, s);
     }
 }
@@ -322,26 +402,21 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const RowsArgs a, con
     }
 }
 
-// 16 codes of a row from element i on (missing ones read 0).
-__device__ __forceinline__ uint4 load_row_codes(const uint8_t *p, size_t hidden, size_t i,
-                                                bool aligned)
+// 16 codes of row `row` from element i < hidden on; those past the row's end are
+// of no use.
+__device__ __forceinline__ uint4 load_row_codes(const RowsArgs &a, int row, size_t i, bool aligned)
 {
+    const uint8_t *p = a.codes + static_cast<size_t>(row) * a.hidden;
     if (aligned)
-        return wide_load_codes(p, hidden, i);
-    const size_t n = hidden - i < kWideElems ? hidden - i : kWideElems;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (LPC_READ_OK(p + i, n)) {
-#pragma unroll
-        for (int j = 0; j < kWideElems; ++j)
-            if (static_cast<size_t>(j) < n)
-                w[j / 4] |= static_cast<uint32_t>(p[i + j]) << (8 * (j % 4));
-    }
+        return wide_load_codes(p, a.hidden, i);
+    uint32_t w[4];
+    load_words(p + i, static_cast<const uint8_t *>(a.codes) + a.nrows * a.hidden, w);
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The same from FP8 payloads: a row's value is fl(e4m3(code) * scale). A lane
-// holds 16 consecutive elements; a warp's results go through shared memory, so
-// that its stores are consecutive.
+// The same from FP8 payloads, with fl(weight * scale) as the factor of a code's
+// value. A lane holds 16 consecutive elements; a warp's results go through
+// shared memory, so that its stores are consecutive.
 template <int DT, int W>
 __global__ void __launch_bounds__(kThreads) combine_lp_kernel(const RowsArgs a, const Cut cut)
 {
@@ -357,10 +432,10 @@ __global__ void __launch_bounds__(kThreads) combine_lp_kernel(const RowsArgs a, 
     const float weights = lane_weight(a, me.t, lane);
     const size_t nb = row_blocks(a.hidden);
     const bool aligned = a.hidden % 16 == 0, inside = i < a.hidden;
-    float acc[kWideElems];
+    float2 acc[kWideElems / 2];
 #pragma unroll
-    for (int j = 0; j < kWideElems; ++j)
-        acc[j] = 0.0f;
+    for (int j = 0; j < kWideElems / 2; ++j)
+        acc[j] = make_float2(0.0f, 0.0f);
     for (int k0 = 0; k0 < a.topk; k0 += C) {
         uint4 v[C];
         float sc[C];
@@ -369,8 +444,7 @@ __global__ void __launch_bounds__(kThreads) combine_lp_kernel(const RowsArgs a, 
             const int row = __shfl_sync(kAll, rows, (k0 + c) & 31);
             if (k0 + c < a.topk && has_row(row, a) && inside) {
                 sc[c] = load_scale(a.scales + row * nb + i / kBlock);
-                v[c] = load_row_codes(a.codes + static_cast<size_t>(row) * a.hidden, a.hidden, i,
-                                      aligned);
+                v[c] = load_row_codes(a, row, i, aligned);
             }
         }
 #pragma unroll
@@ -378,16 +452,23 @@ __global__ void __launch_bounds__(kThreads) combine_lp_kernel(const RowsArgs a, 
             const int row = __shfl_sync(kAll, rows, (k0 + c) & 31);
             const float w = __shfl_sync(kAll, weights, (k0 + c) & 31);
             if (k0 + c < a.topk && has_row(row, a) && inside) {
-                float x[kWideElems];
-                wide_dequant(v[c], sc[c], x);
+                const float f = __fmul_rn(w, sc[c]);
+                const uint32_t codes[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
-                for (int j = 0; j < kWideElems; ++j)
-                    acc[j] = fmaf(w, x[j], acc[j]);
+                for (int j = 0; j < kWideElems / 2; ++j)
+                    acc[j] = fma_pair(make_float2(f, f), dec2(codes[j / 2] >> (16 * (j % 2))),
+                                      acc[j]);
             }
         }
     }
+    float y[kWideElems];
+#pragma unroll
+    for (int j = 0; j < kWideElems / 2; ++j) {
+        y[2 * j] = acc[j].x;
+        y[2 * j + 1] = acc[j].y;
+    }
     char *const out = static_cast<char *>(a.out) + me.t * a.hidden * (16 / Fmt<DT>::kVec);
-    wide_store_results<DT, W == 16>(out, a.hidden, i - static_cast<size_t>(lane) * kWideElems, acc,
+    wide_store_results<DT, W == 16>(out, a.hidden, i - static_cast<size_t>(lane) * kWideElems, y,
                                     stage_all[threadIdx.x >> 5], lane);
 }
 

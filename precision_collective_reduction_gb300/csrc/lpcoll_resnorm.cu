@@ -161,8 +161,7 @@ __device__ __forceinline__ float inv_rms(float sum, float per_hidden, float eps)
     return rsqrtf(fmaf(sum, per_hidden, eps));
 }
 
-// N FP32 values, multiplied and added two at a time where N is even (each
-// lane of a packed operation rounds as the scalar one does).
+// N FP32 values, multiplied and added two at a time where N is even.
 template <int N> struct Vec {
     float v[N];
 };
@@ -182,11 +181,12 @@ __device__ __forceinline__ Vec<N> mul(const Vec<N> &a, const Vec<N> &b)
     Vec<N> r;
     if constexpr (N % 2 == 0) {
 #pragma unroll
-        for (int j = 0; j < N; j += 2)
-            asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-                "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-                : "=f"(r.v[j]), "=f"(r.v[j + 1])
-                : "f"(a.v[j]), "f"(a.v[j + 1]), "f"(b.v[j]), "f"(b.v[j + 1]));
+        for (int j = 0; j < N; j += 2) {
+            const float2 p = mul_pair(make_float2(a.v[j], a.v[j + 1]),
+                                      make_float2(b.v[j], b.v[j + 1]));
+            r.v[j] = p.x;
+            r.v[j + 1] = p.y;
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j)
@@ -207,12 +207,13 @@ __device__ __forceinline__ Vec<N> fma(const Vec<N> &a, const Vec<N> &b, const Ve
     Vec<N> r;
     if constexpr (N % 2 == 0) {
 #pragma unroll
-        for (int j = 0; j < N; j += 2)
-            asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-                "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-                : "=f"(r.v[j]), "=f"(r.v[j + 1])
-                : "f"(a.v[j]), "f"(a.v[j + 1]), "f"(b.v[j]), "f"(b.v[j + 1]), "f"(c.v[j]),
-                  "f"(c.v[j + 1]));
+        for (int j = 0; j < N; j += 2) {
+            const float2 p = fma_pair(make_float2(a.v[j], a.v[j + 1]),
+                                      make_float2(b.v[j], b.v[j + 1]),
+                                      make_float2(c.v[j], c.v[j + 1]));
+            r.v[j] = p.x;
+            r.v[j + 1] = p.y;
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j)
@@ -520,10 +521,16 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
     if constexpr (kMode != kWide)
         me.weights(a, post, channel, pre, a.branch_scale, wq, wp);
     const auto scale = [&](int c) {
-        return kMode == kWide ? me.scale(a, post, channel, a.branch_scale, c) : wq[c];
+        if constexpr (kMode == kWide)
+            return me.scale(a, post, channel, a.branch_scale, c);
+        else
+            return wq[c];
     };
     const auto w_pre = [&](int c) {
-        return kMode == kWide ? load_vec_of<DT, W>(a.w_pre, me.col(c)) : unpack<DT, W>(wp[c]);
+        if constexpr (kMode == kWide)
+            return load_vec_of<DT, W>(a.w_pre, me.col(c));
+        else
+            return unpack<DT, W>(wp[c]);
     };
 
     // The ranks' sum for the row in `stage`, left in FP32 in the place of the
