@@ -69,24 +69,24 @@ size_t clear_ctas(size_t nrows, int threads)
     return (nrows + per_cta - 1) / per_cta;
 }
 
-// How a token's row is cut: `segs` CTAs of `threads` lanes each, a lane with
-// `per_lane` elements, evenly, so that the last CTA is not nearly empty. Short
-// rows share a CTA, `tokens` of them.
+// How a token's row is cut: `segs` CTAs of `threads` lanes each (up to `most`), a
+// lane with `per_lane` elements, evenly, so that the last CTA is not nearly
+// empty. Short rows share a CTA, `tokens` of them.
 struct Cut {
     unsigned segs;
     int threads, tokens;
     size_t ctas(size_t all_tokens) const { return (all_tokens + tokens - 1) / tokens * segs; }
     int block() const { return threads * tokens; }
 };
-Cut cut_row(size_t hidden, int per_lane)
+Cut cut_row(size_t hidden, int per_lane, int most)
 {
     const size_t lanes = (hidden + per_lane - 1) / per_lane;
-    const size_t segs = (lanes + kThreads - 1) / kThreads;
+    const size_t segs = (lanes + most - 1) / most;
     const size_t each = (lanes + segs - 1) / segs;
     Cut c;
     c.segs = static_cast<unsigned>(segs);
     c.threads = static_cast<int>((each + 31) / 32 * 32);
-    c.tokens = segs > 1 ? 1 : kThreads / c.threads;
+    c.tokens = segs > 1 ? 1 : most / c.threads;
     return c;
 }
 
@@ -572,13 +572,16 @@ combine_backward_kernel(const RowsArgs a, const Cut cut, unsigned clear)
     }
 }
 
-// CTAs from which on a call is bound by traffic, not by latency.
-constexpr size_t kManyCtas = 152 * 8;
+// 16-byte vectors from which on a call is bound by traffic, not by latency: 2048
+// for each SM.
+constexpr size_t kManyVectors = 152 * 2048;
+
+size_t row_vectors(const RowsArgs &a) { return a.tokens * (a.hidden * dtype_bytes(a.dtype) / 16); }
 
 // Shortest row, in bytes, that dispatch sends with bulk copies, and the shared
 // memory of a CTA that does. 8192 tokens to 4 rows of 16 KB each took 99 us
 // against 131 us with the lanes' own stores (floor 99), 32 tokens to 8 rows 4.0
-// against 2.1 us, so bulk copies are for calls of many CTAs.
+// against 2.1 us, so bulk copies are for large calls.
 constexpr size_t kBulkRow = 1024, kBulkChunk = 16 * 1024;
 
 cudaError_t dispatch_bulk(const RowsArgs &a, size_t row_bytes, cudaStream_t st)
@@ -598,10 +601,12 @@ template <int DT, int W>
 cudaError_t dispatch_dt(const RowsArgs &a, bool lp, cudaStream_t st)
 {
     const size_t row_bytes = a.hidden * dtype_bytes(DT);
-    const Cut c = cut_row(a.hidden, lp ? kWideElems : 16 / kOne<DT>);
     if (W == 16 && !lp && row_bytes >= kBulkRow && row_bytes <= 64 * kBulkChunk &&
-        c.ctas(a.tokens) >= kManyCtas)
+        row_vectors(a) >= kManyVectors)
         return dispatch_bulk(a, row_bytes, st);
+    // CTAs of 128 lanes for payloads: 4097 elements 69 against 75 us with 256
+    const Cut c = lp ? cut_row(a.hidden, kWideElems, kThreads / 2)
+                     : cut_row(a.hidden, 16 / kOne<DT>, kThreads);
     const size_t clear = clear_ctas(a.nrows, c.block());
     return launch_kernel_block(lp ? dispatch_lp_kernel<DT, W> : dispatch_kernel<DT, W>,
                                clear + c.ctas(a.tokens), c.block(), 0, st, a, c,
@@ -611,20 +616,24 @@ cudaError_t dispatch_dt(const RowsArgs &a, bool lp, cudaStream_t st)
 template <int DT, int W>
 cudaError_t combine_dt(const RowsArgs &a, bool lp, cudaStream_t st)
 {
+    // CTAs of 64 lanes: 8192 tokens of 4 rows of 8192 BF16 take 97 us against 101
+    // with 256, from FP8 payloads 85 against 89
+    constexpr int kLanes = 64;
     if (lp) {
-        const Cut c = cut_row(a.hidden, kWideElems);
+        const Cut c = cut_row(a.hidden, kWideElems, kLanes);
         return launch_kernel_block(combine_lp_kernel<DT, W>, c.ctas(a.tokens), c.block(), 0, st,
                                    a, c);
     }
     if constexpr (W == 16) {
         // four vectors a lane once there is enough to do: 8192 tokens of 4 rows
-        // of 8192 BF16 99.7 against 108.8 us, 32 tokens of 8 rows 3.6 against 2.3
-        const Cut c = cut_row(a.hidden, 4 * Fmt<DT>::kVec);
-        if (c.ctas(a.tokens) >= kManyCtas)
+        // of 8192 BF16 101 against 109 us, 32 tokens of 8 rows 3.6 against 2.3
+        if (row_vectors(a) >= kManyVectors) {
+            const Cut c = cut_row(a.hidden, 4 * Fmt<DT>::kVec, kLanes);
             return launch_kernel_block(combine_kernel<DT, W, 4>, c.ctas(a.tokens), c.block(), 0,
                                        st, a, c);
+        }
     }
-    const Cut c = cut_row(a.hidden, Fmt<DT>::kVec);
+    const Cut c = cut_row(a.hidden, Fmt<DT>::kVec, kLanes);
     return launch_kernel_block(combine_kernel<DT, W, kPer<W>>, c.ctas(a.tokens), c.block(), 0, st,
                                a, c);
 }
