@@ -41,9 +41,9 @@
  *     while the previous kernel of the stream still runs, but it touches no
  *     memory before that kernel has completed, so stream order holds for
  *     every buffer, also inside CUDA graph capture.
- *   - Resources: kernels of 256 threads, one warp per work item (grids
- *     grow with the message and may exceed what the GPU holds at once; no
- *     CTA ever waits on another). FP32 low-precision allreduces of 8 ranks
+ *   - Resources of the collectives: kernels of 256 threads, one warp per
+ *     work item (grids grow with the message and may exceed what the GPU
+ *     holds at once; no CTA ever waits on another). FP32 low-precision allreduces of 8 ranks
  *     with 1 GiB of input or more, and low-precision all-gathers of
  *     16-byte-aligned contributions, stage results in up to 46 KB of
  *     dynamic shared memory per CTA and write them with bulk (TMA) copies;
@@ -315,7 +315,12 @@ int dda_flat_sim_noalloc(const void *const *in, void *const *out, int nranks,
  *   - all sums are FP32, in an order that depends on the sizes alone, rounded
  *     once at the output; the same call gives the same bits again;
  *   - checks come in the order above; sizes are checked with the dtype
- *     (LPCOLL_ERR_ARG), and an array of no elements may be NULL.
+ *     (LPCOLL_ERR_ARG), and an array of no elements may be NULL;
+ *   - any hidden size works; rows of a multiple of 16 bytes are the fast ones;
+ *   - resources: CTAs of up to 1024 threads and, for residual_norm and its
+ *     gradient, up to 224 KB of dynamic shared memory and clusters of up to 8
+ *     CTAs, which wait for one another (and for nobody else). All copies have
+ *     completed when a kernel does.
  * Limits: rows, slots < 2^31; ntokens * ceil(hidden / 256) < 2^30.
  * ------------------------------------------------------------------------ */
 #define LPCOLL_MAX_EXPERTS 1024

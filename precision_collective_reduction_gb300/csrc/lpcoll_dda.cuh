@@ -310,6 +310,17 @@ __device__ __forceinline__ void dda_units(const DdaParams &p, size_t unit0, int 
             GlobalSink<N, DT, MODE, true>{p, ((unit0 + k) * 32 + lane) * V, V}, lane, raw[k]);
 }
 
+// One thread's bulk copy of `bytes` from shared to global memory; its
+// completion is tracked with commit / wait groups.
+__device__ __forceinline__ void bulk_store(void *gdst, const void *ssrc, uint32_t bytes)
+{
+    if (!LPC_WRITE_OK(gdst, bytes))
+        return;
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst),
+                 "r"(static_cast<uint32_t>(__cvta_generic_to_shared(ssrc))), "r"(bytes)
+                 : "memory");
+}
+
 // Tile path. Full tiles (kTileUnits consecutive full units) go through the
 // CTA's shared-memory tile and bulk copies, two tile buffers alternating;
 // the units after the last full tile (fewer than kTileUnits full ones and

@@ -126,11 +126,9 @@ inline void debug_range(const void *, size_t, bool) {}
 // The launch helpers have internal linkage: in the bounds-checked build each
 // translation unit must copy the buffer list into its own g_debug_ranges, so
 // no two units may share one instantiation of them.
-// `cluster` CTAs form a thread-block cluster (1: none).
 template <typename... Params, typename... Args>
-static cudaError_t launch_kernel_cluster(void (*kernel)(Params...), size_t grid, int threads,
-                                         int cluster, size_t smem, cudaStream_t stream,
-                                         Args... args)
+static cudaError_t launch_kernel_smem(void (*kernel)(Params...), int grid, size_t smem,
+                                      cudaStream_t stream, Args... args)
 {
 #ifdef LPCOLL_DEBUG_BOUNDS
     const cudaError_t de = cudaMemcpyToSymbolAsync(g_debug_ranges, &debug_pending(),
@@ -139,35 +137,17 @@ static cudaError_t launch_kernel_cluster(void (*kernel)(Params...), size_t grid,
     if (de != cudaSuccess)
         return de;
 #endif
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <typename... Params, typename... Args>
-static cudaError_t launch_kernel_block(void (*kernel)(Params...), size_t grid, int threads,
-                                       size_t smem, cudaStream_t stream, Args... args)
-{
-    return launch_kernel_cluster(kernel, grid, threads, 1, smem, stream, args...);
-}
-
-template <typename... Params, typename... Args>
-static cudaError_t launch_kernel_smem(void (*kernel)(Params...), int grid, size_t smem,
-                                      cudaStream_t stream, Args... args)
-{
-    return launch_kernel_block(kernel, static_cast<size_t>(grid), kThreads, smem, stream, args...);
 }
 
 template <typename... Params, typename... Args>
@@ -527,17 +507,6 @@ __device__ __forceinline__ void dequantize_lane(Codes<DT> c, float s,
         v[4 * k + 2] = __fmul_rn(hi.x, s);
         v[4 * k + 3] = __fmul_rn(hi.y, s);
     }
-}
-
-// One thread's bulk copy of `bytes` from shared to global memory; its
-// completion is tracked with commit / wait groups.
-__device__ __forceinline__ void bulk_store(void *gdst, const void *ssrc, uint32_t bytes)
-{
-    if (!LPC_WRITE_OK(gdst, bytes))
-        return;
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst),
-                 "r"(static_cast<uint32_t>(__cvta_generic_to_shared(ssrc))), "r"(bytes)
-                 : "memory");
 }
 
 // Number of valid elements of a lane whose first element is e0.

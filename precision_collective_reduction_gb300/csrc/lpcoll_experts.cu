@@ -8,6 +8,7 @@
 // entry outside [0, nrows) counts as "no row": nothing is read or written for
 // it. Rows that no slot uses are written as zeros by the first CTAs of the same
 // launch.
+#include "lpcoll_dda.cuh"
 #include "lpcoll_layers.cuh"
 #include "lpcoll_wide.cuh"
 

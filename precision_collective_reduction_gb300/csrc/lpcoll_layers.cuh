@@ -152,6 +152,44 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// Launches as launch_kernel does, with CTAs of any size; `cluster` CTAs form a
+// thread-block cluster (1: none). Internal linkage for the same reason.
+template <typename... Params, typename... Args>
+static cudaError_t launch_kernel_cluster(void (*kernel)(Params...), size_t grid, int threads,
+                                         int cluster, size_t smem, cudaStream_t stream,
+                                         Args... args)
+{
+#ifdef LPCOLL_DEBUG_BOUNDS
+    const cudaError_t de = cudaMemcpyToSymbolAsync(g_debug_ranges, &debug_pending(),
+                                                   sizeof(DebugRanges), 0,
+                                                   cudaMemcpyHostToDevice, stream);
+    if (de != cudaSuccess)
+        return de;
+#endif
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename... Params, typename... Args>
+static cudaError_t launch_kernel_block(void (*kernel)(Params...), size_t grid, int threads,
+                                       size_t smem, cudaStream_t stream, Args... args)
+{
+    return launch_kernel_cluster(kernel, grid, threads, 1, smem, stream, args...);
+}
+
 // -- launchers (one translation unit each; called by lpcoll_layers_api.cu) --
 
 struct RouteArgs {

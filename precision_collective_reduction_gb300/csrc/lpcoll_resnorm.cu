@@ -27,11 +27,10 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kSms = 152;
-// A thread holds kElems = 8 or 16 columns. An SM holds two CTAs of kThreadsTwo
-// threads, with several teams if the rows are short, or one of kThreadsOne, at
-// 64 or 128 registers a thread.
+// A thread holds kElems = 8 or 16 columns, at 64 or 128 registers, so that an SM
+// holds kThreadsOne threads: a CTA, or several smaller ones. Short rows share a
+// CTA of up to half as many.
 template <int kElems> constexpr int kThreadsOne = 8192 / kElems;
-template <int kElems> constexpr int kThreadsTwo = 4096 / kElems;
 constexpr int kWideThreads = 1024;
 constexpr int kMaxWarps = kWideThreads / 32;
 
@@ -47,6 +46,7 @@ enum Mode { kGeneral, kPlain, kWide };
 
 constexpr int kMaxStages = 4;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxCtas = 3;  // per SM
 
 // How rows are dealt out: `threads` lanes of each of `cluster` CTAs share a
 // row, `packs` accesses of it per CTA; a CTA has `groups` such teams and a
@@ -784,11 +784,11 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
 }
 
 // Column sums of the workspace: a CTA adds 32 columns of one of the two sums.
-// 32 threads per column take every 32nd CTA's part, all in flight at once (up to
-// kColumnParts), and a warp adds up a column's 32.
-constexpr int kColumnParts = 2 * kSms / 32 + 1;  // of at most 2 CTAs per SM
+// 32 threads per column take every 32nd CTA's part, all in flight at once (kPer
+// of them, for as many CTAs per SM), and a warp adds up a column's 32.
+constexpr int kPer = (kSms + 31) / 32;
 
-template <int DT>
+template <int DT, int kPerSm>
 __global__ void __launch_bounds__(1024)
 norm_column_sums_kernel(const __grid_constant__ NormArgs a, int parts, int column_ctas)
 {
@@ -802,9 +802,10 @@ norm_column_sums_kernel(const __grid_constant__ NormArgs a, int parts, int colum
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int first = (blockIdx.x % column_ctas) * 32;
     const float *p = a.partial + static_cast<size_t>(which) * parts * a.hidden + first + lane;
-    float v[kColumnParts];
+    constexpr int kParts = kPer * kPerSm;
+    float v[kParts];
 #pragma unroll
-    for (int i = 0; i < kColumnParts; ++i) {
+    for (int i = 0; i < kParts; ++i) {
         const int q = i * 32 + warp;
         v[i] = q < parts && first + lane < a.hidden
                    ? load_f32(p + static_cast<size_t>(q) * a.hidden)
@@ -812,7 +813,7 @@ norm_column_sums_kernel(const __grid_constant__ NormArgs a, int parts, int colum
     }
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kColumnParts; ++i)
+    for (int i = 0; i < kParts; ++i)
         sum += v[i];
     red[warp][lane] = sum;
     __syncthreads();
@@ -846,8 +847,9 @@ struct Plan {
     size_t smem;  // dynamic shared memory of a CTA
 };
 
-// Shared memory of the rings of a CTA, for one or two CTAs per SM.
-constexpr size_t kSmemOne = 224 * 1024, kSmemTwo = 110 * 1024;
+// Shared memory of the rings of a CTA, for one to kMaxCtas CTAs per SM.
+constexpr size_t kSmem[kMaxCtas] = {224 * 1024, 110 * 1024, 72 * 1024};
+constexpr size_t kSmemOne = kSmem[0];
 
 // A row is one CTA's, or, where there are few tokens or the row does not fit
 // one, a cluster's. 16 columns a thread halve what a row costs besides its
@@ -879,19 +881,20 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
     d.cluster = cluster;
     d.packs = ((hidden + kn - 1) / kn + cluster - 1) / cluster;
     d.threads = round_up((d.packs + p.elems / kn - 1) / (p.elems / kn), 32);
-    const int share = p.elems == 8 ? kThreadsTwo<8> : kThreadsTwo<16>;
-    d.groups = cluster > 1 || d.threads * 2 > share ? 1 : share / d.threads;
+    const int room = p.elems == 8 ? kThreadsOne<8> : kThreadsOne<16>;
+    d.groups = cluster > 1 || d.threads * 4 > room ? 1 : room / 2 / d.threads;
     p.even = width == 16 && hidden % kn == 0 && d.packs * cluster * kn == hidden &&
              d.packs % (32 * (p.elems / kn)) == 0;
-    const bool two = d.threads * d.groups <= share;
+    int per_sm = p.wide ? 1 : room / (d.threads * d.groups);
+    per_sm = per_sm < 1 ? 1 : (per_sm > kMaxCtas ? kMaxCtas : per_sm);
     const size_t steps = (tokens + d.groups - 1) / d.groups;
-    const size_t most = static_cast<size_t>(kSms) * (two ? 2 : 1) / cluster;
+    const size_t most = static_cast<size_t>(kSms) * per_sm / cluster;
     p.ctas = static_cast<int>(steps < most ? steps : most);
     const size_t stage =
         static_cast<size_t>(row_part_bytes(width, d.packs, d.threads, p.elems)) * streams *
         d.groups;
     // as many rows under way as fit, and no more than a team has
-    size_t stages = (two ? kSmemTwo : kSmemOne) / stage;
+    size_t stages = kSmem[per_sm - 1] / stage;
     const size_t rows = (steps + p.ctas - 1) / p.ctas;
     stages = stages > kMaxStages ? kMaxStages : stages;
     stages = stages > rows ? rows : stages;
@@ -961,6 +964,16 @@ cudaError_t forward_dt(const NormArgs &a, cudaStream_t st)
                        a, p, streams, st);
 }
 
+template <int DT> cudaError_t column_sums(const NormArgs &a, int parts, cudaStream_t st)
+{
+    static_assert(kMaxCtas == 3, "one kernel per number of CTAs per SM");
+    const int ctas = (a.hidden + 31) / 32;
+    const auto kernel = parts <= kSms ? norm_column_sums_kernel<DT, 1>
+                                      : (parts <= 2 * kSms ? norm_column_sums_kernel<DT, 2>
+                                                           : norm_column_sums_kernel<DT, 3>);
+    return launch_kernel_block(kernel, static_cast<size_t>(2) * ctas, 1024, 0, st, a, parts, ctas);
+}
+
 }  // namespace
 
 int norm_backward_parts(size_t tokens, size_t hidden, int dtype)
@@ -997,10 +1010,8 @@ cudaError_t launch_residual_norm_backward(const NormArgs &args, cudaStream_t st)
     }
     if (!sums)
         return cudaSuccess;
-    const int ctas = (a.hidden + 31) / 32;
-    return launch_kernel_block(a.dtype == LPCOLL_F32 ? norm_column_sums_kernel<LPCOLL_F32>
-                                                     : norm_column_sums_kernel<LPCOLL_BF16>,
-                               static_cast<size_t>(2) * ctas, 1024, 0, st, a, parts, ctas);
+    return a.dtype == LPCOLL_F32 ? column_sums<LPCOLL_F32>(a, parts, st)
+                                 : column_sums<LPCOLL_BF16>(a, parts, st);
 }
 
 }  // namespace lpc

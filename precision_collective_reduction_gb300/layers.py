@@ -21,23 +21,28 @@ MAX_TOPK = 32
 MAX_HIDDEN = 16384
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
+_SORT_ONE_CTA = 2048  # slots that expert_sort takes without scratch memory
 # host arrays of 0..16 device pointers
 _POINTERS = [ctypes.c_void_p * n for n in range(B.MAX_RANKS + 1)]
 
 torch = None  # imported by the first call, as everywhere in the binding
-_raw_stream = None
+_raw_device = _raw_stream = None
 _DTYPE = {}
 
 
 def _device():
     """Index of the current CUDA device, which every call runs on."""
-    global torch, _raw_stream
+    global torch, _raw_device, _raw_stream
     if torch is None:
-        torch = B._torch()
-        # the current stream's handle without a Stream object around it
-        _raw_stream = torch._C._cuda_getCurrentRawStream
-        _DTYPE.update({torch.float32: B.F32, torch.bfloat16: B.BF16})
-    return torch.cuda.current_device()
+        t = B._torch()
+        t.cuda.current_device()  # initializes CUDA, or says why not
+        # the same without that check, and the current stream's handle without
+        # a Stream object around it
+        _raw_device = t._C._cuda_getDevice
+        _raw_stream = t._C._cuda_getCurrentRawStream
+        _DTYPE.update({t.float32: B.F32, t.bfloat16: B.BF16})
+        torch = t
+    return _raw_device()
 
 
 def _ptr(t, what, dtype, shape, device, rank=None):
@@ -175,7 +180,7 @@ def expert_sort(ids, nexperts, slot_row, row_slot, offsets, counts, capacity=0,
          _ptr(offsets, "offsets", i32, (nexperts + 1,), dev),
          _ptr(counts, "counts", i32, (nexperts,), dev))
     L = B.lib()
-    need = L.expert_sort_workspace_bytes(T * K, nexperts)
+    need = L.expert_sort_workspace_bytes(T * K, nexperts) if T * K > _SORT_ONE_CTA else 0
     wp, wn, _keep = _scratch(workspace, need, stream, dev)
     B._check(L.expert_sort(p[0], T * K, nexperts, capacity, p[1], p[2], p[3], p[4], wp, wn,
                            _stream(stream, dev)), "expert_sort")

@@ -555,24 +555,29 @@ def test_graph_capture():
     ids, wt = e(T, K, dtype=torch.int32), e(T, K, dtype=torch.float32)
     m = (e(T, K, dtype=torch.int32), e(T * K, dtype=torch.int32), e(E + 1, dtype=torch.int32),
          e(E, dtype=torch.int32))
-    rows, y = e(T * K, H), e(T, H)
+    rows, y, xo, n, dx, dh = e(T * K, H), e(T, H), e(T, H), e(T, H), e(T, H), e(T, H)
+    w, dw = torch.ones(H, dtype=torch.bfloat16, device="cuda"), e(H, dtype=torch.float32)
 
     def step():
         pcr.expert_route(logits, ids, wt, renormalize=True)
         pcr.expert_sort(ids, E, *m)
         pcr.expert_dispatch(x, m[0], m[1], rows)
         pcr.expert_combine(m[0], y, rows, weights=wt)
+        pcr.residual_norm([y] * 9, x, xo, n, w_post=w, w_pre=w)
+        pcr.residual_norm_backward(x, n, y, xo, dx, dh, w_post=w, w_pre=w, dw_post=dw)
     step()
     torch.cuda.synchronize()
-    want = y.clone()
+    made = (ids, wt, *m, rows, y, xo, n, dx, dh, dw)
+    want = [t.clone() for t in made]
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         step()
-    for t in (ids, wt, *m, rows, y):
+    for t in made:
         t.zero_()
     graph.replay()
     torch.cuda.synchronize()
-    assert torch.equal(y, want)
+    for t, v in zip(made, want):
+        assert torch.equal(t, v)
 
 
 def test_refusals():
