@@ -580,6 +580,52 @@ def test_graph_capture():
         assert torch.equal(t, v)
 
 
+def test_scratch_memory_of_threads_and_streams():
+    # gradients of different sizes from several threads, on the default stream
+    # and on others, with and without a workspace: the same bits as alone
+    import threading
+    sizes = [(700, 1024), (40, 512), (1500, 264), (9, 4096)]
+    cases, want = [], []
+    for T, H in sizes:
+        g = rng(T, H, 77)
+        t = [dev(g.normal(size=(T, H)), "bf16") for _ in range(4)]
+        w = dev(1 + 0.1 * g.normal(size=H), "bf16")
+        cases.append((t, w))
+
+    def run(i, stream=None, workspace=None):
+        (d, n, h, x), w = cases[i]
+        out = [torch.zeros_like(x), torch.zeros_like(x),
+               *(torch.zeros(x.shape[1], device="cuda") for _ in range(2))]
+        if stream is not None:
+            torch.cuda.synchronize()
+        pcr.residual_norm_backward(d, n, h, x, out[0], out[1], w_post=w, w_pre=w, dw_post=out[2],
+                                   dw_pre=out[3], stream=stream, workspace=workspace)
+        return out
+    for i in range(len(sizes)):
+        need = pcr.residual_norm_backward_workspace_bytes(*sizes[i], pcr.BF16)
+        want.append(run(i, workspace=torch.empty(need, dtype=torch.uint8, device="cuda")))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            side = torch.cuda.Stream()
+            for k in range(30):
+                j = (i + k) % len(sizes)
+                got = run(j, stream=side if k % 3 == 0 else None)
+                torch.cuda.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[j])):
+                    wrong.append((i, k))
+        except Exception as e:  # reported by the main thread
+            wrong.append(repr(e))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=120)
+    assert not wrong
+
+
 def test_refusals():
     T, K, E, H = 4, 2, 3, 16
     f = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
