@@ -910,7 +910,8 @@ template <class Kernel>
 cudaError_t launch_plan(Kernel kernel, const NormArgs &a, const Plan &p, int streams,
                         cudaStream_t st)
 {
-    if (p.smem > 48 * 1024) {
+    // 48 KB hold the kernels' static shared memory too
+    if (p.smem > 44 * 1024) {
         // always the same value: calls of several threads must not undo each other's
         const cudaError_t e = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemOne));

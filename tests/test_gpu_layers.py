@@ -434,7 +434,8 @@ def test_gate_of_one_dimension_where_both_fit():
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("T,H", [(700, 1025), (1300, 130), (400, 1024), (310, 8704), (160, 16384),
-                                 (5000, 64), (311, 2051), (160, 12288)])
+                                 (5000, 64), (311, 2051), (160, 12288), (100, 6000),
+                                 (100, 6100)])
 @pytest.mark.parametrize("kind,post,pre", [("channel", True, True), ("token", False, True),
                                            ("full", True, True)])
 def test_norms_of_many_tokens(lib, dt, T, H, kind, post, pre):
