@@ -883,16 +883,21 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
     d.threads = round_up((d.packs + p.elems / kn - 1) / (p.elems / kn), 32);
     const int room = p.elems == 8 ? kThreadsOne<8> : kThreadsOne<16>;
     d.groups = cluster > 1 || d.threads * 4 > room ? 1 : room / 2 / d.threads;
+    // one row of each of a CTA's teams, in all streams
+    const size_t row =
+        static_cast<size_t>(row_part_bytes(width, d.packs, d.threads, p.elems)) * streams;
+    while (d.groups > 1 && row * d.groups > kSmem[1])
+        d.groups /= 2;
     p.even = width == 16 && hidden % kn == 0 && d.packs * cluster * kn == hidden &&
              d.packs % (32 * (p.elems / kn)) == 0;
     int per_sm = p.wide ? 1 : room / (d.threads * d.groups);
     per_sm = per_sm < 1 ? 1 : (per_sm > kMaxCtas ? kMaxCtas : per_sm);
+    while (per_sm > 1 && row * d.groups > kSmem[per_sm - 1])
+        --per_sm;
     const size_t steps = (tokens + d.groups - 1) / d.groups;
     const size_t most = static_cast<size_t>(kSms) * per_sm / cluster;
     p.ctas = static_cast<int>(steps < most ? steps : most);
-    const size_t stage =
-        static_cast<size_t>(row_part_bytes(width, d.packs, d.threads, p.elems)) * streams *
-        d.groups;
+    const size_t stage = row * d.groups;
     // as many rows under way as fit, and no more than a team has
     size_t stages = kSmem[per_sm - 1] / stage;
     const size_t rows = (steps + p.ctas - 1) / p.ctas;

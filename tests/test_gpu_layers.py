@@ -445,7 +445,8 @@ def test_norms_of_many_tokens(lib, dt, T, H, kind, post, pre):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("T,H", [(3, 8192), (200, 4096), (40, 777), (2, 16384)])
+@pytest.mark.parametrize("T,H", [(3, 8192), (200, 4096), (40, 777), (2, 16384), (170, 768),
+                                 (40, 768), (9, 1)])
 @pytest.mark.parametrize("kind", [None, "full"])
 def test_residual_norm_of_16_ranks(lib, dt, T, H, kind):
     a, b, eps = (float(np.float32(v)) for v in (0.9, 0.7, 1e-5))
