@@ -7,7 +7,12 @@
 // tokens and reads or writes a token's row once for its K choices. A map
 // entry outside [0, nrows) counts as "no row": nothing is read or written for
 // it. Rows that no slot uses are written as zeros by the first CTAs of the same
-// launch.
+// launch (last, their long runs of stores were its tail).
+//
+// Measured on one GB300, 8192 tokens and 4 rows of 8192 BF16 each: dispatch 99 us
+// and combine 97 us (6.7 TB/s), as FP8 payloads 76 and 86 us; the gradient of
+// 4001 tokens and 8 rows of 4100 FP32 178 us (6.2 TB/s). DRAM bounds all of them
+// but the FP8 combine (latency of its short row pieces).
 #include "lpcoll_dda.cuh"
 #include "lpcoll_layers.cuh"
 #include "lpcoll_wide.cuh"
@@ -289,7 +294,8 @@ __device__ __forceinline__ void store_codes16(uint8_t *p, int n, const uint32_t 
 __device__ __forceinline__ size_t row_blocks(size_t hidden) { return (hidden + kBlock - 1) / kBlock; }
 
 // Low precision: a lane quantizes 16 consecutive elements, 8 lanes a block of
-// 128, once per token, and writes codes and scales into the K rows.
+// 128, once per token, and writes codes and scales into the K rows. (Quantizing
+// takes 68% of the issue slots, so it must not be done per row.)
 template <int DT, int W>
 __global__ void __launch_bounds__(kThreads)
 dispatch_lp_kernel(const RowsArgs a, const Cut cut, unsigned clear)
@@ -416,8 +422,8 @@ __device__ __forceinline__ uint4 load_row_codes(const RowsArgs &a, int row, size
 }
 
 // The same from FP8 payloads, with fl(weight * scale) as the factor of a code's
-// value. A lane holds 16 consecutive elements; a warp's results go through
-// shared memory, so that its stores are consecutive.
+// value. A lane holds 16 consecutive elements (with 8, 118 us instead of 93); a
+// warp's results go through shared memory, so that its stores are consecutive.
 template <int DT, int W>
 __global__ void __launch_bounds__(kThreads) combine_lp_kernel(const RowsArgs a, const Cut cut)
 {
@@ -482,7 +488,9 @@ constexpr int kBackThreads = 1024, kBackShort = 128;
 // The lanes of a token go through its row in batches; with dy's batch in
 // registers they take one choice after the other: the row's batch is read,
 // drows = w dy written and the partial products of dw = <row, dy> added up,
-// over a warp with shuffles, over the warps in shared memory at the end.
+// over a warp with shuffles, over the warps in shared memory at the end. dy is
+// read once for all choices. A second choice's batch in flight took 124
+// registers and 203 instead of 190 us.
 template <int DT, int W, int B, int C>
 __global__ void __launch_bounds__(B == 1 ? kThreads : kBackThreads)
 combine_backward_kernel(const RowsArgs a, const Cut cut, unsigned clear)
