@@ -879,7 +879,8 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
     while (!p.wide && cluster < kMaxCluster &&
            (static_cast<size_t>(hidden) * width / kn / cluster + 2048) * streams > kSmemOne)
         cluster *= 2;
-    const bool light = !gradient && streams <= 2 && hidden <= kRow;
+    const bool light =
+        !gradient && streams <= 2 && hidden <= kRow && dtype == LPCOLL_BF16;
     p.elems = hidden <= 256 || tokens <= kSms || light ? 8 : 16;
     Deal &d = p.deal;
     d.cluster = cluster;

@@ -11,8 +11,8 @@
 // not in the rest, is chosen again with both parts apart. A lane sorts its
 // numbers once, and the winner of a choice moves up its list. Every sum is
 // FP32 in a fixed order. Measured on one GB300, 32768 tokens of 256 FP32 logits,
-// 8 choices: 17.7 us (442 instructions per token, 72% issue active; with keys and
-// indexes apart 30 us), the gradient 12.2 us (0.84 of the copy rate).
+// 8 choices: 16.6 us (some 400 instructions per token, 72% issue active; with keys
+// and indexes apart 30 us), the gradient 12.2 us (0.84 of the copy rate).
 #include "lpcoll_layers.cuh"
 
 namespace lpc {
@@ -188,10 +188,18 @@ __device__ __noinline__ int choose_apart(const void *logits, size_t t, int exper
     return my_id;
 }
 
-template <int DT, int PER>
+// MOST: choices that the kernel is made for. For few (kFew) the steps are unrolled
+// and a lane's list is kept, and moved up, only as far as later steps can reach
+// (32768 tokens of 256 FP32 17.7 -> 16.6 us, 16384 of 384 BF16 14.5 -> 11.6); with
+// 4 logits a lane or fewer there is nothing to save.
+constexpr int kFew = 8;
+
+template <int DT, int PER, int MOST>
 __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a)
 {
     wait_prior_grid();
+    // the number after the last choice tells whether that one was sure
+    constexpr int L = PER < MOST + 1 ? PER : MOST + 1;
     const int lane = threadIdx.x & 31;
     const size_t t = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
     if (t >= a.tokens)
@@ -207,18 +215,25 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a)
         list[i] = (logit_key(x[i]) & ~kIndexBits) | (kIndexBits - expert_of<DT, PER>(i, lane));
     }
     sort_down<0, PER>(list);
-    uint32_t mine = 0, most = 0;
-    for (int j = 0; j < a.topk; ++j) {
-        most = __reduce_max_sync(kAll, list[0]);
-        if (most <= kKeyNone)
-            break;
-        if (lane == j)
+    uint32_t mine = 0;
+    const auto step = [&](int j) {
+        const uint32_t most = __reduce_max_sync(kAll, list[0]);
+        if (lane == j && most > kKeyNone)
             mine = most;
         const bool won = list[0] == most;
 #pragma unroll
-        for (int i = 0; i + 1 < PER; ++i)
-            list[i] = won ? list[i + 1] : list[i];
-        list[PER - 1] = won ? 0u : list[PER - 1];
+        for (int i = 0; i < L; ++i)
+            if (MOST != kFew || i < MOST - j)
+                list[i] = won ? (i + 1 < L ? list[i + 1] : 0u) : list[i];
+    };
+    if constexpr (MOST == kFew) {
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)
+            if (j < a.topk)
+                step(j);
+    } else {
+        for (int j = 0; j < a.topk; ++j)
+            step(j);
     }
     int my_id = mine != 0 ? static_cast<int>(kIndexBits - (mine & kIndexBits)) : -1;
     const auto logit_of = [&](int id) {
@@ -582,7 +597,12 @@ cudaError_t route_per(const RouteArgs &a, bool backward, cudaStream_t st)
     if (backward)
         return launch_kernel_block(route_backward_kernel<DT, PER>,
                                    token_ctas(a.tokens, kPairs<PER>), kThreads, 0, st, a);
-    return launch_kernel_block(route_kernel<DT, PER>, token_ctas(a.tokens, 1), kThreads, 0, st, a);
+    const size_t ctas = token_ctas(a.tokens, 1);
+    if constexpr (PER >= kFew) {
+        if (a.topk <= kFew)
+            return launch_kernel_block(route_kernel<DT, PER, kFew>, ctas, kThreads, 0, st, a);
+    }
+    return launch_kernel_block(route_kernel<DT, PER, LPCOLL_MAX_TOPK>, ctas, kThreads, 0, st, a);
 }
 
 // Logits per lane: the smallest power of two that holds the experts.
