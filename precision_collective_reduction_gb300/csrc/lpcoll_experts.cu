@@ -480,9 +480,11 @@ __global__ void __launch_bounds__(kThreads) combine_lp_kernel(const RowsArgs a, 
 }
 
 // Accesses of a row and choices that a lane of the gradient kernel has in
-// flight: kBackBatch of one choice, or, for rows of at most one access per lane
-// of 128, one access of kBackChoices choices.
-constexpr int kBackBatch = 4, kBackChoices = 4;
+// flight: kBackBatch of one choice (narrow ones are more, so that a lane's batch
+// is 64 or 32 bytes), or, for rows of at most one access per lane of 128, one
+// access of kBackChoices choices.
+template <int W> constexpr int kBackBatch = W == 16 ? 4 : 16;
+constexpr int kBackChoices = 4;
 constexpr int kBackThreads = 1024, kBackShort = 128;
 
 // The lanes of a token go through its row in batches; with dy's batch in
@@ -653,7 +655,7 @@ cudaError_t combine_backward_dt(const RowsArgs &a, cudaStream_t st)
     constexpr int kN = Pack<DT, W>::kN;
     const size_t packs = (a.hidden + kN - 1) / kN;
     const bool brief = packs <= kBackShort;
-    const size_t lanes = brief ? packs : (packs + kBackBatch - 1) / kBackBatch;
+    const size_t lanes = brief ? packs : (packs + kBackBatch<W> - 1) / kBackBatch<W>;
     Cut c;
     c.segs = 1;
     c.threads = static_cast<int>(lanes < 32 ? 32
@@ -662,7 +664,7 @@ cudaError_t combine_backward_dt(const RowsArgs &a, cudaStream_t st)
     c.tokens = c.threads > kThreads ? 1 : kThreads / c.threads;
     const size_t clear = clear_ctas(a.hidden > 0 ? a.nrows : 0, c.block());
     return launch_kernel_block(brief ? combine_backward_kernel<DT, W, 1, kBackChoices>
-                                     : combine_backward_kernel<DT, W, kBackBatch, 1>,
+                                     : combine_backward_kernel<DT, W, kBackBatch<W>, 1>,
                                clear + c.ctas(a.tokens), c.block(), 0, st, a, c,
                                static_cast<unsigned>(clear));
 }
