@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads) combine_lp_kernel(const RowsArgs a, 
 // flight: kBackBatch of one choice (narrow ones are more, so that a lane's batch
 // is 64 or 32 bytes), or, for rows of at most one access per lane of 128, one
 // access of kBackChoices choices.
-template <int W> constexpr int kBackBatch = W == 16 ? 4 : 16;
+template <int W> constexpr int kBackBatch = W == 16 ? 4 : (W == 8 ? 8 : 16);
 constexpr int kBackChoices = 4;
 constexpr int kBackThreads = 1024, kBackShort = 128;
 

@@ -4,9 +4,8 @@
 //
 // Rows of these operators are `hidden` elements long and follow one another
 // without padding, so a row starts on a 16-byte boundary only if its length
-// in bytes is a multiple of 16. Each kernel exists for accesses of W = 16
-// bytes, of 4 bytes (FP32 rows of any length, BF16 rows of even length) and
-// of 2 bytes (BF16 rows of odd length).
+// in bytes is a multiple of 16. Each kernel exists for accesses of W = 16, 8
+// and 4 bytes, and of 2 bytes (BF16 rows of odd length).
 #pragma once
 
 #include "lpcoll_device.cuh"
@@ -18,6 +17,10 @@ template <int DT, int W> struct Pack;
 template <int DT> struct Pack<DT, 16> {
     using Raw = uint4;
     static constexpr int kN = Fmt<DT>::kVec;
+};
+template <int DT> struct Pack<DT, 8> {
+    using Raw = uint2;
+    static constexpr int kN = Fmt<DT>::kVec / 2;
 };
 template <int DT> struct Pack<DT, 4> {
     using Raw = uint32_t;
@@ -36,18 +39,19 @@ inline size_t dtype_bytes(int dtype) { return dtype == LPCOLL_F32 ? 4 : 2; }
 inline int row_width(size_t hidden, int dtype)
 {
     const size_t bytes = hidden * dtype_bytes(dtype);
-    return bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
+    return bytes % 16 == 0 ? 16 : (bytes % 8 == 0 ? 8 : (bytes % 4 == 0 ? 4 : 2));
 }
 
 // fn<dtype, width>(...) for a call's dtype and row length.
+#define LPC_BY_WIDTH(fn, DT, width, ...)                                                     \
+    ((width) == 16 ? fn<DT, 16>(__VA_ARGS__)                                                 \
+                   : ((width) == 8 ? fn<DT, 8>(__VA_ARGS__) : fn<DT, 4>(__VA_ARGS__)))
 #define LPC_BY_ROW(fn, dtype, hidden, ...)                                                   \
     ((dtype) == LPCOLL_F32                                                                   \
-         ? (row_width(hidden, dtype) == 16 ? fn<LPCOLL_F32, 16>(__VA_ARGS__)                 \
-                                           : fn<LPCOLL_F32, 4>(__VA_ARGS__))                 \
-         : (row_width(hidden, dtype) == 16                                                   \
-                ? fn<LPCOLL_BF16, 16>(__VA_ARGS__)                                           \
-                : (row_width(hidden, dtype) == 4 ? fn<LPCOLL_BF16, 4>(__VA_ARGS__)           \
-                                                 : fn<LPCOLL_BF16, 2>(__VA_ARGS__))))
+         ? LPC_BY_WIDTH(fn, LPCOLL_F32, row_width(hidden, dtype), __VA_ARGS__)               \
+         : (row_width(hidden, dtype) == 2                                                    \
+                ? fn<LPCOLL_BF16, 2>(__VA_ARGS__)                                            \
+                : LPC_BY_WIDTH(fn, LPCOLL_BF16, row_width(hidden, dtype), __VA_ARGS__)))
 
 template <int DT, int W>
 __device__ __forceinline__ typename Pack<DT, W>::Raw load_pack(const void *base, size_t e0)
@@ -74,6 +78,18 @@ __device__ __forceinline__ void widen_pack(typename Pack<DT, W>::Raw v,
 {
     if constexpr (W == 16) {
         widen<DT>(v, x);
+    } else if constexpr (W == 8) {
+        const uint32_t w[2] = {v.x, v.y};
+        if constexpr (DT == LPCOLL_F32) {
+            x[0] = __uint_as_float(w[0]);
+            x[1] = __uint_as_float(w[1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                x[2 * j] = __uint_as_float(w[j] << 16);
+                x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        }
     } else if constexpr (DT == LPCOLL_F32) {
         x[0] = __uint_as_float(v);
     } else {
@@ -89,6 +105,15 @@ narrow_pack(const float (&x)[Pack<DT, W>::kN])
 {
     if constexpr (W == 16) {
         return narrow<DT>(x);
+    } else if constexpr (W == 8) {
+        if constexpr (DT == LPCOLL_F32) {
+            return make_uint2(__float_as_uint(x[0]), __float_as_uint(x[1]));
+        } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(x[2], x[3]);
+            return make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                              *reinterpret_cast<const uint32_t *>(&hi));
+        }
     } else if constexpr (DT == LPCOLL_F32) {
         return __float_as_uint(x[0]);
     } else if constexpr (W == 4) {

@@ -275,7 +275,7 @@ __device__ __forceinline__ void store_vec_of(void *base, size_t e0,
     store_pack<DT, W>(base, e0, narrow_pack<DT, W>(x.v));
 }
 
-// W (16 or 4) bytes from global into this thread's place in shared memory.
+// W (16, 8 or 4) bytes from global into this thread's place in shared memory.
 template <int W>
 __device__ __forceinline__ void copy_async(void *dst, const void *src)
 {
@@ -288,6 +288,8 @@ __device__ __forceinline__ void copy_async(void *dst, const void *src)
     const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
     if constexpr (W == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else if constexpr (W == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
 }
