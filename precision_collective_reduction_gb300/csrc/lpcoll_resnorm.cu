@@ -38,9 +38,9 @@ template <int kElems> constexpr int kThreadsOne = 8192 / kElems;
 constexpr int kWideThreads = 1024;
 constexpr int kMaxWarps = kWideThreads / 32;
 
-// Forms of both kernels. kPlain is for calls in which every thread has all its
-// columns, both norms are there, one rank's h, no full gate and, in the
-// gradient, dx_out: without the conditions around every access the compiler
+// Forms of both kernels. kPlain is for calls without clusters in which every
+// thread has all its columns, both norms are there, one rank's h, no full gate
+// and, in the gradient, dx_out: without the conditions around every access the compiler
 // interleaves a thread's accesses (gradient of 8192 x 8192 BF16 143 -> 134 us).
 // kWide is for the forward pass of rows of more than 8192 columns, in a CTA of
 // 1024 threads with 16 columns each at 64 registers a thread, the weights from
@@ -68,8 +68,8 @@ __device__ __forceinline__ unsigned cluster_rank()
 
 __device__ __forceinline__ void cluster_barrier()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\t"
+                 "barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // The float at `p` of this CTA's shared memory in CTA `rank` of the cluster.
@@ -84,15 +84,18 @@ __device__ __forceinline__ float cluster_load(const float *p, unsigned rank)
 }
 
 // Waits for the threads of this team: of all CTAs of its cluster, of its CTA,
-// or of its part of a CTA (barrier 1 + team of the CTA).
-__device__ __forceinline__ void team_barrier(const Deal &deal)
+// or of its part of a CTA (barrier 1 + team of the CTA). Not the ".aligned" forms
+// (bar.sync is one): they count a warp's parts as whole warps where the compiler
+// lets its lanes, of which some have no columns, run apart. kAlone: there is no
+// cluster.
+template <bool kAlone> __device__ __forceinline__ void team_barrier(const Deal &deal)
 {
-    if (deal.cluster > 1)
+    if (!kAlone && deal.cluster > 1)
         cluster_barrier();
     else if (deal.groups == 1)
         __syncthreads();
     else  // teams of 64 threads or more, 8 of them at most
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / deal.threads),
+        asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / deal.threads),
                      "r"(deal.threads)
                      : "memory");
 }
@@ -105,7 +108,7 @@ template <int N> constexpr int kSplit = N == 1 ? 1 : (N == 2 ? 2 : 8);
 // one: 9 shuffles for 6 values instead of 30); the warps' sums then meet in
 // `red`. The caller alternates between two `red`, so that one barrier per sum
 // is enough. first_warp: the team's first in its CTA.
-template <int N>
+template <bool kAlone, int N>
 __device__ __forceinline__ void team_sums(float (&v)[N], float (*red)[8], const Deal &deal,
                                           int first_warp)
 {
@@ -130,13 +133,13 @@ __device__ __forceinline__ void team_sums(float (&v)[N], float (*red)[8], const 
 #pragma unroll
     for (int m = P; m < 32; m <<= 1)
         sum += __shfl_xor_sync(kAll, sum, m);
-    if (warps > 1 || deal.cluster > 1) {
+    if (warps > 1 || (!kAlone && deal.cluster > 1)) {
         if (lane < P)
             red[threadIdx.x >> 5][lane] = sum;
         __syncwarp();
-        team_barrier(deal);
+        team_barrier<kAlone>(deal);
         sum = 0.0f;
-        if (deal.cluster == 1) {
+        if (kAlone || deal.cluster == 1) {
             for (int w = lane / P; w < warps; w += 32 / P)
                 sum += red[first_warp + w][lane % P];
         } else {
@@ -353,12 +356,14 @@ template <int DT, int W, int kElems, int kMode> struct Member {
         group = static_cast<int>(threadIdx.x) / deal.threads;
         const int id = static_cast<int>(threadIdx.x) - group * deal.threads;
         first_warp = group * (deal.threads >> 5);
-        const int part = deal.cluster > 1 ? static_cast<int>(cluster_rank()) * deal.packs : 0;
+        const bool alone = kMode == kPlain || deal.cluster == 1;
+        const int part = alone ? 0 : static_cast<int>(cluster_rank()) * deal.packs;
         const int p0 = (id >> 5) * NV * 32 + (id & 31);
         col0 = (part + p0) * kN;
         packs = min(deal.packs, (hidden + kN - 1) / kN - part) - p0;
-        step = static_cast<size_t>(gridDim.x / deal.cluster) * deal.groups;
-        t0 = static_cast<size_t>(blockIdx.x / deal.cluster) * deal.groups + group;
+        step = static_cast<size_t>(alone ? gridDim.x : gridDim.x / deal.cluster) * deal.groups;
+        t0 = static_cast<size_t>(alone ? blockIdx.x : blockIdx.x / deal.cluster) * deal.groups +
+             group;
         row_bytes = row_part_bytes(W, deal.packs, deal.threads, kElems);
         stage_bytes = row_bytes * streams;
         place = smem + static_cast<size_t>(group) * stage_bytes * deal.stages;
@@ -568,7 +573,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
     if (summed) {
         float s[1] = {me.t0 < a.tokens ? sum_ranks(me.t0, 0) : 0.0f};
         if (post) {
-            team_sums(s, red[1], deal, me.first_warp);
+            team_sums<kMode == kPlain>(s, red[1], deal, me.first_warp);
             r1 = inv_rms(s[0], per_hidden, a.eps);
         }
     }
@@ -596,7 +601,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
         me.ready(deal.stages - 1);
         float s[2] = {fold(sq), summed && t + me.step < a.tokens ? sum_ranks(t + me.step, stage) : 0.0f};
         if (post || pre)
-            team_sums(s, red[turn], deal, me.first_warp);
+            team_sums<kMode == kPlain>(s, red[turn], deal, me.first_warp);
         r1 = post ? inv_rms(s[1], per_hidden, a.eps) : 1.0f;
         if (pre) {
             const float r2 = inv_rms(s[0], per_hidden, a.eps);
@@ -607,7 +612,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
                                         mul(mul(r2, w_pre(c)), v[c]));
         }
     }
-    if (deal.cluster > 1)
+    if (kMode != kPlain && deal.cluster > 1)
         cluster_barrier();  // no CTA leaves while another reads its sums
 }
 
@@ -710,7 +715,7 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
         me.ready(deal.stages - 1);
         float s[6];
         row_sums(t, stage, s);
-        team_sums(s, red[turn], deal, me.first_warp);
+        team_sums<kMode == kPlain>(s, red[turn], deal, me.first_warp);
         const float r1 = post ? inv_rms(s[0], per_hidden, a.eps) : 1.0f;
         const float r2 = pre ? inv_rms(s[1], per_hidden, a.eps) : 0.0f;
         const float c2 = pre ? r2 * r2 * s[2] * per_hidden : 0.0f;
@@ -751,7 +756,7 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
         stage = stage + 1 == deal.stages ? 0 : stage + 1;
     }
     copy_wait(0);
-    if (deal.cluster > 1)
+    if (kMode != kPlain && deal.cluster > 1)
         cluster_barrier();  // no CTA leaves while another reads its sums
 
     // The CTA's sums over its tokens: the groups add theirs in order in shared
@@ -870,7 +875,7 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
     const int kn = width / static_cast<int>(dtype_bytes(dtype));
     constexpr int kRow = 8192;  // columns of the largest CTA but kWide's
     Plan p;
-    p.wide = !gradient && width == 16 && hidden > kRow && tokens > kSms &&
+    p.wide = !gradient && tokens > kSms && hidden > kRow && width == 16 &&
              static_cast<size_t>(hidden) * width / kn * streams <= kSmemOne;
     int cluster = hidden > kRow && !p.wide ? 2 : 1;
     // few tokens: a row over up to 8 CTAs, while there are SMs left and a CTA
@@ -883,12 +888,12 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
         cluster *= 2;
     const bool light =
         !gradient && streams <= 2 && hidden <= kRow && dtype == LPCOLL_BF16;
-    p.elems = hidden <= 256 || tokens <= kSms || light ? 8 : 16;
+    p.elems = !p.wide && (hidden <= 256 || tokens <= kSms || light) ? 8 : 16;
     Deal &d = p.deal;
     d.cluster = cluster;
     d.packs = ((hidden + kn - 1) / kn + cluster - 1) / cluster;
     d.threads = round_up((d.packs + p.elems / kn - 1) / (p.elems / kn), 32);
-    const int room = p.elems == 8 ? kThreadsOne<8> : kThreadsOne<16>;
+    const int room = p.wide ? kWideThreads : (p.elems == 8 ? kThreadsOne<8> : kThreadsOne<16>);
     d.groups = cluster > 1 || d.threads * 4 > room ? 1 : room / 2 / d.threads;
     // one row of each of a CTA's teams, in all streams
     const size_t row =
@@ -897,7 +902,7 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
         d.groups /= 2;
     p.even = width == 16 && hidden % kn == 0 && d.packs * cluster * kn == hidden &&
              d.packs % (32 * (p.elems / kn)) == 0;
-    int per_sm = p.wide ? 1 : room / (d.threads * d.groups);
+    int per_sm = room / (d.threads * d.groups);
     per_sm = per_sm < 1 ? 1 : (per_sm > kMaxCtas ? kMaxCtas : per_sm);
     while (per_sm > 1 && row * d.groups > kSmem[per_sm - 1])
         --per_sm;
@@ -947,7 +952,8 @@ cudaError_t backward_dt(const NormArgs &a, const Plan &p, cudaStream_t st)
     const bool full = a.gate_kind == LPCOLL_GATE_FULL;
     const int streams = full ? 5 : 4;
     if constexpr (W == 16) {
-        if (p.even && !full && a.w_post != nullptr && a.w_pre != nullptr && a.dx_out != nullptr)
+        if (p.even && p.deal.cluster == 1 && !full && a.w_post != nullptr && a.w_pre != nullptr &&
+            a.dx_out != nullptr)
             return launch_plan(p.elems == 8 ? residual_norm_backward_kernel<DT, W, 8, kPlain>
                                             : residual_norm_backward_kernel<DT, W, 16, kPlain>,
                                a, p, streams, st);
@@ -966,8 +972,8 @@ cudaError_t forward_dt(const NormArgs &a, cudaStream_t st)
     if constexpr (W == 16) {
         if (p.wide)
             return launch_plan(residual_norm_kernel<DT, W, 16, kWide>, a, p, streams, st);
-        if (p.even && !full && a.w_post != nullptr && a.w_pre != nullptr && a.nranks == 1 &&
-            a.h_sum == nullptr)
+        if (p.even && p.deal.cluster == 1 && !full && a.w_post != nullptr && a.w_pre != nullptr &&
+            a.nranks == 1 && a.h_sum == nullptr)
             return launch_plan(p.elems == 8 ? residual_norm_kernel<DT, W, 8, kPlain>
                                             : residual_norm_kernel<DT, W, 16, kPlain>,
                                a, p, streams, st);
