@@ -86,11 +86,10 @@ __device__ __forceinline__ float cluster_load(const float *p, unsigned rank)
 // Waits for the threads of this team: of all CTAs of its cluster, of its CTA,
 // or of its part of a CTA (barrier 1 + team of the CTA). Not the ".aligned" forms
 // (bar.sync is one): they count a warp's parts as whole warps where the compiler
-// lets its lanes, of which some have no columns, run apart. kAlone: there is no
-// cluster.
-template <bool kAlone> __device__ __forceinline__ void team_barrier(const Deal &deal)
+// lets its lanes, of which some have no columns, run apart.
+__device__ __forceinline__ void team_barrier(const Deal &deal)
 {
-    if (!kAlone && deal.cluster > 1)
+    if (deal.cluster > 1)
         cluster_barrier();
     else if (deal.groups == 1)
         __syncthreads();
@@ -108,7 +107,7 @@ template <int N> constexpr int kSplit = N == 1 ? 1 : (N == 2 ? 2 : 8);
 // one: 9 shuffles for 6 values instead of 30); the warps' sums then meet in
 // `red`. The caller alternates between two `red`, so that one barrier per sum
 // is enough. first_warp: the team's first in its CTA.
-template <bool kAlone, int N>
+template <int N>
 __device__ __forceinline__ void team_sums(float (&v)[N], float (*red)[8], const Deal &deal,
                                           int first_warp)
 {
@@ -133,13 +132,13 @@ __device__ __forceinline__ void team_sums(float (&v)[N], float (*red)[8], const 
 #pragma unroll
     for (int m = P; m < 32; m <<= 1)
         sum += __shfl_xor_sync(kAll, sum, m);
-    if (warps > 1 || (!kAlone && deal.cluster > 1)) {
+    if (warps > 1 || deal.cluster > 1) {
         if (lane < P)
             red[threadIdx.x >> 5][lane] = sum;
         __syncwarp();
-        team_barrier<kAlone>(deal);
+        team_barrier(deal);
         sum = 0.0f;
-        if (kAlone || deal.cluster == 1) {
+        if (deal.cluster == 1) {
             for (int w = lane / P; w < warps; w += 32 / P)
                 sum += red[first_warp + w][lane % P];
         } else {
@@ -332,8 +331,10 @@ __host__ __device__ constexpr int row_part_bytes(int width, int packs, int threa
 }
 
 // What a thread of a team works on: its warp's part of a row is kElems * 32
-// consecutive columns, access c of all lanes side by side.
-template <int DT, int W, int kElems, int kMode> struct Member {
+// consecutive columns, access c of all lanes side by side. kAlone: known to have
+// no cluster (for the plain gradient 132 against 135 us at 8192 x 8192 BF16; the
+// plain forward pass is compiled to a slower kernel with it, 168 against 161).
+template <int DT, int W, int kElems, int kMode, bool kAlone> struct Member {
     static constexpr int kN = Pack<DT, W>::kN;
     static constexpr int NV = kElems / kN;
     int group;         // team of the CTA
@@ -356,7 +357,7 @@ template <int DT, int W, int kElems, int kMode> struct Member {
         group = static_cast<int>(threadIdx.x) / deal.threads;
         const int id = static_cast<int>(threadIdx.x) - group * deal.threads;
         first_warp = group * (deal.threads >> 5);
-        const bool alone = kMode == kPlain || deal.cluster == 1;
+        const bool alone = kAlone || deal.cluster == 1;
         const int part = alone ? 0 : static_cast<int>(cluster_rank()) * deal.packs;
         const int p0 = (id >> 5) * NV * 32 + (id & 31);
         col0 = (part + p0) * kN;
@@ -506,7 +507,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
     __shared__ float red[2][kMaxWarps][8];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems, kMode> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
+    const Member<DT, W, kElems, kMode, false> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
     const bool post = kMode == kPlain || a.w_post != nullptr;
     const bool pre = kMode == kPlain || a.w_pre != nullptr;
     const bool full = kMode != kPlain && a.gate_kind == LPCOLL_GATE_FULL;
@@ -573,7 +574,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
     if (summed) {
         float s[1] = {me.t0 < a.tokens ? sum_ranks(me.t0, 0) : 0.0f};
         if (post) {
-            team_sums<kMode == kPlain>(s, red[1], deal, me.first_warp);
+            team_sums(s, red[1], deal, me.first_warp);
             r1 = inv_rms(s[0], per_hidden, a.eps);
         }
     }
@@ -601,7 +602,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, const Deal deal, int st
         me.ready(deal.stages - 1);
         float s[2] = {fold(sq), summed && t + me.step < a.tokens ? sum_ranks(t + me.step, stage) : 0.0f};
         if (post || pre)
-            team_sums<kMode == kPlain>(s, red[turn], deal, me.first_warp);
+            team_sums(s, red[turn], deal, me.first_warp);
         r1 = post ? inv_rms(s[1], per_hidden, a.eps) : 1.0f;
         if (pre) {
             const float r2 = inv_rms(s[0], per_hidden, a.eps);
@@ -642,7 +643,7 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
     __shared__ float red[2][kMaxWarps][8];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems, kMode> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
+    const Member<DT, W, kElems, kMode, kMode == kPlain> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
     const bool post = kMode == kPlain || a.w_post != nullptr;
     const bool pre = kMode == kPlain || a.w_pre != nullptr;
     const bool given = kMode == kPlain || a.dx_out != nullptr;
@@ -715,7 +716,7 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
         me.ready(deal.stages - 1);
         float s[6];
         row_sums(t, stage, s);
-        team_sums<kMode == kPlain>(s, red[turn], deal, me.first_warp);
+        team_sums(s, red[turn], deal, me.first_warp);
         const float r1 = post ? inv_rms(s[0], per_hidden, a.eps) : 1.0f;
         const float r2 = pre ? inv_rms(s[1], per_hidden, a.eps) : 0.0f;
         const float c2 = pre ? r2 * r2 * s[2] * per_hidden : 0.0f;
