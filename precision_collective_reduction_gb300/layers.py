@@ -14,6 +14,7 @@ between a thread's calls on the default stream).
 """
 import ctypes
 import threading
+import warnings
 
 from . import _binding as B
 
@@ -288,13 +289,17 @@ def expert_combine_backward(dout, slot_row, row_slot, drows, rows=None, weights=
 def _gate(gate, dtype, T, H, dev, kind):
     """(kind, pointer) of a gate of shape [H], [T] or [T, H]. A gate of one
     dimension is one value per channel if it has H values, whatever T is;
-    ``kind`` says otherwise."""
+    ``kind`` says otherwise. Where both fit and differ, so that a caller's gate
+    per token would change its meaning with the batch, a warning asks for it."""
     if gate is None:
         return GATE_NONE, None
     if not isinstance(gate, torch.Tensor):
         raise TypeError("gate must be a torch.Tensor")
     if kind is None:
         kind = "full" if gate.dim() == 2 else "channel" if gate.shape == (H,) else "token"
+        if kind == "channel" and T == H > 1:
+            warnings.warn("gate of %d values for as many tokens as channels is taken as one per "
+                          "channel: say so, or otherwise, with gate_kind" % H, stacklevel=3)
     if kind not in ("channel", "token", "full"):
         raise ValueError("gate_kind must be 'channel', 'token' or 'full', got %r" % (kind,))
     shape = {"channel": (H,), "token": (T,), "full": (T, H)}[kind]
@@ -310,7 +315,7 @@ def residual_norm(h, x, x_out, n_out=None, gate=None, w_post=None, w_pre=None, r
     branch_scale * gate * u. With ``w_pre`` [H], n_out is the RMS norm of
     x_out. ``h_sum`` receives the summed h. ``gate_kind`` ("channel", "token",
     "full") names the gate's kind; without it the shape does, and [H] goes
-    before [T] where the two are equal."""
+    before [T] where the two are equal, with a warning."""
     dev = _device()
     if isinstance(h, torch.Tensor):
         h = (h,)

@@ -1,4 +1,6 @@
 """Corners of the operators around the collectives."""
+import warnings
+
 import numpy as np
 import pytest
 import torch
@@ -45,3 +47,44 @@ def test_equal_rows_are_equal_in_every_team(lib, dt, T, H):  # noqa: F811
                                       f64(wq), f64(wp), a, b, eps, dt)
     within(dx[:1], want["dx"], "dx")
     within(dh[:1], want["dh"], "dh")
+
+
+# -- a gate of one dimension where [T] and [H] are the same shape --------------
+
+def test_gate_that_two_kinds_fit_is_reported():
+    T = H = 6
+    g, (h,), x, gate, wq, wp = norm_case(T, H, "f32", "token", True, True)
+    out = [torch.empty_like(x) for _ in range(4)]
+    dgate = torch.empty(T, device="cuda")
+    kw = dict(gate=gate, w_post=wq, w_pre=wp)
+    with pytest.warns(UserWarning, match="gate_kind"):
+        pcr.residual_norm(h, x, out[0], out[1], **kw)
+    with pytest.warns(UserWarning, match="gate_kind"):
+        pcr.residual_norm_backward(x, x, h, out[0], out[2], out[3], dgate=dgate, **kw)
+    a, b, eps = 1.0, 1.0, float(np.float32(1e-6))
+    for kind in ("channel", "token"):
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            pcr.residual_norm(h, x, out[0], out[1], gate_kind=kind, **kw)
+            pcr.residual_norm_backward(x, x, h, out[0], out[2], out[3], dgate=dgate,
+                                       gate_kind=kind, **kw)
+        want = ref.residual_norm([f64(h)], f64(x), f64(gate), kind, f64(wq), f64(wp), a, b, eps,
+                                 "f32")
+        within(out[0], want[0], "x_out, " + kind)
+        within(out[1], want[1], "n_out, " + kind)
+        want = ref.residual_norm_backward(f64(x), f64(x), f64(h), f64(out[0]), f64(gate), kind,
+                                          f64(wq), f64(wp), a, b, eps, "f32")
+        for got, name in ((out[2], "dx"), (out[3], "dh"), (dgate, "dgate")):
+            within(got, want[name], name + ", " + kind)
+
+
+def test_gate_that_one_kind_fits_is_not_reported():
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        for T, H in ((6, 5), (1, 1)):  # of one value both kinds are the same
+            x, out = torch.ones(T, H, device="cuda"), torch.empty(T, H, device="cuda")
+            for n in {T, H}:
+                pcr.residual_norm(x, x, out, gate=torch.full((n,), 2.0, device="cuda"))
+                assert bool((out == 3).all())
+            pcr.residual_norm(x, x, out, gate=torch.full((T, H), 2.0, device="cuda"))
+            assert bool((out == 3).all())
