@@ -7,7 +7,7 @@ import torch
 
 import layers_ref as ref
 import precision_collective_reduction_gb300 as pcr
-from test_gpu_layers import dev, f64, lib, norm_case, within  # noqa: F401
+from test_gpu_layers import Out, dev, f64, lib, norm_case, rng, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,32 @@ def test_gate_that_one_kind_fits_is_not_reported():
                 assert bool((out == 3).all())
             pcr.residual_norm(x, x, out, gate=torch.full((T, H), 2.0, device="cuda"))
             assert bool((out == 3).all())
+
+
+# -- the router's gradient far below the largest logit --------------------------
+
+def test_route_gradient_of_small_probabilities(lib):  # noqa: F811
+    # Logits are multiples of 1/8 below 128, so that z - max is exact. With one
+    # choice m = w dw. Allowed for p m, p = e^d / S of E experts: expf 2 ulp = 4 u,
+    # S (E - 1) u, its quotient, m and the last rounding u each, that is (E + 6) u,
+    # or, where e^d is subnormal, 2 of its ulps of 2^-149; a factor 1 + 2^-8 covers
+    # products of these.
+    T, E = 4000, 8
+    g = rng(T, E)
+    z = -g.integers(160, 827, size=(T, E)) / 8.0     # e^-20 down to e^-103.25
+    top = g.integers(0, E, size=T)
+    z[np.arange(T), top] = 0.0
+    out = Out()
+    ids, w, dl = out(T, 1, dtype=torch.int32), out(T, 1), out(T, E)
+    pcr.expert_route(dev(z), ids, w)
+    assert np.array_equal(ids.cpu().numpy()[:, 0], top)
+    dw = ((1 + g.random((T, 1))) * 2.0 ** 100).astype(np.float32)
+    pcr.expert_route_backward(dev(z), ids, w, dev(dw), dl)
+    p = np.exp(z) / np.exp(z).sum(1, keepdims=True)
+    m = f64(w) * dw.astype(np.float64)
+    bound = m * ((E + 6) * ref.U * p + 2.0 ** -148) * (1 + 2.0 ** -8) + ref.TINY
+    rest = np.arange(E) != top[:, None]              # the chosen one cancels: not of interest
+    got = f64(dl)
+    off = np.abs(got + p * m)[rest]
+    assert (off <= bound[rest]).all(), "worst %g times the bound" % (off / bound[rest]).max()
+    assert out.intact()
