@@ -12,6 +12,7 @@ Results go into tensors that the caller provides; scratch memory is the
 caller's ``workspace`` or, without one, torch's, on the call's stream (kept
 between a thread's calls on the default stream).
 """
+import contextlib
 import ctypes
 import threading
 import warnings
@@ -125,11 +126,16 @@ def _scratch(workspace, need, stream, device):
     return t.data_ptr(), need, t
 
 
-def _new_scratch(need, stream, device):
+def _on(stream, device):
+    """Context in which torch works on cudaStream_t ``stream``."""
     if stream == _raw_stream(device):
-        return torch.empty(need, dtype=torch.uint8, device="cuda")
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if stream
-                           else torch.cuda.default_stream()):
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if stream
+                             else torch.cuda.default_stream())
+
+
+def _new_scratch(need, stream, device):
+    with _on(stream, device):
         return torch.empty(need, dtype=torch.uint8, device="cuda")
 
 
@@ -350,7 +356,8 @@ def residual_norm_backward(dx_out, dn_out, h, x_out, dx, dh, gate=None, w_post=N
     """Gradients of residual_norm: dx_out, dn_out (either may be None where
     that output has no gradient or does not exist), the summed h and the
     result x_out -> dx, dh and, where given, dgate (float32 [H] or [T], or of
-    x_out's type [T, H]), dw_post and dw_pre (float32 [H])."""
+    x_out's type [T, H]), dw_post and dw_pre (float32 [H]). Without dn_out,
+    dw_pre is zeros."""
     dev = _device()
     T, H = _shape(x_out, 2, "x_out")
     dt, f32 = x_out.dtype, torch.float32
@@ -361,8 +368,8 @@ def residual_norm_backward(dx_out, dn_out, h, x_out, dx, dh, gate=None, w_post=N
             raise ValueError("a gradient of %s needs %s" % (what, what))
     if dx_out is None and dn_out is None:
         raise ValueError("need dx_out or dn_out")
-    if (dn_out is None) != (w_pre is None):
-        raise ValueError("dn_out and w_pre go together")
+    if dn_out is not None and w_pre is None:
+        raise ValueError("dn_out needs w_pre")
     gshape = {GATE_CHANNEL: (H,), GATE_TOKEN: (T,), GATE_FULL: (T, H)}.get(kind)
     p = (_opt(dx_out, "dx_out", dt, (T, H), dev), _opt(dn_out, "dn_out", dt, (T, H), dev),
          _ptr(h, "h", dt, (T, H), dev), _ptr(x_out, "x_out", dt, (T, H), dev))
@@ -375,9 +382,14 @@ def residual_norm_backward(dx_out, dn_out, h, x_out, dx, dh, gate=None, w_post=N
     code = _code(x_out)
     need = L.residual_norm_backward_workspace_bytes(T, H, code)
     st = _stream(stream, dev)
+    if dn_out is None:  # the second norm has no part in these gradients
+        pre = None
     wp, wn, _keep = _scratch(workspace, need, st, dev)
     B._check(L.residual_norm_backward(p[0], p[1], p[2], p[3], gp, kind, post, pre, res_scale,
                                       branch_scale, eps, T, H, code, q[0], q[1], q[2], q[3],
                                       q[4], wp, wn, st),
              "residual_norm_backward")
+    if dn_out is None and dw_pre is not None:
+        with _on(st, dev):
+            dw_pre.detach().zero_()
     return dx, dh

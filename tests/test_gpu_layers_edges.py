@@ -7,7 +7,7 @@ import torch
 
 import layers_ref as ref
 import precision_collective_reduction_gb300 as pcr
-from test_gpu_layers import Out, dev, f64, lib, norm_case, rng, within  # noqa: F401
+from test_gpu_layers import DT, Out, dev, f64, lib, norm_case, opt64, rng, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,52 @@ def test_route_gradient_of_small_probabilities(lib):  # noqa: F811
     off = np.abs(got + p * m)[rest]
     assert (off <= bound[rest]).all(), "worst %g times the bound" % (off / bound[rest]).max()
     assert out.intact()
+
+
+# -- outputs without a gradient --------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,post", [(None, True), ("channel", True), ("token", False),
+                                       ("full", True)])
+@pytest.mark.parametrize("T,H", [(1, 7), (40, 768), (200, 1025)])
+def test_norm_gradient_without_that_of_n_out(lib, dt, kind, post, T, H):  # noqa: F811
+    # as if there were no second norm, whose weight's gradient is 0
+    g, (h,), xo, gate, wq, wp = norm_case(T, H, dt, kind, post, True)
+    dxo = dev(g.normal(size=(T, H)), dt)
+    kw = dict(gate=gate, gate_kind=kind, w_post=wq, res_scale=0.9, branch_scale=0.7, eps=1e-5)
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        out = Out()
+        dx, dh = out(T, H, dtype=DT[dt]), out(T, H, dtype=DT[dt])
+        grads = {}
+        if kind:
+            grads["dgate"] = (out(T, H, dtype=DT[dt]) if kind == "full"
+                              else out(H if kind == "channel" else T))
+        if post:
+            grads["dw_post"] = out(H)
+        same = [torch.empty_like(dx), torch.empty_like(dh),
+                {k: torch.empty_like(v) for k, v in grads.items()}]
+        pcr.residual_norm_backward(dxo, None, h, xo, same[0], same[1], **kw, **same[2])
+        dw_pre = out(H)
+        dw_pre.fill_(7.0)
+        torch.cuda.synchronize()
+        pcr.residual_norm_backward(dxo, None, h, xo, dx, dh, w_pre=wp, dw_pre=dw_pre,
+                                   stream=stream, **kw, **grads)
+        torch.cuda.synchronize()
+        assert torch.equal(dx, same[0]) and torch.equal(dh, same[1])
+        for k, v in grads.items():
+            assert torch.equal(v, same[2][k]), k
+        assert not bool(dw_pre.any())
+        assert out.intact()
+    want = ref.residual_norm_backward(f64(dxo), None, f64(h), f64(xo), opt64(gate), kind,
+                                      opt64(wq), None, *(float(np.float32(v))
+                                                         for v in (0.9, 0.7, 1e-5)), dt)
+    within(dx, want["dx"], "dx")
+    within(dh, want["dh"], "dh")
+
+
+def test_norm_gradient_of_neither_output_is_refused():
+    x = torch.zeros(4, 16, device="cuda")
+    w = torch.ones(16, device="cuda")
+    with pytest.raises(ValueError):
+        pcr.residual_norm_backward(None, None, x, x, x, x, w_pre=w)
