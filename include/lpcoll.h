@@ -452,7 +452,8 @@ int residual_norm(const void *const *h, int nranks, const void *x, const void *g
  *   dw_post, dw_pre  out: float [hidden]; NULL if not wanted; ignored without
  *                    their weights
  *   workspace        residual_norm_backward_workspace_bytes(...) bytes
- * With ntokens = 0 the sums over tokens are written as zeros.               */
+ * With ntokens = 0 the sums over tokens are written as zeros, with hidden = 0
+ * the gradient of a token's gate.                                           */
 size_t residual_norm_backward_workspace_bytes(size_t ntokens, size_t hidden,
                                               lpcoll_dtype dtype);
 int residual_norm_backward(const void *dx_out, const void *dn_out, const void *h,

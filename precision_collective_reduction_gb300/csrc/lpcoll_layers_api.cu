@@ -378,8 +378,15 @@ int residual_norm_backward(const void *dx_out, const void *dn_out, const void *h
         dw_pre = nullptr;
     if (gate_kind == LPCOLL_GATE_NONE)
         dgate = nullptr;
-    if (hidden == 0)
-        return LPCOLL_OK;
+    if (hidden == 0) {
+        // rows of no elements: only a token's gate has a gradient, a sum over nothing
+        if (gate_kind != LPCOLL_GATE_TOKEN || dgate == nullptr || ntokens == 0)
+            return LPCOLL_OK;
+        st = check_ptr(dgate);
+        return st != LPCOLL_OK ? st
+                               : finish(cudaMemsetAsync(dgate, 0, ntokens * sizeof(float),
+                                                        static_cast<cudaStream_t>(stream)));
+    }
     const size_t need = norm_workspace(ntokens, hidden, dtype);
     if (workspace_bytes < need)
         return LPCOLL_ERR_ARG;

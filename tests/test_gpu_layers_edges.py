@@ -166,3 +166,23 @@ def test_norm_gradient_of_neither_output_is_refused():
     w = torch.ones(16, device="cuda")
     with pytest.raises(ValueError):
         pcr.residual_norm_backward(None, None, x, x, x, x, w_pre=w)
+
+
+# -- rows of no elements ----------------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_token_gate_of_rows_without_elements(lib, dt):  # noqa: F811
+    # a sum over no channels is 0
+    e = torch.empty(5, 0, dtype=DT[dt], device="cuda")
+    gate = torch.ones(5, dtype=DT[dt], device="cuda")
+    out = Out()
+    dgate = out(5)
+    dgate.fill_(7.0)
+    pcr.residual_norm_backward(e, None, e, e, e, e, gate=gate, gate_kind="token", dgate=dgate)
+    assert not bool(dgate.any())
+    assert out.intact()
+    misaligned = torch.zeros(6, device="cuda")[1:]
+    with pytest.raises(pcr.LpcollError) as r:
+        pcr.residual_norm_backward(e, None, e, e, e, e, gate=gate, gate_kind="token",
+                                   dgate=misaligned)
+    assert r.value.status == 2
