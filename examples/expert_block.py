@@ -9,15 +9,19 @@ Every rank holds its own tokens and 1/N of the experts. Forward, per rank:
     logits = n @ router            torch
     ids, weights                   expert_route
     slots sorted by expert         expert_sort, with a capacity: equal chunks
-    rows of every expert           expert_dispatch
-    rows to the experts' ranks     all_to_all_sim (exact or FP8 payloads)
+    rows of every expert           expert_dispatch (exact or FP8 payloads)
+    rows to the experts' ranks     all_to_all_sim
     experts' products              torch, one batch over the local experts
     results back                   all_to_all_sim
     y = weighted sum of results    expert_combine
     norm, gate, residual, norm     residual_norm
 
-and the gradients the same way back. The library runs on buffers that its
-caller provides, so a block makes all of its own once.
+and the gradients the same way back. In low precision the rows of both
+exchanges are FP8 payloads: expert_dispatch quantizes a token once for all its
+rows, and expert_combine reads the results' payload. (Rows that are not a whole
+number of payload blocks are dispatched and combined exact, and all_to_all_sim
+quantizes on its way.) The library runs on buffers that its caller provides, so a
+block makes all of its own once.
 """
 import argparse
 import os
@@ -74,25 +78,40 @@ class ExpertBlock:
         self.experts, self.local, self.topk = experts, experts // ranks, topk
         self.capacity = capacity or -(-tokens * topk * 5 // (experts * 4))
         self.block = pcr.BLOCK if low_precision else 0
+        self.payloads = low_precision and hidden % pcr.BLOCK == 0
         self.scales = dict(res_scale=1.0, branch_scale=1.0, eps=1e-6)
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.rank = [_Rank(tokens, hidden, experts, self.local, topk, self.capacity, dtype, g)
                      for _ in range(ranks)]
-        if low_precision:
+        self.wire = {}
+        if self.payloads:
+            rows = experts * self.capacity
+            for r in self.rank:
+                # a rank's payload as sent and as received
+                r.codes, r.codes_in = (_empty(rows, hidden, dtype=torch.uint8) for _ in range(2))
+                r.scales, r.scales_in = (_empty(rows, pcr.nblocks(hidden), dtype=torch.float32)
+                                         for _ in range(2))
+        elif low_precision:
             n = experts * self.capacity * hidden
             chunk = self.local * self.capacity * hidden
             self.wire = dict(
                 wire_codes=[_empty(n, dtype=torch.uint8) for _ in range(ranks)],
                 wire_scales=[_empty(ranks * pcr.nblocks(chunk), dtype=torch.float32)
                              for _ in range(ranks)])
-        else:
-            self.wire = {}
 
     def _exchange(self, src, dst, block):
         """Chunk j of every rank's rows to rank j."""
         pcr.all_to_all_sim([getattr(r, src).view(-1) for r in self.rank],
                            [getattr(r, dst).view(-1) for r in self.rank], block=block,
                            **(self.wire if block else {}))
+
+    def _exchange_payloads(self):
+        """The same for chunks of every rank's payload, which is there already: a copy
+        does not look into what it moves, so four codes travel as one FP32 number."""
+        for part in ("codes", "scales"):
+            pcr.all_to_all_sim([getattr(r, part).view(-1).view(torch.float32) for r in self.rank],
+                               [getattr(r, part + "_in").view(-1).view(torch.float32)
+                                for r in self.rank], block=0)
 
     def _by_expert(self, rows):
         """Rows as received, [source rank, local expert, capacity] -> one batch
@@ -115,13 +134,31 @@ class ExpertBlock:
             pcr.expert_route(nr @ r.router, r.ids, r.weights, renormalize=True)
             pcr.expert_sort(r.ids, self.experts, r.slot_row, r.row_slot, r.offsets, r.counts,
                             capacity=self.capacity)
-            pcr.expert_dispatch(nr, r.slot_row, r.row_slot, r.sent)
-        self._exchange("sent", "got", self.block)
+            if self.payloads:
+                pcr.expert_dispatch(nr, r.slot_row, r.row_slot, block=pcr.BLOCK, codes=r.codes,
+                                    scales=r.scales)
+            else:
+                pcr.expert_dispatch(nr, r.slot_row, r.row_slot, r.sent)
+        if self.payloads:
+            self._exchange_payloads()
+            for r in self.rank:
+                pcr.lp_dequantize(r.codes_in.view(-1), r.scales_in.view(-1), r.got.view(-1))
+        else:
+            self._exchange("sent", "got", self.block)
         for r in self.rank:
             self._by_source(self._experts(self._by_expert(r.got), r.w_in, r.w_out), r.made)
-        self._exchange("made", "back", self.block)
+        if self.payloads:
+            for r in self.rank:
+                pcr.lp_quantize(r.made.view(-1), r.codes.view(-1), r.scales.view(-1))
+            self._exchange_payloads()
+        else:
+            self._exchange("made", "back", self.block)
         for r, xr in zip(self.rank, x):
-            pcr.expert_combine(r.slot_row, r.y, r.back, weights=r.weights)
+            if self.payloads:
+                pcr.expert_combine(r.slot_row, r.y, weights=r.weights, block=pcr.BLOCK,
+                                   codes=r.codes_in, scales=r.scales_in)
+            else:
+                pcr.expert_combine(r.slot_row, r.y, r.back, weights=r.weights)
             pcr.residual_norm(r.y, xr, r.x_out, r.n_out, gate=r.gate, gate_kind="channel",
                               w_post=r.w_post, w_pre=r.w_pre, **self.scales)
         return [(r.x_out, r.n_out) for r in self.rank]
@@ -163,7 +200,7 @@ def main():
     for name, value in (("ranks", 4), ("tokens", 512), ("hidden", 1024), ("experts", 16),
                         ("topk", 4)):
         p.add_argument("--" + name, type=int, default=value)
-    p.add_argument("--low-precision", action="store_true", help="FP8 payloads in the all-to-all")
+    p.add_argument("--low-precision", action="store_true", help="rows travel as FP8 payloads")
     a = p.parse_args()
     block = ExpertBlock(a.ranks, a.tokens, a.hidden, a.experts, a.topk,
                         low_precision=a.low_precision)
