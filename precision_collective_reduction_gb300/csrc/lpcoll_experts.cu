@@ -10,9 +10,9 @@
 // launch (last, their long runs of stores were its tail).
 //
 // Measured on one GB300, 8192 tokens and 4 rows of 8192 BF16 each: dispatch 99 us
-// and combine 97 us (6.7 TB/s), as FP8 payloads 76 and 86 us; the gradient of
+// and combine 97 us (6.7 TB/s), as FP8 payloads 76 and 85 us; the gradient of
 // 4001 tokens and 8 rows of 4100 FP32 178 us (6.2 TB/s). DRAM bounds all of them
-// but the FP8 combine (latency of its short row pieces).
+// but the FP8 combine (instructions: 73% issue active, DRAM at 43%).
 #include "lpcoll_dda.cuh"
 #include "lpcoll_layers.cuh"
 #include "lpcoll_wide.cuh"
@@ -422,7 +422,7 @@ __device__ __forceinline__ uint4 load_row_codes(const RowsArgs &a, int row, size
 }
 
 // The same from FP8 payloads, with fl(weight * scale) as the factor of a code's
-// value. A lane holds 16 consecutive elements (with 8, 118 us instead of 93); a
+// value. A lane holds 16 consecutive elements (with 8, 118 us where 16 took 93, now 85); a
 // warp's results go through shared memory, so that its stores are consecutive.
 template <int DT, int W>
 __global__ void __launch_bounds__(kThreads) combine_lp_kernel(const RowsArgs a, const Cut cut)

@@ -18,11 +18,16 @@
 // the weights and gates of a channel give stays in its registers, and a team
 // goes through its rows one after the other while its next rows are on their
 // way into shared memory (cp.async): each thread copies and reads its own
-// columns only, so no barrier guards them.
+// columns only, so no barrier guards them. Where shared memory holds one row of a
+// team (8 ranks of 4096 or 8192 BF16 columns, the FP32 gradient of 8192), a forward
+// team sends for its next row once this one's columns are read, before the sums
+// meet, and a gradient's team at the row's end. Rows of that many bytes keep DRAM
+// busy all the same: 8192 x 8192 of 8 ranks 238 us, 4096 x 8192 FP32 gradient 132 us
+// (bytes at the copy rate: 238 and 119).
 //
-// Measured on one GB300, BF16: 16384 x 8192 forward 162 us (6.6 TB/s, DRAM), the
-// gradient of 8192 x 8192 133 us (6.1 TB/s; a team's phases between barriers), 32
-// x 8192 of 8 ranks 5.8 us (latency).
+// Measured on one GB300, BF16: 16384 x 8192 forward 161 us (6.7 TB/s, DRAM), the
+// gradient of 8192 x 8192 131 us (6.1 TB/s; a team's phases between barriers), 32
+// x 8192 of 8 ranks 5.9 us (latency).
 #include "lpcoll_layers.cuh"
 
 namespace lpc {
@@ -41,11 +46,13 @@ constexpr int kMaxWarps = kWideThreads / 32;
 // Forms of both kernels. kPlain is for calls without clusters in which every
 // thread has all its columns, both norms are there, one rank's h, no full gate
 // and, in the gradient, dx_out: without the conditions around every access the compiler
-// interleaves a thread's accesses (gradient of 8192 x 8192 BF16 143 -> 134 us).
+// interleaves a thread's accesses (gradient of 8192 x 8192 BF16 143 -> 134 us). Calls
+// without it pay: 16384 x 8192 BF16 with the second norm alone 216 us, with both 161.
 // kWide is for the forward pass of rows of more than 8192 columns, in a CTA of
 // 1024 threads with 16 columns each at 64 registers a thread, the weights from
-// L1 each time (8192 x 12288 BF16: 166 us, 241 with a cluster of two CTAs and the
-// weights in registers; the gradient, which keeps its sums too, 268 against 174).
+// L1 each time (8192 x 12288 BF16: 167 us, 241 with a cluster of two CTAs and the
+// weights in registers; the gradient of 4096 rows, which keeps its sums too, 268
+// against 174; 180 now, the price of the unaligned cluster barriers).
 enum Mode { kGeneral, kPlain, kWide };
 
 constexpr int kMaxStages = 4;
@@ -872,8 +879,8 @@ constexpr size_t kSmemOne = kSmem[0];
 // one, a cluster's. 16 columns a thread halve what a row costs besides its
 // columns (sums, addresses), 8 columns give twice the warps. 8192 columns in
 // BF16: the gradients of 8192 tokens take 134 us with 16 and 177 with 8, the
-// forward pass of 16384 tokens 183 and 160 (of 8 ranks at 4096 columns 121 and
-// 125). 8 are also faster where latency counts (32 tokens: 5.6 against 6.1 us)
+// forward pass of 16384 tokens 183 and 160 (8192 tokens of 8 ranks at 4096 columns
+// 121 and 125). 8 are also faster where latency counts (32 tokens: 5.6 against 6.1 us)
 // and for the shortest rows (128 columns: 7.2 against 9.0 us).
 Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
 {

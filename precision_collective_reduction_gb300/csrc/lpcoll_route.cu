@@ -11,8 +11,8 @@
 // not in the rest, is chosen again with both parts apart. A lane sorts its
 // numbers once, and the winner of a choice moves up its list. Every sum is
 // FP32 in a fixed order. Measured on one GB300, 32768 tokens of 256 FP32 logits,
-// 8 choices: 16.6 us (some 400 instructions per token, 72% issue active; with keys
-// and indexes apart 30 us), the gradient 13.2 us (0.78 of the copy rate).
+// 8 choices: 16.4 us (some 400 instructions per token, 70% issue active; with keys
+// and indexes apart 30 us; 18.8 for logits of BF16 values, whose ties are chosen again), the gradient 13.2 us (0.78 of the copy rate).
 #include "lpcoll_layers.cuh"
 
 namespace lpc {
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteArg
 // on another, then each of its warps takes a contiguous part of the chunk and
 // gives its slots their ranks in order, 32 at a time. Integer sums only: the
 // result does not depend on the order in which anything runs. Latency bounds it:
-// 4.5 us for 256 slots in one launch, 6.2 for 32768 and 7.0 for 131072 in two.
+// 4.6 us for 256 slots in one launch, 6.3 for 32768 and 7.0 for 131072 in two.
 // ---------------------------------------------------------------------------
 
 // The largest sort of one launch, in one CTA, and the smallest chunk of others:

@@ -9,8 +9,9 @@ As in ``_binding``, the functions check the torch tensors they are given
 (CUDA, on the current device, contiguous, of the right type and shape), pass
 their pointers to the library and raise ``LpcollError`` on a non-zero status.
 Results go into tensors that the caller provides; scratch memory is the
-caller's ``workspace`` or, without one, torch's, on the call's stream (kept
-between a thread's calls on the default stream).
+caller's ``workspace`` or, without one, torch's, on the call's stream (on the
+default stream kept, at the largest call's size, until the thread ends; a caller
+who wants the memory back passes a workspace).
 """
 import contextlib
 import ctypes
