@@ -464,6 +464,130 @@ int residual_norm_backward(const void *dx_out, const void *dn_out, const void *h
                            float *dw_post, float *dw_pre, void *workspace,
                            size_t workspace_bytes, void *stream);
 
+/* Layer norm of every token's row:
+ *   out = (x - m) / sqrt(mean((x - m)^2) + eps) * w + b,  m = mean(x)
+ *   x, out  [ntokens][hidden] of dtype; hidden up to LPCOLL_MAX_HIDDEN
+ *   w, b    [hidden] of dtype, or NULL for ones and zeros
+ *   eps     > 0
+ * The squares are summed about the row's mean, so that a mean that is large
+ * beside the spread costs no digits but those of x - m itself.              */
+int layer_norm(const void *x, const void *w, const void *b, float eps, size_t ntokens,
+               size_t hidden, lpcoll_dtype dtype, void *out, void *stream);
+
+/* Gradients of layer_norm; the statistics are taken from x again.
+ *   dout, x    [ntokens][hidden] of dtype
+ *   dx         out: [ntokens][hidden] of dtype; NULL if not wanted
+ *   dw, db     out: float [hidden]; NULL if not wanted; zeros if ntokens is 0
+ *   workspace  layer_norm_backward_workspace_bytes(...) bytes; none are needed
+ *              without dw and db                                            */
+size_t layer_norm_backward_workspace_bytes(size_t ntokens, size_t hidden,
+                                           lpcoll_dtype dtype);
+int layer_norm_backward(const void *dout, const void *x, const void *w, float eps,
+                        size_t ntokens, size_t hidden, lpcoll_dtype dtype, void *dx,
+                        float *dw, float *db, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* End of a block of a model with layer norms, for every token's row t:
+ *   h     = sum over r of h[r], FP32 in rank order
+ *   d     = h / (1 - p) where kept, 0 where dropped (whatever h is there)
+ *   x_out = x + d
+ *   n_out = layer norm of the unrounded x_out, with w, b and eps
+ *   h[r], x, x_out, n_out  [ntokens][hidden] of dtype; x may be NULL (0); with
+ *         n_out NULL there is no norm, w, b and eps are ignored, and hidden is
+ *         not limited
+ *   p     0 <= p < 1, the share that is dropped
+ *   rng   device memory of two 64-bit numbers, a seed and an offset, read when
+ *         the call runs (a replayed CUDA graph sees what stands there then); not
+ *         read, and may be NULL, if p is 0. Calls that are to drop
+ *         different elements need different offsets (or seeds).
+ *   first_row  number of the first row: a part of the rows drops what the whole
+ *         does
+ * Element (t, c) is kept if word c % 4 of the Philox4x32 generator of 10 rounds
+ * is not below floor(p 2^32), for the seed as key (low word first) and the
+ * counter of 128 bits whose low half is (first_row + t) * ceil(hidden / 4) + c / 4
+ * and whose high half is the offset. No mask is stored.                     */
+int residual_dropout(const void *const *h, int nranks, const void *x, const uint64_t *rng,
+                     float p, size_t first_row, const void *w, const void *b, float eps,
+                     size_t ntokens, size_t hidden, lpcoll_dtype dtype, void *x_out,
+                     void *n_out, void *stream);
+
+/* Gradients of residual_dropout, for the same rng, p and first_row.
+ *   dx_out, dn_out  gradients of the two outputs; dn_out NULL: no norm, or no
+ *              gradient through it; dx_out may be NULL (0) if dn_out is given
+ *   x_out      the result, from which the norm's statistics are taken again;
+ *              read only if dn_out is given
+ *   dx, dh     out: of x, and of every h[r], [ntokens][hidden] of dtype; NULL
+ *              if not wanted (without dn_out, dx is dx_out itself)
+ *   dw, db     out: float [hidden]; NULL if not wanted; zeros without dn_out or
+ *              with ntokens 0
+ *   workspace  residual_dropout_backward_workspace_bytes(...) bytes; none are
+ *              needed without dn_out, or without dw and db                  */
+size_t residual_dropout_backward_workspace_bytes(size_t ntokens, size_t hidden,
+                                                 lpcoll_dtype dtype);
+int residual_dropout_backward(const void *dx_out, const void *dn_out, const void *x_out,
+                              const uint64_t *rng, float p, size_t first_row, const void *w,
+                              float eps, size_t ntokens, size_t hidden, lpcoll_dtype dtype,
+                              void *dx, void *dh, float *dw, float *db, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Balance loss of a router over the valid tokens, with p_t = softmax(logits[t]):
+ *   n_e  = choices of expert e,  S = sum over e of n_e,  V = valid tokens
+ *   P_e  = sum over t of p_t[e]
+ *   loss = coef * nexperts * sum over e of (n_e / S) (P_e / V);  0 if S V is 0
+ *   logits     [ntokens][nexperts] of dtype
+ *   ids        [ntokens][topk] as expert_route writes them; entries outside
+ *              [0, nexperts) count nowhere
+ *   valid      [ntokens], 0 where a token is padding (its logits and ids are not
+ *              read into the result); NULL: none is
+ *   loss       out: float [1]
+ *   counts     out: int32 [nexperts + 1], n_e and then V
+ *   prob_sums  out: float [nexperts], P_e
+ *   workspace  expert_balance_workspace_bytes(ntokens, nexperts) bytes
+ * A token without a logit above -infinity has p_t = 0. Counts and sums of several
+ * ranks may be added up before the loss is taken from them.                 */
+size_t expert_balance_workspace_bytes(size_t ntokens, int nexperts);
+int expert_balance(const void *logits, lpcoll_dtype dtype, size_t ntokens, int nexperts,
+                   const int32_t *ids, int topk, const uint8_t *valid, float coef,
+                   float *loss, int32_t *counts, float *prob_sums, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Gradient of the balance loss with respect to the logits; the counts have none.
+ *   counts      as expert_balance wrote them, or their sums over ranks
+ *   dloss       float [1], in device memory
+ *   accumulate  0: dlogits is written, zeros for padding; 1: the gradient is
+ *               added to what stands there (expert_route_backward's)
+ *   dlogits     out: [ntokens][nexperts] of dtype; may be logits itself if
+ *               accumulate is 0
+ * dlogits[t][j] = dloss coef nexperts / (S V) p_t[j] (n_j - sum_e n_e p_t[e]). */
+int expert_balance_backward(const void *logits, lpcoll_dtype dtype, size_t ntokens,
+                            int nexperts, const uint8_t *valid, const int32_t *counts,
+                            float coef, const float *dloss, int accumulate, void *dlogits,
+                            void *stream);
+
+/* Type of token ids. */
+typedef enum { LPCOLL_I32 = 0, LPCOLL_I64 = 1 } lpcoll_index;
+
+/* Rows of a shard of a vocabulary: out[t] = scale * table[ids[t] - first_id], and
+ * +0 where ids[t] is outside [first_id, first_id + vocab): the ids of other
+ * shards (whose results an allreduce adds) and padding.
+ *   table  [vocab][hidden] of dtype      out  [ntokens][hidden] of dtype
+ *   ids    [ntokens] of index's type     vocab < 2^31                       */
+int token_embed(const void *table, size_t vocab, const void *ids, lpcoll_index index,
+                int64_t first_id, size_t ntokens, size_t hidden, lpcoll_dtype dtype,
+                float scale, void *out, void *stream);
+
+/* Gradient of token_embed: dtable[v] = scale * sum of dout[t] over the tokens t of
+ * row v, FP32 in an order that depends on the ids alone.
+ *   accumulate  0: dtable is written, zeros in rows without a token; 1: the sums
+ *               are added to what stands there, other rows are not touched
+ *   dtable      out: float [vocab][hidden], none of the inputs
+ *   workspace   token_embed_backward_workspace_bytes(...) bytes             */
+size_t token_embed_backward_workspace_bytes(size_t ntokens, size_t vocab, size_t hidden);
+int token_embed_backward(const void *dout, const void *ids, lpcoll_index index,
+                         int64_t first_id, size_t ntokens, size_t vocab, size_t hidden,
+                         lpcoll_dtype dtype, float scale, int accumulate, float *dtable,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
 /* Bounds checks, a test tool with no counterpart in the method. The
  * bounds-checked build of this library (liblpcoll_debug_bounds.so, compiled
  * with -DLPCOLL_DEBUG_BOUNDS) makes every entry point list the buffers its

@@ -16,10 +16,15 @@ from ._binding import (BF16, BLOCK, E4M3, E5M2, F32, MAX_RANKS, VARIANT_BLOCKS,
                        shard_len, status_string)
 from .allreduce import Workspace, allreduce_sim, choose
 from .layers import (GATE_CHANNEL, GATE_FULL, GATE_NONE, GATE_TOKEN, MAX_EXPERTS, MAX_HIDDEN,
-                     MAX_TOPK, expert_combine, expert_combine_backward, expert_dispatch,
-                     expert_dispatch_backward, expert_route, expert_route_backward,
-                     expert_sort, expert_sort_workspace_bytes, residual_norm,
-                     residual_norm_backward, residual_norm_backward_workspace_bytes)
+                     MAX_TOPK, expert_balance, expert_balance_backward,
+                     expert_balance_workspace_bytes, expert_combine, expert_combine_backward,
+                     expert_dispatch, expert_dispatch_backward, expert_route,
+                     expert_route_backward, expert_sort, expert_sort_workspace_bytes,
+                     layer_norm, layer_norm_backward, layer_norm_backward_workspace_bytes,
+                     residual_dropout, residual_dropout_backward,
+                     residual_dropout_backward_workspace_bytes, residual_norm,
+                     residual_norm_backward, residual_norm_backward_workspace_bytes,
+                     token_embed, token_embed_backward, token_embed_backward_workspace_bytes)
 
 __all__ = ["BF16", "BLOCK", "F32", "MAX_RANKS", "LpcollError", "Workspace",
            "all_gather_sim", "all_to_all_sim", "allreduce_sim", "choose",
@@ -33,4 +38,8 @@ __all__ = ["BF16", "BLOCK", "F32", "MAX_RANKS", "LpcollError", "Workspace",
            "expert_dispatch", "expert_dispatch_backward", "expert_route",
            "expert_route_backward", "expert_sort", "expert_sort_workspace_bytes",
            "residual_norm", "residual_norm_backward",
-           "residual_norm_backward_workspace_bytes"]
+           "residual_norm_backward_workspace_bytes", "expert_balance",
+           "expert_balance_backward", "expert_balance_workspace_bytes", "layer_norm",
+           "layer_norm_backward", "layer_norm_backward_workspace_bytes", "residual_dropout",
+           "residual_dropout_backward", "residual_dropout_backward_workspace_bytes",
+           "token_embed", "token_embed_backward", "token_embed_backward_workspace_bytes"]

@@ -115,11 +115,29 @@ def _declare_layers(L):
     L.residual_norm_backward_workspace_bytes.argtypes = [sz, sz, ci]
     L.residual_norm_backward.argtypes = [vp, vp, vp, vp, vp, ci, vp, vp, cf, cf, cf, sz, sz, ci,
                                          vp, vp, vp, vp, vp, vp, sz, vp]
+    L.layer_norm.argtypes = [vp, vp, vp, cf, sz, sz, ci, vp, vp]
+    L.layer_norm_backward_workspace_bytes.argtypes = [sz, sz, ci]
+    L.layer_norm_backward.argtypes = [vp, vp, vp, cf, sz, sz, ci, vp, vp, vp, vp, sz, vp]
+    L.residual_dropout.argtypes = [pp, ci, vp, vp, cf, sz, vp, vp, cf, sz, sz, ci, vp, vp, vp]
+    L.residual_dropout_backward_workspace_bytes.argtypes = [sz, sz, ci]
+    L.residual_dropout_backward.argtypes = [vp, vp, vp, vp, cf, sz, vp, cf, sz, sz, ci, vp, vp,
+                                            vp, vp, vp, sz, vp]
+    L.expert_balance_workspace_bytes.argtypes = [sz, ci]
+    L.expert_balance.argtypes = [vp, ci, sz, ci, vp, ci, vp, cf, vp, vp, vp, vp, sz, vp]
+    L.expert_balance_backward.argtypes = [vp, ci, sz, ci, vp, vp, cf, vp, ci, vp, vp]
+    i64 = ctypes.c_int64
+    L.token_embed.argtypes = [vp, sz, vp, ci, i64, sz, sz, ci, cf, vp, vp]
+    L.token_embed_backward_workspace_bytes.argtypes = [sz, sz, sz]
+    L.token_embed_backward.argtypes = [vp, vp, ci, i64, sz, sz, sz, ci, cf, ci, vp, vp, sz, vp]
     for f in ("expert_route", "expert_route_backward", "expert_sort", "expert_dispatch",
               "expert_combine", "expert_combine_backward", "residual_norm",
-              "residual_norm_backward"):
+              "residual_norm_backward", "layer_norm", "layer_norm_backward", "residual_dropout",
+              "residual_dropout_backward", "expert_balance", "expert_balance_backward",
+              "token_embed", "token_embed_backward"):
         getattr(L, f).restype = ci
-    for f in ("expert_sort_workspace_bytes", "residual_norm_backward_workspace_bytes"):
+    for f in ("expert_sort_workspace_bytes", "residual_norm_backward_workspace_bytes",
+              "layer_norm_backward_workspace_bytes", "residual_dropout_backward_workspace_bytes",
+              "expert_balance_workspace_bytes", "token_embed_backward_workspace_bytes"):
         getattr(L, f).restype = sz
 
 

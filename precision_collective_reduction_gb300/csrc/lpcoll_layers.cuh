@@ -146,13 +146,23 @@ __device__ __forceinline__ void store_f32(float *p, float v)
         *p = v;
 }
 
-// Two FP32 products, or products and sums, in one instruction; each half rounds
+// Two FP32 products, sums, or products and sums, in one instruction; each half rounds
 // as the scalar operation does.
 __device__ __forceinline__ float2 mul_pair(float2 a, float2 b)
 {
     float2 r;
     asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
         "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
         : "=f"(r.x), "=f"(r.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
@@ -275,5 +285,75 @@ struct NormArgs {
 int norm_backward_parts(size_t tokens, size_t hidden, int dtype);
 cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t st);
 cudaError_t launch_residual_norm_backward(const NormArgs &a, cudaStream_t st);
+
+// Dropout's random numbers (lpcoll_philox.cuh).
+struct DropArgs {
+    const unsigned long long *rng;  // seed, offset (device memory)
+    unsigned long long first_row;
+    uint32_t least;  // smallest word that is kept; 0: all are, and rng is not read
+    float scale;     // 1 / (1 - p)
+};
+
+struct LayerNormArgs {
+    const void *h[LPCOLL_MAX_RANKS];  // partial products; none for layer_norm
+    int nranks;
+    const void *x;  // layer_norm: its input; else the residual or NULL; gradients: x'
+    const void *w, *b;
+    void *x_out, *n_out;
+    const void *dx_out, *dn_out;  // gradients
+    void *dx, *dh;
+    float *dw, *db;
+    float *partial;  // workspace of the sums over tokens
+    DropArgs drop;
+    float eps;
+    size_t tokens;
+    int hidden, dtype;
+};
+
+// Rows of sums that a gradient leaves in its workspace, and their sums.
+int layer_norm_parts(size_t tokens, size_t hidden, int dtype, bool dropout);
+cudaError_t launch_layer_norm_sums(const LayerNormArgs &a, int parts, cudaStream_t st);
+cudaError_t launch_layer_norm(const LayerNormArgs &a, cudaStream_t st);
+cudaError_t launch_layer_norm_backward(const LayerNormArgs &a, cudaStream_t st);
+// residual_dropout with its norm, and without.
+cudaError_t launch_dropout_norm(const LayerNormArgs &a, cudaStream_t st);
+cudaError_t launch_dropout_norm_backward(const LayerNormArgs &a, cudaStream_t st);
+cudaError_t launch_dropout(const LayerNormArgs &a, cudaStream_t st);
+
+struct BalanceArgs {
+    const void *logits;
+    const int32_t *ids;
+    const uint8_t *valid;  // NULL: every token is
+    float *loss, *prob_sums;
+    int32_t *counts;
+    float *rows;           // workspace: sums and counts of each CTA
+    const float *dloss;    // backward
+    void *dlogits;         // backward
+    float coef;
+    size_t tokens;
+    int experts, topk, dtype, accumulate;
+};
+// Rows that a call's launch of CTAs leaves (1: all in one cluster), and their bytes.
+int balance_rows(size_t tokens);
+size_t balance_workspace(size_t tokens, int experts);
+cudaError_t launch_balance(const BalanceArgs &a, cudaStream_t st);
+cudaError_t launch_balance_backward(const BalanceArgs &a, cudaStream_t st);
+
+struct EmbedArgs {
+    const void *table;     // forward
+    void *out;             // forward
+    const void *dout;      // backward
+    float *dtable;         // backward
+    const void *ids;
+    int ids64;             // ids are int64_t, not int32_t
+    long long first_id;
+    float scale;
+    size_t tokens, vocab, hidden;
+    int dtype, accumulate;
+    void *workspace;       // backward
+};
+size_t embed_workspace(size_t tokens, size_t vocab, size_t hidden);
+cudaError_t launch_embed(const EmbedArgs &a, cudaStream_t st);
+cudaError_t launch_embed_backward(const EmbedArgs &a, cudaStream_t st);
 
 }  // namespace lpc

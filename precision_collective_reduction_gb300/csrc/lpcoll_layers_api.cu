@@ -66,6 +66,41 @@ int check_route(int dtype, size_t ntokens, int nexperts, int topk)
     return ntokens > kMaxIndex / static_cast<size_t>(topk) ? LPCOLL_ERR_ARG : LPCOLL_OK;
 }
 
+// Workspace of a layer norm's gradients.
+size_t layer_norm_workspace(size_t ntokens, size_t hidden, int dtype, bool dropout)
+{
+    return static_cast<size_t>(2) * layer_norm_parts(ntokens, hidden, dtype, dropout) * hidden *
+           sizeof(float);
+}
+
+// Sizes of residual_dropout without a norm: CTAs along every token's row.
+int check_dropout(float p, size_t ntokens, size_t hidden, int dtype)
+{
+    if (bad_dtype(dtype) || !(p >= 0.0f && p < 1.0f))
+        return LPCOLL_ERR_ARG;
+    return check_rows(ntokens, 1, 0, hidden, dtype);
+}
+
+// The random words that are kept, and what a kept value is multiplied by.
+DropArgs drop_args(const uint64_t *rng, float p, size_t first_row)
+{
+    DropArgs d;
+    d.rng = reinterpret_cast<const unsigned long long *>(rng);
+    d.first_row = first_row;
+    d.least = static_cast<uint32_t>(static_cast<double>(p) * 4294967296.0);
+    d.scale = static_cast<float>(1.0 / (1.0 - static_cast<double>(p)));
+    return d;
+}
+
+int check_embed(size_t ntokens, size_t vocab, size_t hidden, int dtype, int index)
+{
+    if (index != LPCOLL_I32 && index != LPCOLL_I64)
+        return LPCOLL_ERR_ARG;
+    return check_rows(ntokens, 1, vocab, hidden, dtype);
+}
+
+size_t index_bytes(int index) { return index == LPCOLL_I64 ? 8 : 4; }
+
 }  // namespace
 
 }  // namespace lpc
@@ -440,6 +475,362 @@ int residual_norm_backward(const void *dx_out, const void *dn_out, const void *h
     a.hidden = static_cast<int>(hidden);
     a.dtype = dtype;
     return finish(launch_residual_norm_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+int layer_norm(const void *x, const void *w, const void *b, float eps, size_t ntokens,
+               size_t hidden, lpcoll_dtype dtype, void *out, void *stream)
+{
+    int st = check_norm(LPCOLL_GATE_NONE, eps, ntokens, hidden, dtype);
+    if (st != LPCOLL_OK || ntokens == 0 || hidden == 0)
+        return st;
+    st = first_error({check_ptr(x), check_optional(w), check_optional(b), check_ptr(out)});
+    if (st != LPCOLL_OK)
+        return st;
+    const size_t es = elem_bytes(dtype), all = ntokens * hidden * es;
+    debug_begin();
+    debug_range(x, all, false);
+    debug_range(w, hidden * es, false);
+    debug_range(b, hidden * es, false);
+    debug_range(out, all, true);
+    LayerNormArgs a = {};
+    a.x = x;
+    a.w = w;
+    a.b = b;
+    a.n_out = out;
+    a.eps = eps;
+    a.tokens = ntokens;
+    a.hidden = static_cast<int>(hidden);
+    a.dtype = dtype;
+    return finish(launch_layer_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t layer_norm_backward_workspace_bytes(size_t ntokens, size_t hidden, lpcoll_dtype dtype)
+{
+    if (check_norm(LPCOLL_GATE_NONE, 1.0f, ntokens, hidden, dtype) != LPCOLL_OK)
+        return 0;
+    return layer_norm_workspace(ntokens, hidden, dtype, false);
+}
+
+int layer_norm_backward(const void *dout, const void *x, const void *w, float eps,
+                        size_t ntokens, size_t hidden, lpcoll_dtype dtype, void *dx, float *dw,
+                        float *db, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int st = check_norm(LPCOLL_GATE_NONE, eps, ntokens, hidden, dtype);
+    if (st != LPCOLL_OK)
+        return st;
+    const bool sums = dw != nullptr || db != nullptr;
+    const size_t need = sums ? layer_norm_workspace(ntokens, hidden, dtype, false) : 0;
+    if (workspace_bytes < need)
+        return LPCOLL_ERR_ARG;
+    if (hidden == 0 || (!sums && (dx == nullptr || ntokens == 0)))
+        return LPCOLL_OK;
+    st = first_error({check_array(dout, ntokens), check_array(x, ntokens), check_optional(w),
+                      check_optional(dx), check_optional(dw), check_optional(db),
+                      check_array(workspace, need)});
+    if (st != LPCOLL_OK)
+        return st;
+    const size_t es = elem_bytes(dtype), all = ntokens * hidden * es;
+    debug_begin();
+    debug_range(dout, all, false);
+    debug_range(x, all, false);
+    debug_range(w, hidden * es, false);
+    debug_range(dx, all, true);
+    debug_range(dw, hidden * sizeof(float), true);
+    debug_range(db, hidden * sizeof(float), true);
+    debug_range(workspace, need, true);
+    LayerNormArgs a = {};
+    a.x = x;
+    a.w = w;
+    a.dn_out = dout;
+    a.dx = dx;
+    a.dw = dw;
+    a.db = db;
+    a.partial = static_cast<float *>(workspace);
+    a.eps = eps;
+    a.tokens = ntokens;
+    a.hidden = static_cast<int>(hidden);
+    a.dtype = dtype;
+    return finish(launch_layer_norm_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+int residual_dropout(const void *const *h, int nranks, const void *x, const uint64_t *rng,
+                     float p, size_t first_row, const void *w, const void *b, float eps,
+                     size_t ntokens, size_t hidden, lpcoll_dtype dtype, void *x_out, void *n_out,
+                     void *stream)
+{
+    int st = check_dropout(p, ntokens, hidden, dtype);
+    const bool norm = n_out != nullptr;
+    if (st == LPCOLL_OK && norm)
+        st = check_norm(LPCOLL_GATE_NONE, eps, ntokens, hidden, dtype);
+    if (st == LPCOLL_OK && (nranks < 1 || nranks > LPCOLL_MAX_RANKS))
+        st = LPCOLL_ERR_ARG;
+    if (st != LPCOLL_OK || ntokens == 0 || hidden == 0)
+        return st;
+    LayerNormArgs a = {};
+    a.drop = drop_args(rng, p, first_row);
+    st = first_error({check_rank_array(h, nranks), check_optional(x),
+                      a.drop.least != 0 ? check_ptr(rng) : LPCOLL_OK,
+                      norm ? check_optional(w) : LPCOLL_OK, norm ? check_optional(b) : LPCOLL_OK,
+                      check_ptr(x_out), check_optional(n_out)});
+    if (st != LPCOLL_OK)
+        return st;
+    const size_t es = elem_bytes(dtype), all = ntokens * hidden * es;
+    debug_begin();
+    for (int r = 0; r < nranks; ++r) {
+        a.h[r] = h[r];
+        debug_range(h[r], all, false);
+    }
+    debug_range(x, all, false);
+    debug_range(a.drop.least != 0 ? rng : nullptr, 2 * sizeof(uint64_t), false);
+    debug_range(norm ? w : nullptr, hidden * es, false);
+    debug_range(norm ? b : nullptr, hidden * es, false);
+    debug_range(x_out, all, true);
+    debug_range(n_out, all, true);
+    a.nranks = nranks;
+    a.x = x;
+    a.w = w;
+    a.b = b;
+    a.x_out = x_out;
+    a.n_out = n_out;
+    a.eps = eps;
+    a.tokens = ntokens;
+    a.hidden = static_cast<int>(hidden);
+    a.dtype = dtype;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(norm ? launch_dropout_norm(a, s) : launch_dropout(a, s));
+}
+
+size_t residual_dropout_backward_workspace_bytes(size_t ntokens, size_t hidden,
+                                                 lpcoll_dtype dtype)
+{
+    if (check_norm(LPCOLL_GATE_NONE, 1.0f, ntokens, hidden, dtype) != LPCOLL_OK)
+        return 0;
+    return layer_norm_workspace(ntokens, hidden, dtype, true);
+}
+
+int residual_dropout_backward(const void *dx_out, const void *dn_out, const void *x_out,
+                              const uint64_t *rng, float p, size_t first_row, const void *w,
+                              float eps, size_t ntokens, size_t hidden, lpcoll_dtype dtype,
+                              void *dx, void *dh, float *dw, float *db, void *workspace,
+                              size_t workspace_bytes, void *stream)
+{
+    int st = check_dropout(p, ntokens, hidden, dtype);
+    const bool sums = dw != nullptr || db != nullptr;
+    const bool norm = dn_out != nullptr;
+    if (st == LPCOLL_OK && (norm || sums))
+        st = check_norm(LPCOLL_GATE_NONE, eps, ntokens, hidden, dtype);
+    if (st != LPCOLL_OK)
+        return st;
+    const size_t need = norm && sums ? layer_norm_workspace(ntokens, hidden, dtype, true) : 0;
+    if (workspace_bytes < need)
+        return LPCOLL_ERR_ARG;
+    const bool rows = ntokens != 0 && (dx != nullptr || dh != nullptr);
+    if (hidden == 0 || (!sums && !rows))
+        return LPCOLL_OK;
+    LayerNormArgs a = {};
+    a.drop = drop_args(rng, p, first_row);
+    if (dh == nullptr)  // the generator is not read
+        a.drop.least = 0;
+    const bool drop = a.drop.least != 0;
+    st = first_error({norm || !rows ? check_optional(dx_out) : check_ptr(dx_out),
+                      check_optional(dn_out), norm ? check_array(x_out, ntokens) : LPCOLL_OK,
+                      drop && ntokens != 0 ? check_ptr(rng) : LPCOLL_OK,
+                      norm ? check_optional(w) : LPCOLL_OK, check_optional(dx),
+                      check_optional(dh), check_optional(dw), check_optional(db),
+                      check_array(workspace, need)});
+    if (st != LPCOLL_OK)
+        return st;
+    const size_t es = elem_bytes(dtype), all = ntokens * hidden * es;
+    debug_begin();
+    debug_range(dx_out, all, false);
+    debug_range(dn_out, all, false);
+    debug_range(norm ? x_out : nullptr, all, false);
+    debug_range(drop ? rng : nullptr, 2 * sizeof(uint64_t), false);
+    debug_range(norm ? w : nullptr, hidden * es, false);
+    debug_range(dx, all, true);
+    debug_range(dh, all, true);
+    debug_range(dw, hidden * sizeof(float), true);
+    debug_range(db, hidden * sizeof(float), true);
+    debug_range(workspace, need, true);
+    a.tokens = ntokens;
+    a.hidden = static_cast<int>(hidden);
+    a.dtype = dtype;
+    a.dx = dx;
+    a.dw = dw;
+    a.db = db;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (norm) {
+        a.x = x_out;
+        a.w = w;
+        a.dx_out = dx_out;
+        a.dn_out = dn_out;
+        a.dh = dh;
+        a.partial = static_cast<float *>(workspace);
+        a.eps = eps;
+        return finish(launch_dropout_norm_backward(a, s));
+    }
+    // without the norm's part, dh is dx_out through the same mask
+    a.h[0] = dx_out;
+    a.nranks = 1;
+    a.x_out = dh;
+    cudaError_t e = rows ? launch_dropout(a, s) : cudaSuccess;
+    if (e == cudaSuccess && sums)
+        e = launch_layer_norm_sums(a, 0, s);
+    return finish(e);
+}
+
+size_t expert_balance_workspace_bytes(size_t ntokens, int nexperts)
+{
+    if (check_route(LPCOLL_F32, ntokens, nexperts, 1) != LPCOLL_OK)
+        return 0;
+    return balance_workspace(ntokens, nexperts);
+}
+
+int expert_balance(const void *logits, lpcoll_dtype dtype, size_t ntokens, int nexperts,
+                   const int32_t *ids, int topk, const uint8_t *valid, float coef, float *loss,
+                   int32_t *counts, float *prob_sums, void *workspace, size_t workspace_bytes,
+                   void *stream)
+{
+    int st = check_route(dtype, ntokens, nexperts, topk);
+    if (st != LPCOLL_OK)
+        return st;
+    const size_t need = balance_workspace(ntokens, nexperts);
+    if (workspace_bytes < need)
+        return LPCOLL_ERR_ARG;
+    st = first_error({check_array(logits, ntokens), check_array(ids, ntokens),
+                      check_optional(valid), check_ptr(loss), check_ptr(counts),
+                      check_ptr(prob_sums), check_ptr(workspace)});
+    if (st != LPCOLL_OK)
+        return st;
+    debug_begin();
+    debug_range(logits, ntokens * nexperts * elem_bytes(dtype), false);
+    debug_range(ids, ntokens * topk * sizeof(int32_t), false);
+    debug_range(valid, ntokens, false);
+    debug_range(loss, sizeof(float), true);
+    debug_range(counts, (static_cast<size_t>(nexperts) + 1) * sizeof(int32_t), true);
+    debug_range(prob_sums, nexperts * sizeof(float), true);
+    debug_range(workspace, need, true);
+    BalanceArgs a = {};
+    a.logits = logits;
+    a.ids = ids;
+    a.valid = valid;
+    a.loss = loss;
+    a.counts = counts;
+    a.prob_sums = prob_sums;
+    a.rows = static_cast<float *>(workspace);
+    a.coef = coef;
+    a.tokens = ntokens;
+    a.experts = nexperts;
+    a.topk = topk;
+    a.dtype = dtype;
+    return finish(launch_balance(a, static_cast<cudaStream_t>(stream)));
+}
+
+int expert_balance_backward(const void *logits, lpcoll_dtype dtype, size_t ntokens, int nexperts,
+                            const uint8_t *valid, const int32_t *counts, float coef,
+                            const float *dloss, int accumulate, void *dlogits, void *stream)
+{
+    int st = check_route(dtype, ntokens, nexperts, 1);
+    if (st != LPCOLL_OK || ntokens == 0)
+        return st;
+    st = first_error({check_ptr(logits), check_optional(valid), check_ptr(counts),
+                      check_ptr(dloss), check_ptr(dlogits)});
+    if (st != LPCOLL_OK)
+        return st;
+    const size_t all = ntokens * nexperts * elem_bytes(dtype);
+    debug_begin();
+    debug_range(logits, all, false);
+    debug_range(valid, ntokens, false);
+    debug_range(counts, (static_cast<size_t>(nexperts) + 1) * sizeof(int32_t), false);
+    debug_range(dloss, sizeof(float), false);
+    debug_range(dlogits, all, true);
+    BalanceArgs a = {};
+    a.logits = logits;
+    a.valid = valid;
+    a.counts = const_cast<int32_t *>(counts);
+    a.dloss = dloss;
+    a.dlogits = dlogits;
+    a.coef = coef;
+    a.tokens = ntokens;
+    a.experts = nexperts;
+    a.topk = 1;
+    a.dtype = dtype;
+    a.accumulate = accumulate;
+    return finish(launch_balance_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+int token_embed(const void *table, size_t vocab, const void *ids, lpcoll_index index,
+                int64_t first_id, size_t ntokens, size_t hidden, lpcoll_dtype dtype, float scale,
+                void *out, void *stream)
+{
+    int st = check_embed(ntokens, vocab, hidden, dtype, index);
+    if (st != LPCOLL_OK || ntokens == 0 || hidden == 0)
+        return st;
+    st = first_error({check_array(table, vocab), check_ptr(ids), check_ptr(out)});
+    if (st != LPCOLL_OK)
+        return st;
+    const size_t row = hidden * elem_bytes(dtype);
+    debug_begin();
+    debug_range(table, vocab * row, false);
+    debug_range(ids, ntokens * index_bytes(index), false);
+    debug_range(out, ntokens * row, true);
+    EmbedArgs a = {};
+    a.table = table;
+    a.out = out;
+    a.ids = ids;
+    a.ids64 = index == LPCOLL_I64;
+    a.first_id = first_id;
+    a.scale = scale;
+    a.tokens = ntokens;
+    a.vocab = vocab;
+    a.hidden = hidden;
+    a.dtype = dtype;
+    return finish(launch_embed(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t token_embed_backward_workspace_bytes(size_t ntokens, size_t vocab, size_t hidden)
+{
+    if (check_embed(ntokens, vocab, hidden, LPCOLL_F32, LPCOLL_I32) != LPCOLL_OK)
+        return 0;
+    return embed_workspace(ntokens, vocab, hidden);
+}
+
+int token_embed_backward(const void *dout, const void *ids, lpcoll_index index, int64_t first_id,
+                         size_t ntokens, size_t vocab, size_t hidden, lpcoll_dtype dtype,
+                         float scale, int accumulate, float *dtable, void *workspace,
+                         size_t workspace_bytes, void *stream)
+{
+    int st = check_embed(ntokens, vocab, hidden, dtype, index);
+    if (st != LPCOLL_OK)
+        return st;
+    const size_t need = embed_workspace(ntokens, vocab, hidden);
+    if (workspace_bytes < need)
+        return LPCOLL_ERR_ARG;
+    if (vocab == 0 || hidden == 0 || (ntokens == 0 && accumulate))
+        return LPCOLL_OK;
+    st = first_error({check_array(dout, ntokens), check_array(ids, ntokens), check_ptr(dtable),
+                      check_array(workspace, need)});
+    if (st != LPCOLL_OK)
+        return st;
+    debug_begin();
+    debug_range(dout, ntokens * hidden * elem_bytes(dtype), false);
+    debug_range(ids, ntokens * index_bytes(index), false);
+    debug_range(dtable, vocab * hidden * sizeof(float), true);
+    debug_range(workspace, need, true);
+    EmbedArgs a = {};
+    a.dout = dout;
+    a.dtable = dtable;
+    a.ids = ids;
+    a.ids64 = index == LPCOLL_I64;
+    a.first_id = first_id;
+    a.scale = scale;
+    a.tokens = ntokens;
+    a.vocab = vocab;
+    a.hidden = hidden;
+    a.dtype = dtype;
+    a.accumulate = accumulate;
+    a.workspace = workspace;
+    return finish(launch_embed_backward(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -3,7 +3,10 @@ function per C entry point of that part of include/lpcoll.h, where their
 semantics stand: the router (``expert_route``), tokens sorted by expert, sent
 out as rows and brought back with their weights (``expert_sort``,
 ``expert_dispatch``, ``expert_combine``), the end of a block with its norms,
-gate and residual (``residual_norm``), and the gradients.
+gate and residual (``residual_norm``), layer norms (``layer_norm``), the end of a
+block with dropout (``residual_dropout``), the router's balance loss
+(``expert_balance``), the rows of a vocabulary shard (``token_embed``), and the
+gradients.
 
 As in ``_binding``, the functions check the torch tensors they are given
 (CUDA, on the current device, contiguous, of the right type and shape), pass
@@ -394,3 +397,215 @@ def residual_norm_backward(dx_out, dn_out, h, x_out, dx, dh, gate=None, w_post=N
         with _on(st, dev):
             dw_pre.detach().zero_()
     return dx, dh
+
+
+def _rows_of(h):
+    return (h,) if isinstance(h, torch.Tensor) else h
+
+
+def layer_norm(x, out, w=None, b=None, eps=1e-5, stream=None):
+    """Layer norm of the rows of x [T, H]: out = (x - mean) / sqrt(var + eps) *
+    w + b, with w, b [H] (None stands for ones and zeros)."""
+    dev = _device()
+    T, H = _shape(x, 2, "x")
+    dt = x.dtype
+    p = (_ptr(x, "x", dt, (T, H), dev), _opt(w, "w", dt, (H,), dev), _opt(b, "b", dt, (H,), dev),
+         _ptr(out, "out", dt, (T, H), dev))
+    B._check(B.lib().layer_norm(p[0], p[1], p[2], eps, T, H, _code(x), p[3],
+                                _stream(stream, dev)), "layer_norm")
+    return out
+
+
+def layer_norm_backward_workspace_bytes(ntokens, hidden, dtype):
+    """Scratch bytes of layer_norm_backward; dtype F32 or BF16."""
+    return B.lib().layer_norm_backward_workspace_bytes(ntokens, hidden, dtype)
+
+
+def layer_norm_backward(dout, x, dx=None, w=None, eps=1e-5, dw=None, db=None, workspace=None,
+                        stream=None):
+    """Gradients of layer_norm: dout and its input x -> dx and, where given, dw
+    and db (float32 [H])."""
+    dev = _device()
+    T, H = _shape(x, 2, "x")
+    dt, f32 = x.dtype, torch.float32
+    p = (_ptr(dout, "dout", dt, (T, H), dev), _ptr(x, "x", dt, (T, H), dev),
+         _opt(w, "w", dt, (H,), dev), _opt(dx, "dx", dt, (T, H), dev),
+         _opt(dw, "dw", f32, (H,), dev), _opt(db, "db", f32, (H,), dev))
+    L = B.lib()
+    code = _code(x)
+    sums = dw is not None or db is not None
+    need = L.layer_norm_backward_workspace_bytes(T, H, code) if sums else 0
+    st = _stream(stream, dev)
+    wp, wn, _keep = _scratch(workspace, need, st, dev)
+    B._check(L.layer_norm_backward(p[0], p[1], p[2], eps, T, H, code, p[3], p[4], p[5], wp, wn,
+                                   st), "layer_norm_backward")
+    return dx
+
+
+def residual_dropout(h, x, x_out, rng, p, n_out=None, w=None, b=None, eps=1e-5, first_row=0,
+                     stream=None):
+    """End of a block of a model with layer norms: h (one [T, H] tensor, or the
+    partial products of up to 16 ranks) is summed, dropped with probability p
+    (what stays is divided by 1 - p) and added to the residual x (or None):
+    x_out. With ``n_out``, the layer norm of x_out (w, b, eps). ``rng``: int64
+    [2] on the GPU, seed and offset (as 64 bits), read when the kernel runs; may
+    be None if p is 0. ``first_row`` numbers the rows of a part of a larger
+    batch."""
+    dev = _device()
+    h = _rows_of(h)
+    T, H = _shape(x_out, 2, "x_out")
+    dt = x_out.dtype
+    hp = [_ptr(t, "h", dt, (T, H), dev, r) for r, t in enumerate(h)]
+    if not 1 <= len(hp) <= B.MAX_RANKS:
+        raise ValueError("need 1 to %d ranks, got %d" % (B.MAX_RANKS, len(hp)))
+    if n_out is None and (w is not None or b is not None):
+        raise ValueError("w and b need n_out")
+    q = (_opt(x, "x", dt, (T, H), dev), _opt(rng, "rng", torch.int64, (2,), dev),
+         _opt(w, "w", dt, (H,), dev), _opt(b, "b", dt, (H,), dev),
+         _ptr(x_out, "x_out", dt, (T, H), dev), _opt(n_out, "n_out", dt, (T, H), dev))
+    B._check(B.lib().residual_dropout(_POINTERS[len(hp)](*hp), len(hp), q[0], q[1], p,
+                                      _row_number(first_row), q[2], q[3], eps, T, H,
+                                      _code(x_out), q[4], q[5], _stream(stream, dev)),
+             "residual_dropout")
+    return x_out, n_out
+
+
+def _row_number(first_row):
+    if first_row < 0:
+        raise ValueError("first_row must not be negative")
+    return first_row
+
+
+def residual_dropout_backward_workspace_bytes(ntokens, hidden, dtype):
+    """Scratch bytes of residual_dropout_backward; dtype F32 or BF16."""
+    return B.lib().residual_dropout_backward_workspace_bytes(ntokens, hidden, dtype)
+
+
+def residual_dropout_backward(dx_out, dn_out, x_out, dx, dh, rng, p, w=None, eps=1e-5, dw=None,
+                              db=None, first_row=0, workspace=None, stream=None):
+    """Gradients of residual_dropout: dx_out, dn_out (either may be None where that
+    output has no gradient or does not exist) and, with dn_out, the result x_out
+    -> dx (or None), dh (or None) and, where given, dw and db (float32 [H]; zeros
+    without dn_out). rng, p and first_row are the forward pass's."""
+    dev = _device()
+    like = dn_out if dn_out is not None else dx_out
+    if like is None:
+        raise ValueError("need dx_out or dn_out")
+    T, H = _shape(like, 2, "dn_out" if dn_out is not None else "dx_out")
+    dt, f32 = like.dtype, torch.float32
+    if dn_out is not None and x_out is None:
+        raise ValueError("dn_out needs x_out")
+    q = (_opt(dx_out, "dx_out", dt, (T, H), dev), _opt(dn_out, "dn_out", dt, (T, H), dev),
+         _opt(x_out, "x_out", dt, (T, H), dev), _opt(rng, "rng", torch.int64, (2,), dev),
+         _opt(w, "w", dt, (H,), dev), _opt(dx, "dx", dt, (T, H), dev),
+         _opt(dh, "dh", dt, (T, H), dev), _opt(dw, "dw", f32, (H,), dev),
+         _opt(db, "db", f32, (H,), dev))
+    L = B.lib()
+    code = _code(like)
+    need = 0
+    if dn_out is not None and (dw is not None or db is not None):
+        need = L.residual_dropout_backward_workspace_bytes(T, H, code)
+    st = _stream(stream, dev)
+    wp, wn, _keep = _scratch(workspace, need, st, dev)
+    B._check(L.residual_dropout_backward(q[0], q[1], q[2], q[3], p, _row_number(first_row), q[4],
+                                         eps, T, H, code, q[5], q[6], q[7], q[8], wp, wn, st),
+             "residual_dropout_backward")
+    return dx, dh
+
+
+def _valid(valid, ntokens, dev):
+    if valid is not None and isinstance(valid, torch.Tensor) and valid.dtype == torch.bool:
+        return _ptr(valid, "valid", torch.bool, (ntokens,), dev)
+    return _opt(valid, "valid", torch.uint8, (ntokens,), dev)
+
+
+def expert_balance_workspace_bytes(ntokens, nexperts):
+    """Scratch bytes of expert_balance."""
+    return B.lib().expert_balance_workspace_bytes(ntokens, nexperts)
+
+
+def expert_balance(logits, ids, loss, counts, prob_sums, coef=1.0, valid=None, workspace=None,
+                   stream=None):
+    """Balance loss of a router: logits [T, E] and the ids [T, K] that
+    expert_route chose -> loss (float32 [1]), counts (int32 [E + 1]: choices of
+    every expert, then the valid tokens) and prob_sums (float32 [E], the sums of
+    the softmax). ``valid`` (uint8 or bool [T]) is 0 where a token is padding."""
+    dev = _device()
+    T, E = _shape(logits, 2, "logits")
+    K = _topk(ids, T, "ids")
+    f32, i32 = torch.float32, torch.int32
+    p = (_ptr(logits, "logits", logits.dtype, (T, E), dev), _ptr(ids, "ids", i32, (T, K), dev),
+         _valid(valid, T, dev), _ptr(loss, "loss", f32, (1,), dev),
+         _ptr(counts, "counts", i32, (E + 1,), dev), _ptr(prob_sums, "prob_sums", f32, (E,), dev))
+    L = B.lib()
+    st = _stream(stream, dev)
+    wp, wn, _keep = _scratch(workspace, L.expert_balance_workspace_bytes(T, E), st, dev)
+    B._check(L.expert_balance(p[0], _code(logits), T, E, p[1], K, p[2], coef, p[3], p[4], p[5],
+                              wp, wn, st), "expert_balance")
+    return loss
+
+
+def expert_balance_backward(logits, counts, dloss, dlogits, coef=1.0, valid=None,
+                            accumulate=False, stream=None):
+    """dloss (float32 [1]) -> dlogits [T, E], for the counts that expert_balance
+    wrote (or their sums over ranks) and the same coef and valid. With
+    ``accumulate`` the gradient is added to dlogits, say to
+    expert_route_backward's."""
+    dev = _device()
+    T, E = _shape(logits, 2, "logits")
+    dt = logits.dtype
+    p = (_ptr(logits, "logits", dt, (T, E), dev), _valid(valid, T, dev),
+         _ptr(counts, "counts", torch.int32, (E + 1,), dev),
+         _ptr(dloss, "dloss", torch.float32, (1,), dev),
+         _ptr(dlogits, "dlogits", dt, (T, E), dev))
+    B._check(B.lib().expert_balance_backward(p[0], _code(logits), T, E, p[1], p[2], coef, p[3],
+                                             1 if accumulate else 0, p[4], _stream(stream, dev)),
+             "expert_balance_backward")
+    return dlogits
+
+
+def _ids(ids, dev):
+    """(pointer, type code, tokens) of the token ids, int32 or int64 [T]."""
+    T, = _shape(ids, 1, "ids")
+    if ids.dtype == torch.int64:
+        return _ptr(ids, "ids", torch.int64, (T,), dev), 1, T
+    return _ptr(ids, "ids", torch.int32, (T,), dev), 0, T
+
+
+def token_embed(table, ids, out, first_id=0, scale=1.0, stream=None):
+    """Rows of a shard of a vocabulary: table [V, H] holds the ids first_id ..
+    first_id + V - 1; out [T, H] = scale * table[ids - first_id], and zeros for
+    all other ids (int32 or int64 [T])."""
+    dev = _device()
+    ip, index, T = _ids(ids, dev)
+    V, H = _shape(table, 2, "table")
+    tp = _ptr(table, "table", table.dtype, (V, H), dev)
+    op = _ptr(out, "out", table.dtype, (T, H), dev)
+    B._check(B.lib().token_embed(tp, V, ip, index, first_id, T, H, _code(table), scale, op,
+                                 _stream(stream, dev)), "token_embed")
+    return out
+
+
+def token_embed_backward_workspace_bytes(ntokens, vocab, hidden):
+    """Scratch bytes of token_embed_backward."""
+    return B.lib().token_embed_backward_workspace_bytes(ntokens, vocab, hidden)
+
+
+def token_embed_backward(dout, ids, dtable, first_id=0, scale=1.0, accumulate=False,
+                         workspace=None, stream=None):
+    """dout [T, H] -> dtable (float32 [V, H]): every row the scaled sum of its
+    tokens' gradients, zeros in rows without a token. With ``accumulate`` the
+    sums are added to dtable, and rows without a token are not touched."""
+    dev = _device()
+    ip, index, T = _ids(ids, dev)
+    V, H = _shape(dtable, 2, "dtable")
+    gp = _ptr(dout, "dout", dout.dtype if isinstance(dout, torch.Tensor) else None, (T, H), dev)
+    tp = _ptr(dtable, "dtable", torch.float32, (V, H), dev)
+    L = B.lib()
+    st = _stream(stream, dev)
+    need = L.token_embed_backward_workspace_bytes(T, V, H)
+    wp, wn, _keep = _scratch(workspace, need, st, dev)
+    B._check(L.token_embed_backward(gp, ip, index, first_id, T, V, H, _code(dout), scale,
+                                    1 if accumulate else 0, tp, wp, wn, st),
+             "token_embed_backward")
+    return dtable
