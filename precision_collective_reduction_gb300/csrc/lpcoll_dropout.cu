@@ -12,76 +12,120 @@ namespace lpc {
 namespace {
 
 constexpr int kLanes = 256;  // of a CTA
+#ifndef DR_A
+#define DR_A 1
+#endif
+#ifndef DR_C
+#define DR_C 6
+#endif
+constexpr int kAhead = DR_A;    // pieces that a lane has in flight
 
-// Lanes per row: rows share a CTA where they are short.
-struct Rows {
-    unsigned segs;      // CTAs of a row
-    int lanes, per_cta;  // lanes of a row in a CTA, rows of a CTA
+// How rows are dealt out: `lanes` lanes of each of `segs` CTAs go through a row in
+// pieces of 16 bytes, `pieces` of them; short rows share a CTA, `rows` of them.
+struct Cut {
+    unsigned segs, pieces;
+    int lanes, rows;
 };
 
 template <int DT, int W>
-__global__ void __launch_bounds__(kLanes)
-dropout_kernel(const __grid_constant__ LayerNormArgs a, const Rows rows)
+__global__ void __launch_bounds__(kLanes, DR_C)
+dropout_kernel(const __grid_constant__ LayerNormArgs a, const Cut cut)
 {
     wait_prior_grid();
-    constexpr int kN = Pack<DT, W>::kN;      // columns of an access
-    constexpr int kCols = Fmt<DT>::kVec;     // of a lane
+    constexpr int kN = Pack<DT, W>::kN;   // columns of an access
+    constexpr int kCols = Fmt<DT>::kVec;  // of a piece
     constexpr int kPacks = kCols / kN;
-    const int which = static_cast<int>(threadIdx.x) / rows.lanes;
-    const int lane = static_cast<int>(threadIdx.x) - which * rows.lanes;
-    const size_t t = static_cast<size_t>(blockIdx.x / rows.segs) * rows.per_cta + which;
-    const size_t col = (static_cast<size_t>(blockIdx.x % rows.segs) * rows.lanes + lane) * kCols;
-    if (t >= a.tokens || col >= static_cast<size_t>(a.hidden))
-        return;
+    constexpr int kGroups = kCols / 4;
+    size_t t = blockIdx.x;
+    unsigned piece = threadIdx.x;
+    if (cut.segs > 1) {
+        t = blockIdx.x / cut.segs;
+        piece += blockIdx.x % cut.segs * cut.lanes;
+    } else if (cut.rows > 1) {
+        const unsigned which = threadIdx.x / cut.lanes;
+        t = t * cut.rows + which;
+        piece -= which * cut.lanes;
+    }
     const Philox rnd(a.drop, a.hidden);
-    const size_t e0 = t * a.hidden + col;
-    const auto has = [&](int i) { return W == 16 || col + i * kN < static_cast<size_t>(a.hidden); };
-    Vec<kN> x[kPacks], h[kPacks];
+    if (t >= a.tokens || (cut.segs == 1 && threadIdx.x >= static_cast<unsigned>(cut.lanes * cut.rows)))
+        return;
+    const unsigned step = cut.segs * cut.lanes;
+    const unsigned long long row = rnd.row(t);
+    const size_t e0 = t * a.hidden;
+    const bool drop = a.drop.least != 0;
+    for (; piece < cut.pieces; piece += kAhead * step) {
+        Vec<kN> h[kAhead][kPacks], x[kAhead][kPacks];
+        const auto col = [&](int u, int i) { return (piece + u * step) * kCols + i * kN; };
+        const auto has = [&](int u, int i) {
+            return W == 16 ? (u == 0 || piece + u * step < cut.pieces)
+                           : col(u, i) < static_cast<unsigned>(a.hidden);
+        };
 #pragma unroll
-    for (int i = 0; i < kPacks; ++i) {
-        if (!has(i))
-            continue;
-        h[i] = load_vec_of<DT, W>(a.h[0], e0 + i * kN);
-        if (a.x != nullptr)
-            x[i] = load_vec_of<DT, W>(a.x, e0 + i * kN);
-    }
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int i = 0; i < kPacks; ++i)
+                if (has(u, i)) {
+                    h[u][i] = load_vec_of<DT, W>(a.h[0], e0 + col(u, i));
+                    if (a.x != nullptr)
+                        x[u][i] = load_vec_of<DT, W>(a.x, e0 + col(u, i));
+                }
 #pragma unroll 4
-    for (int r = 1; r < a.nranks; ++r)
+        for (int r = 1; r < a.nranks; ++r)
 #pragma unroll
-        for (int i = 0; i < kPacks; ++i)
-            if (has(i))
-                h[i] = plus(h[i], load_vec_of<DT, W>(a.h[r], e0 + i * kN));
-    uint32_t bits = 0;
-    if (a.drop.least != 0) {
-        const unsigned long long group = rnd.row(t) + col / 4;
+            for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-        for (int q = 0; q < kCols / 4; ++q)
-            bits |= rnd.keep4(group + q) << (q * 4);
-    }
+                for (int i = 0; i < kPacks; ++i)
+                    if (has(u, i))
+                        h[u][i] = plus(h[u][i], load_vec_of<DT, W>(a.h[r], e0 + col(u, i)));
+        uint32_t word[kAhead * kCols];
+        if (drop) {
+            unsigned long long group[kAhead * kGroups];
 #pragma unroll
-    for (int i = 0; i < kPacks; ++i) {
-        if (!has(i))
-            continue;
-        if (a.dx != nullptr)  // gradient: of the residual, dx' itself
-            store_vec_of<DT, W>(a.dx, e0 + i * kN, h[i]);
-        if (a.x_out == nullptr)
-            continue;
-        Vec<kN> v = a.drop.least != 0 ? dropped(h[i], a.drop.scale, bits >> (i * kN)) : h[i];
-        if (a.x != nullptr)
-            v = plus(x[i], v);
-        store_vec_of<DT, W>(a.x_out, e0 + i * kN, v);
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int q = 0; q < kGroups; ++q)
+                    group[u * kGroups + q] = row + (piece + u * step) * kGroups + q;
+            rnd.words(group, word);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int i = 0; i < kPacks; ++i) {
+                if (!has(u, i))
+                    continue;
+                Vec<kN> v = h[u][i];
+                if (a.dx != nullptr)  // gradient: of the residual, dx' itself
+                    store_vec_of<DT, W>(a.dx, e0 + col(u, i), v);
+                if (a.x_out == nullptr)
+                    continue;
+                if (drop) {
+                    v = mul(a.drop.scale, v);
+#pragma unroll
+                    for (int j = 0; j < kN; ++j)
+                        v.v[j] = rnd.keep(v.v[j], word[u * kCols + i * kN + j]);
+                }
+                if (a.x != nullptr)
+                    v = plus(x[u][i], v);
+                store_vec_of<DT, W>(a.x_out, e0 + col(u, i), v);
+            }
     }
 }
 
+// A row's lanes have kAhead pieces or more; where there are few rows, more CTAs
+// share one and its lanes have one piece.
 template <int DT, int W> cudaError_t dropout_dt(const LayerNormArgs &a, cudaStream_t st)
 {
-    const size_t lanes = (static_cast<size_t>(a.hidden) + Fmt<DT>::kVec - 1) / Fmt<DT>::kVec;
-    Rows r;
-    r.segs = static_cast<unsigned>((lanes + kLanes - 1) / kLanes);
-    r.lanes = static_cast<int>((lanes + r.segs - 1) / r.segs);
-    r.per_cta = kLanes / r.lanes;
-    const size_t ctas = (a.tokens + r.per_cta - 1) / r.per_cta * r.segs;
-    return launch_kernel_block(dropout_kernel<DT, W>, ctas, r.lanes * r.per_cta, 0, st, a, r);
+    const size_t pieces = (a.hidden + Fmt<DT>::kVec - 1) / Fmt<DT>::kVec;
+    Cut c;
+    c.pieces = static_cast<unsigned>(pieces);
+    const bool few = a.tokens * pieces < static_cast<size_t>(kSms) * 4 * kLanes * kAhead;
+    const size_t lanes = few ? pieces : (pieces + kAhead - 1) / kAhead;
+    c.segs = few ? static_cast<unsigned>((pieces + kLanes - 1) / kLanes) : 1;
+    c.lanes = static_cast<int>(lanes < kLanes ? lanes : kLanes);
+    c.rows = c.segs > 1 ? 1 : kLanes / c.lanes;
+    const size_t ctas = (a.tokens + c.rows - 1) / c.rows * c.segs;
+    // whole warps, whose lanes behind the rows' do nothing
+    return launch_kernel_block(dropout_kernel<DT, W>, ctas, round_up(c.lanes * c.rows, 32), 0, st, a, c);
 }
 
 }  // namespace

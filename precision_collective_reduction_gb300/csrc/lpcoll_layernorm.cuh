@@ -120,41 +120,75 @@ __device__ __forceinline__ void team_moments(float s, float q, const S &share, f
     m2 = warp_sum(sq);
 }
 
-// The bits of this thread's columns in row t that dropout keeps, access c's kN
-// from bit c kN on. Where an access has fewer than a group's four columns, the
-// lanes of a group share its words: each makes the group of one access in turn.
-// (A CTA's first column is a multiple of 4: plans deal out whole groups.)
-template <int kElems, int kN, class M>
-__device__ __forceinline__ uint32_t keep_bits(const Philox &rnd, const M &me, size_t t)
-{
-    constexpr int NV = kElems / kN;
-    const unsigned long long row = rnd.row(t);
-    uint32_t bits = 0;
-    if constexpr (kN >= 4) {
+// What dropout keeps of this thread's columns of a row. An access of four columns
+// or more makes its groups' words where they are used. Where an access has fewer,
+// the lanes of a group share its words: each makes the group of one access in turn,
+// and a row's columns are one bit each. (A CTA's first column is a multiple of 4:
+// plans deal out whole groups.)
+template <int kElems, int kN> struct Keep {
+    unsigned long long row;
+    uint32_t bits;
+
+    template <class M>
+    __device__ __forceinline__ void make(const Philox &rnd, const M &me, size_t t)
+    {
+        row = rnd.row(t);
+        if constexpr (kN < 4) {
+            constexpr int Q = 4 / kN;  // lanes of a group
+            constexpr int kGroups = kElems / 4;
+            const int lane = threadIdx.x & 31, place = lane % Q;
+            bits = 0;
+            // access g Q + place of the group's first lane, two groups at a time
+            static_assert(kGroups % 2 == 0, "pairs of groups");
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            if (!me.has(c))
-                continue;
+            for (int g0 = 0; g0 < kGroups; g0 += 2) {
+                unsigned long long group[2];
 #pragma unroll
-            for (int q = 0; q < kN / 4; ++q)
-                bits |= rnd.keep4(row + (me.col(c) / 4 + q)) << (c * kN + q * 4);
-        }
-    } else {
-        constexpr int Q = 4 / kN;  // lanes of a group
-        const int lane = threadIdx.x & 31, place = lane % Q;
+                for (int g = 0; g < 2; ++g)
+                    group[g] = row + static_cast<unsigned>(me.col((g0 + g) * Q) +
+                                                           place * (32 - 1) * kN) / 4;
+                uint32_t w[8];
+                rnd.words(group, w);
 #pragma unroll
-        for (int c = 0; c < NV; c += Q) {
-            const int col = me.col(c) + place * (32 - 1) * kN;  // of the group's first lane, access c + place
-            const uint32_t four = rnd.keep4(row + static_cast<unsigned>(col) / 4);
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t four = 0;
 #pragma unroll
-            for (int j = 0; j < Q; ++j) {
-                const uint32_t other = __shfl_sync(kAll, four, (lane & ~(Q - 1)) + j);
-                bits |= (other >> (place * kN) & ((1u << kN) - 1u)) << ((c + j) * kN);
+                    for (int j = 0; j < 4; ++j)
+                        four |= w[4 * g + j] >= rnd.least ? 1u << j : 0u;
+#pragma unroll
+                    for (int j = 0; j < Q; ++j) {
+                        const uint32_t other = __shfl_sync(kAll, four, (lane & ~(Q - 1)) + j);
+                        bits |= (other >> (place * kN) & ((1u << kN) - 1u))
+                                << (((g0 + g) * Q + j) * kN);
+                    }
+                }
             }
         }
     }
-    return bits;
-}
+    // d of access c.
+    template <class M>
+    __device__ __forceinline__ Vec<kN> apply(const Philox &rnd, const M &me, const Vec<kN> &x,
+                                             float scale, int c) const
+    {
+        Vec<kN> r = mul(scale, x);
+        if constexpr (kN >= 4) {
+            unsigned long long group[kN / 4];
+#pragma unroll
+            for (int g = 0; g < kN / 4; ++g)
+                group[g] = row + static_cast<unsigned>(me.col(c) / 4 + g);
+            uint32_t w[kN];
+            rnd.words(group, w);
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+                r.v[j] = rnd.keep(r.v[j], w[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+                r.v[j] = (bits >> (c * kN + j) & 1u) != 0 ? r.v[j] : 0.0f;
+        }
+        return r;
+    }
+};
 
 // a + b in one rounding each.
 template <int N> __device__ __forceinline__ Vec<N> plus(const Vec<N> &a, const Vec<N> &b)
@@ -176,126 +210,238 @@ template <int N> __device__ __forceinline__ Vec<N> plus(const Vec<N> &a, const V
     return r;
 }
 
-// d of access c: 0 where a column is dropped, whatever it holds.
-template <int kN>
-__device__ __forceinline__ Vec<kN> dropped(const Vec<kN> &x, float scale, uint32_t bits)
+// warp_sum of N values side by side.
+template <int N> __device__ __forceinline__ void warp_sums(float (&x)[N])
 {
-    Vec<kN> r;
 #pragma unroll
-    for (int j = 0; j < kN; ++j)
-        r.v[j] = (bits >> j & 1u) != 0 ? __fmul_rn(x.v[j], scale) : 0.0f;
-    return r;
+    for (int m = 16; m >= 1; m >>= 1) {
+        float y[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            y[i] = __shfl_xor_sync(kAll, x[i], m);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] += y[i];
+    }
 }
 
-// Streams of a row: x if there is one, then the ranks' h.
-template <int DT, int W, int kElems, int kMode, bool kDrop>
-__global__ void __launch_bounds__(kMode == kWide ? kWideThreads : kThreadsOne<kElems>, 1)
+// Sums over a warp of three values of every lane: lane l returns that of value l % 4
+// (0 for 3), with 6 shuffles instead of 15.
+struct Three {
+    float v[3];
+};
+__device__ __forceinline__ float split_first(const Three &x, float &s1)
+{
+    const bool up = (threadIdx.x & 2) != 0;
+    const float g0 = up ? x.v[0] : x.v[2], g1 = up ? x.v[1] : 0.0f;
+    const float k0 = up ? x.v[2] : x.v[0], k1 = up ? 0.0f : x.v[1];
+    s1 = k1 + __shfl_xor_sync(kAll, g1, 2);
+    return k0 + __shfl_xor_sync(kAll, g0, 2);
+}
+__device__ __forceinline__ float split_second(float s0, float s1)
+{
+    const bool up = (threadIdx.x & 1) != 0;
+    const float give = up ? s0 : s1, keep = up ? s1 : s0;
+    return keep + __shfl_xor_sync(kAll, give, 1);
+}
+__device__ __forceinline__ float split_sum(const Three &x)
+{
+    float s1;
+    const float s0 = split_first(x, s1);
+    float s = split_second(s0, s1);
+#pragma unroll
+    for (int m = 4; m <= 16; m <<= 1)
+        s += __shfl_xor_sync(kAll, s, m);
+    return s;
+}
+// The sum of a thread's values as an accumulator of products with 1.
+template <int N> __device__ __forceinline__ void add_values(Acc<N> &acc, const Vec<N> &a)
+{
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j += 2)
+            acc = plus(acc, Vec<2>{{a.v[j], a.v[j + 1]}});
+    } else {
+        acc = plus(acc, a);
+    }
+}
+
+// A weight of ones, or a bias of zeros.
+template <int DT, int W> __device__ __forceinline__ typename Pack<DT, W>::Raw all_of(float v)
+{
+    float x[Pack<DT, W>::kN];
+#pragma unroll
+    for (int j = 0; j < Pack<DT, W>::kN; ++j)
+        x[j] = v;
+    return narrow_pack<DT, W>(x);
+}
+
+constexpr int kTeamThreads = 512;  // most threads of a CTA but kWide's
+
+// Forms of the kernels beside rows.cuh's: kEven has all its columns as kPlain has,
+// but any number of ranks, and the residual or not.
+constexpr int kEven = kWide + 1;
+
+// A team takes R rows at a time: with two, the steps of one fill the waits of the
+// other, and one barrier serves both. Streams of a row: x if there is one, then the
+// ranks' h.
+template <int DT, int W, int kElems, int kMode, bool kDrop, int R>
+__global__ void __launch_bounds__(kMode == kWide ? kWideThreads : kTeamThreads, 1)
 layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int streams)
 {
     wait_prior_grid();
     extern __shared__ uint4 ring_smem[];
-    __shared__ float2 red[2][kMaxWarps];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems, kMode, false> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
-    const Shares<NV, kN, kMode == kPlain> share(deal, a.hidden, me.first_warp);
-    const bool given = kMode == kPlain || a.x != nullptr;
-    const bool weighted = kMode == kPlain || a.w != nullptr;
-    const bool biased = kMode == kPlain || a.b != nullptr;
+    constexpr bool kAlone = kMode == kPlain || kMode == kEven;
+    __shared__ float2 red[2][R][kMaxWarps];
+    const Member<DT, W, kElems, kAlone ? kPlain : kMode, kAlone> me(deal, a, streams * R, reinterpret_cast<char *>(ring_smem));
+    const Shares<NV, kN, kAlone> share(deal, a.hidden, me.first_warp);
+    const bool given = kMode == kPlain || !kDrop || a.x != nullptr;
     const int h0 = given ? 1 : 0, nranks = !kDrop ? 0 : (kMode == kPlain ? 1 : a.nranks);
     const bool drop = kDrop && a.drop.least != 0;
     const Philox rnd(a.drop, a.hidden);
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
+    const int lane = threadIdx.x & 31, warps = deal.threads >> 5;
     const auto fetch = [&](size_t t, int stage) {
-        if (t < a.tokens) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const size_t row = t + i * me.step;
+            if (row >= a.tokens)
+                break;
             for (int r = 0; r < nranks; ++r)
-                me.copy(stage, h0 + r, a.h[r], t);
+                me.copy(stage, i * streams + h0 + r, a.h[r], row);
             if (given)
-                me.copy(stage, 0, a.x, t);
+                me.copy(stage, i * streams, a.x, row);
         }
         copy_commit();
     };
     for (int s = 0; s < deal.stages; ++s)
-        fetch(me.t0 + s * me.step, s);
+        fetch(me.t0 + s * R * me.step, s);
 
+    // In FP32 where they stay in registers for many rows.
     typename Pack<DT, W>::Raw w[NV], b[NV];
+    Vec<kN> wide_w[NV], wide_b[NV];
+    const auto weights = [&](int c) {
+        w[c] = a.w != nullptr && me.has(c) ? load_pack<DT, W>(a.w, me.col(c)) : all_of<DT, W>(1.0f);
+        b[c] = a.b != nullptr && me.has(c) ? load_pack<DT, W>(a.b, me.col(c)) : all_of<DT, W>(0.0f);
+    };
     if constexpr (kMode != kWide) {
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-            w[c] = b[c] = {};
-            if (me.has(c)) {
-                if (weighted)
-                    w[c] = load_pack<DT, W>(a.w, me.col(c));
-                if (biased)
-                    b[c] = load_pack<DT, W>(a.b, me.col(c));
-            }
+            weights(c);
+            wide_w[c] = unpack<DT, W>(w[c]);
+            wide_b[c] = unpack<DT, W>(b[c]);
         }
     }
 
     int stage = 0, turn = 0;
-    for (size_t t = me.t0; t < a.tokens; t += me.step, turn ^= 1) {
-        const uint32_t bits = drop ? keep_bits<kElems, kN>(rnd, me, t) : 0u;
+    for (size_t t = me.t0; t < a.tokens; t += R * me.step, turn ^= 1) {
         me.ready(deal.stages - 1);
-        Vec<kN> v[NV];
-        float sum = 0.0f;
+        Vec<kN> v[R][NV];
+        float sum[R], sq[R];
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            if (!me.has(c))
-                continue;
-            if constexpr (kDrop) {
-                Vec<kN> h = me.read(t, stage, h0, c);
+        for (int i = 0; i < R; ++i) {
+            const size_t row = t + i * me.step;
+            Keep<kElems, kN> keep;
+            if (drop)
+                keep.make(rnd, me, row);
+            Acc<kN> total = {};
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                if (!me.has(c))
+                    continue;
+                if constexpr (kDrop) {
+                    Vec<kN> h = me.read(row, stage, i * streams + h0, c);
 #pragma unroll 4
-                for (int r = 1; r < nranks; ++r)
-                    h = plus(h, me.read(t, stage, h0 + r, c));
-                if (drop)
-                    h = dropped(h, a.drop.scale, bits >> (c * kN));
-                v[c] = given ? plus(me.read(t, stage, 0, c), h) : h;
-                store_vec_of<DT, W>(a.x_out, me.elem(t, c), v[c]);
-            } else {
-                v[c] = me.read(t, stage, 0, c);
+                    for (int r = 1; r < nranks; ++r)
+                        h = plus(h, me.read(row, stage, i * streams + h0 + r, c));
+                    if (drop)
+                        h = keep.apply(rnd, me, h, a.drop.scale, c);
+                    v[i][c] = given ? plus(me.read(row, stage, i * streams, c), h) : h;
+                    if (R == 1 || row < a.tokens)
+                        store_vec_of<DT, W>(a.x_out, me.elem(row, c), v[i][c]);
+                } else {
+                    v[i][c] = me.read(row, stage, i, c);
+                }
+                add_values<kN>(total, v[i][c]);
             }
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                sum += v[c].v[j];
+            sum[i] = fold(total);
         }
-        fetch(t + deal.stages * me.step, stage);
+        fetch(t + deal.stages * R * me.step, stage);
         stage = stage + 1 == deal.stages ? 0 : stage + 1;
-        sum = warp_sum(sum);
-        const Vec<kN> about = splat<kN>(-(sum * share.inv_own));
-        Acc<kN> sq = {};
+        warp_sums(sum);
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            if (!me.has(c))
-                continue;
-            const Vec<kN> d = plus(v[c], about);
-            add_products(sq, d, d);
-        }
-        float mean, m2;
-        team_moments(sum, warp_sum(fold(sq)), share, red[turn], deal, me.first_warp, a.hidden,
-                     per_hidden, kMode == kPlain || deal.cluster == 1, mean, m2);
-        const float r = inv_rms(m2, per_hidden, a.eps);
-        const Vec<kN> centre = splat<kN>(-mean);
+        for (int i = 0; i < R; ++i) {
+            const Vec<kN> about = splat<kN>(-(sum[i] * share.inv_own));
+            Acc<kN> squares = {};
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            if (!me.has(c))
-                continue;
-            Vec<kN> n = mul(r, plus(v[c], centre));
-            if constexpr (kMode == kWide) {
-                if (weighted)
-                    n = mul(n, load_vec_of<DT, W>(a.w, me.col(c)));
-                if (biased)
-                    n = plus(n, load_vec_of<DT, W>(a.b, me.col(c)));
-            } else if (weighted && biased) {
-                n = fma(n, unpack<DT, W>(w[c]), unpack<DT, W>(b[c]));
-            } else if (weighted) {
-                n = mul(n, unpack<DT, W>(w[c]));
-            } else if (biased) {
-                n = plus(n, unpack<DT, W>(b[c]));
+            for (int c = 0; c < NV; ++c) {
+                if (!me.has(c))
+                    continue;
+                const Vec<kN> d = plus(v[i][c], about);
+                add_products(squares, d, d);
             }
-            store_vec_of<DT, W>(a.n_out, me.elem(t, c), n);
+            sq[i] = fold(squares);
+        }
+        warp_sums(sq);
+        float mean[R], m2[R];
+        if constexpr (kAlone) {
+            float2 e[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                e[i] = lane == 0 ? make_float2(sum[i], sq[i]) : make_float2(0.0f, 0.0f);
+            if (warps > 1) {
+                if (lane == 0)
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        red[turn][i][threadIdx.x >> 5] = e[i];
+                __syncwarp();
+                team_barrier(deal);
+                if (lane < warps)
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        e[i] = red[turn][i][me.first_warp + lane];
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                mean[i] = e[i].x;
+            warp_sums(mean);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                mean[i] *= per_hidden;
+                const float d = fmaf(e[i].x, share.inv0, -mean[i]);
+                m2[i] = fmaf(share.n0 * d, d, e[i].y);
+            }
+            warp_sums(m2);
+        } else {
+            team_moments(sum[0], sq[0], share, red[turn][0], deal, me.first_warp, a.hidden,
+                         per_hidden, deal.cluster == 1, mean[0], m2[0]);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const size_t row = t + i * me.step;
+            if (R > 1 && row >= a.tokens)
+                break;
+            const float r = inv_rms(m2[i], per_hidden, a.eps);
+            const Vec<kN> centre = splat<kN>(-mean[i]);
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                if (!me.has(c))
+                    continue;
+                const Vec<kN> n = mul(r, plus(v[i][c], centre));
+                if constexpr (kMode == kWide) {
+                    weights(c);
+                    store_vec_of<DT, W>(a.n_out, me.elem(row, c),
+                                        fma(n, unpack<DT, W>(w[c]), unpack<DT, W>(b[c])));
+                } else {
+                    store_vec_of<DT, W>(a.n_out, me.elem(row, c), fma(n, wide_w[c], wide_b[c]));
+                }
+            }
         }
     }
-    if (kMode != kPlain && deal.cluster > 1)
+    copy_wait(0);
+    if (!kAlone && deal.cluster > 1)
         cluster_barrier();  // no CTA leaves while another reads its sums
 }
 
@@ -308,53 +454,74 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int 
 // Row streams of a stage.
 enum GradStream { kGradX = 0, kGradDn = 1, kGradDx = 2 };
 
-// The sums of a row in the gradient: s, and about the warp's mean the squares m2
-// and a = sum q (x - mean_w), and q.
+// The sums of a row in the gradient: about the warp's mean the squares m2 and
+// a = sum q (x - mean_w), then q, and the sum of x. A warp leaves them as four floats,
+// lane l < 4 value l; `mine` is that value.
+struct RowSums {
+    float mean, m2, a, q;
+};
+constexpr int kSumOfX = 3;
+
 template <class S>
-__device__ __forceinline__ float4 team_grad_sums(float4 mine, const S &share, float4 *red,
-                                                 const Deal &deal, int first_warp, int hidden,
-                                                 float per_hidden, bool alone)
+__device__ __forceinline__ Three moved(const float4 &v, const S &share, float mean)
+{
+    const float d = fmaf(v.w, share.inv0, -mean);
+    return {{fmaf(share.n0 * d, d, v.x), fmaf(d, v.z, v.y), v.z}};
+}
+
+__device__ __forceinline__ RowSums spread(float mean, float mine)
+{
+    return {mean, __shfl_sync(kAll, mine, 0), __shfl_sync(kAll, mine, 1),
+            __shfl_sync(kAll, mine, 2)};
+}
+
+template <class S>
+__device__ __forceinline__ RowSums team_grad_sums(float mine, float sum, const S &share,
+                                                  float4 *red, const Deal &deal, int first_warp,
+                                                  int hidden, float per_hidden, bool alone)
 {
     const int lane = threadIdx.x & 31, warps = deal.threads >> 5;
     if (warps == 1 && alone)
-        return make_float4(mine.x * share.inv_own, mine.y, mine.z, mine.w);
-    if (lane == 0)
-        red[threadIdx.x >> 5] = mine;
+        return spread(sum * share.inv_own, mine);
+    if (lane < 4)
+        reinterpret_cast<float *>(red + (threadIdx.x >> 5))[lane] = lane == kSumOfX ? sum : mine;
     __syncwarp();
     team_barrier(deal);
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (alone) {
         const float4 v = lane < warps ? red[first_warp + lane] : zero;
-        const float mean = warp_sum(v.x) * per_hidden;
-        const float d = fmaf(v.x, share.inv0, -mean);
-        return make_float4(mean, warp_sum(fmaf(share.n0 * d, d, v.y)), warp_sum(fmaf(d, v.w, v.z)),
-                           warp_sum(v.w));
+        const float mean = warp_sum(v.w) * per_hidden;
+        return spread(mean, split_sum(moved(v, share, mean)));
     }
     float4 v[kMaxCluster];
-    float sum = 0.0f, q = 0.0f, m2 = 0.0f, at = 0.0f;
+    float all = 0.0f;
 #pragma unroll
     for (int c = 0; c < kMaxCluster; ++c) {
         v[c] = c < deal.cluster && lane < warps ? cluster_load4(red + lane, c) : zero;
-        sum += v[c].x;
-        q += v[c].w;
+        all += v[c].w;
     }
-    const float mean = warp_sum(sum) * per_hidden;
+    const float mean = warp_sum(all) * per_hidden;
+    Three s = {};
 #pragma unroll
     for (int c = 0; c < kMaxCluster; ++c) {
         if (c >= deal.cluster)
             break;
         const float n = share.columns(deal, hidden, c);
-        const float d = fmaf(v[c].x, share.inverse(n), -mean);
+        const float d = fmaf(v[c].w, share.inverse(n), -mean);
         if (lane < warps && n > 0.0f) {
-            m2 += fmaf(n * d, d, v[c].y);
-            at += fmaf(d, v[c].w, v[c].z);
+            s.v[0] += fmaf(n * d, d, v[c].x);
+            s.v[1] += fmaf(d, v[c].z, v[c].y);
+            s.v[2] += v[c].z;
         }
     }
-    return make_float4(mean, warp_sum(m2), warp_sum(at), warp_sum(q));
+    return spread(mean, split_sum(s));
 }
 
+// A row's x, less the warp's mean, and dn stay in registers in FP32 from the sums to
+// the outputs, as do the weights: reading them again from shared memory costs the
+// conversions again.
 template <int DT, int W, int kElems, int kMode, bool kDrop>
-__global__ void __launch_bounds__(kThreadsOne<kElems>, 1)
+__global__ void __launch_bounds__(kTeamThreads, 1)
 layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int streams)
 {
     wait_prior_grid();
@@ -362,9 +529,9 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
     __shared__ float4 red[2][kMaxWarps];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems, kMode, kMode == kPlain> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
-    const Shares<NV, kN, kMode == kPlain> share(deal, a.hidden, me.first_warp);
-    const bool weighted = kMode == kPlain || a.w != nullptr;
+    constexpr bool kAlone = kMode == kPlain;
+    const Member<DT, W, kElems, kMode, kAlone> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
+    const Shares<NV, kN, kAlone> share(deal, a.hidden, me.first_warp);
     const bool given = kDrop && (kMode == kPlain || a.dx_out != nullptr);
     const bool want_dx = kMode == kPlain || a.dx != nullptr;
     const bool want_dh = kDrop && (kMode == kPlain || a.dh != nullptr);
@@ -383,77 +550,67 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
     for (int s = 0; s < deal.stages; ++s)
         fetch(me.t0 + s * me.step, s);
 
-    typename Pack<DT, W>::Raw w[NV];
-    Vec<kN> s_w[NV], s_b[NV];
+    Vec<kN> w[NV], s_w[NV], s_b[NV];
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-        w[c] = {};
-        if (weighted && me.has(c))
-            w[c] = load_pack<DT, W>(a.w, me.col(c));
+        w[c] = a.w != nullptr && me.has(c) ? load_vec_of<DT, W>(a.w, me.col(c)) : splat<kN>(1.0f);
         s_w[c] = s_b[c] = splat<kN>(0.0f);
     }
 
     int stage = 0, turn = 0;
     for (size_t t = me.t0; t < a.tokens; t += me.step, turn ^= 1) {
-        const uint32_t bits = drop ? keep_bits<kElems, kN>(rnd, me, t) : 0u;
         me.ready(deal.stages - 1);
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        Vec<kN> d[NV], dn[NV];
+        Acc<kN> total = {}, sq = {}, sa = {}, sqs = {};
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             if (!me.has(c))
                 continue;
-            const Vec<kN> x = me.read(t, stage, kGradX, c);
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                s.x += x.v[j];
+            d[c] = me.read(t, stage, kGradX, c);
+            dn[c] = me.read(t, stage, kGradDn, c);
+            add_values<kN>(total, d[c]);
         }
-        s.x = warp_sum(s.x);
-        const Vec<kN> about = splat<kN>(-(s.x * share.inv_own));
-        Acc<kN> sq = {}, sa = {};
+        const float sum = warp_sum(fold(total));
+        const float own = sum * share.inv_own;  // the warp's mean
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             if (!me.has(c))
                 continue;
-            const Vec<kN> d = plus(me.read(t, stage, kGradX, c), about);
-            Vec<kN> q = me.read(t, stage, kGradDn, c);
-            if (weighted)
-                q = mul(q, unpack<DT, W>(w[c]));
-            add_products(sq, d, d);
-            add_products(sa, q, d);
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                s.w += q.v[j];
+            d[c] = plus(d[c], splat<kN>(-own));
+            const Vec<kN> q = mul(dn[c], w[c]);
+            add_products(sq, d[c], d[c]);
+            add_products(sa, q, d[c]);
+            add_values<kN>(sqs, q);
         }
-        s = team_grad_sums(make_float4(s.x, warp_sum(fold(sq)), warp_sum(fold(sa)), warp_sum(s.w)),
-                           share, red[turn], deal, me.first_warp, a.hidden, per_hidden,
-                           kMode == kPlain || deal.cluster == 1);
-        const float r = inv_rms(s.y, per_hidden, a.eps);
-        const float c1 = s.w * per_hidden, c2 = r * r * (s.z * per_hidden);
-        const Vec<kN> centre = splat<kN>(-s.x);
+        const RowSums s = team_grad_sums(split_sum({{fold(sq), fold(sa), fold(sqs)}}), sum, share,
+                                         red[turn], deal, me.first_warp, a.hidden, per_hidden,
+                                         kAlone || deal.cluster == 1);
+        Keep<kElems, kN> keep;
+        if (drop)
+            keep.make(rnd, me, t);
+        const float r = inv_rms(s.m2, per_hidden, a.eps);
+        const float c1 = s.q * per_hidden, c2 = r * r * (s.a * per_hidden);
+        const Vec<kN> centre = splat<kN>(own - s.mean);
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             if (!me.has(c))
                 continue;
-            const Vec<kN> d = plus(me.read(t, stage, kGradX, c), centre);
-            const Vec<kN> dn = me.read(t, stage, kGradDn, c);
-            s_w[c] = fma(mul(r, d), dn, s_w[c]);
-            s_b[c] = plus(s_b[c], dn);
-            Vec<kN> q = dn;
-            if (weighted)
-                q = mul(q, unpack<DT, W>(w[c]));
-            q = fma(-c2, d, plus(q, splat<kN>(-c1)));
+            const Vec<kN> x = plus(d[c], centre);
+            s_w[c] = fma(mul(r, x), dn[c], s_w[c]);
+            s_b[c] = plus(s_b[c], dn[c]);
+            Vec<kN> q = fma(-c2, x, fma(dn[c], w[c], splat<kN>(-c1)));
             q = given ? fma(r, q, me.read(t, stage, kGradDx, c)) : mul(r, q);
             if (want_dx)
                 store_vec_of<DT, W>(a.dx, me.elem(t, c), q);
             if (want_dh)
                 store_vec_of<DT, W>(a.dh, me.elem(t, c),
-                                    drop ? dropped(q, a.drop.scale, bits >> (c * kN)) : q);
+                                    drop ? keep.apply(rnd, me, q, a.drop.scale, c) : q);
         }
         fetch(t + deal.stages * me.step, stage);
         stage = stage + 1 == deal.stages ? 0 : stage + 1;
     }
     copy_wait(0);
-    if (kMode != kPlain && deal.cluster > 1)
+    if (!kAlone && deal.cluster > 1)
         cluster_barrier();  // no CTA leaves while another reads its sums
     if (a.partial != nullptr)
         leave_sums(me, deal, s_w, s_b, a.partial, reinterpret_cast<float *>(ring_smem));
@@ -466,11 +623,12 @@ inline int group_packs(int hidden, int dtype)
     return kn < 4 ? 4 / kn : 1;
 }
 
+// `even` rows may be taken two at a time.
 Plan layer_norm_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
 {
     const int width = row_width(hidden, dtype);
     const int kn = width / static_cast<int>(dtype_bytes(dtype));
-    constexpr int kRow = 8192;  // columns of the largest CTA
+    constexpr int kRow = 16 * kTeamThreads;  // columns of the largest CTA but kWide's
     Plan p;
     p.wide = !gradient && tokens > kSms && hidden > kRow && width == 16 &&
              static_cast<size_t>(hidden) * width / kn * streams <= kSmemOne;
@@ -483,9 +641,14 @@ Plan layer_norm_plan(size_t tokens, int hidden, int dtype, int streams, bool gra
     while (!p.wide && cluster < kMaxCluster &&
            (static_cast<size_t>(hidden) * width / kn / cluster + 2048) * streams > kSmemOne)
         cluster *= 2;
-    p.elems = !p.wide && (hidden <= 256 || tokens <= kSms) ? 8 : 16;
-    return deal_rows(p, cluster, tokens, hidden, dtype, streams, gradient,
-                     group_packs(hidden, dtype));
+    p.elems = !p.wide && (hidden <= 256 || (tokens <= kSms && hidden <= kRow / 2 * cluster)) ? 8 : 16;
+    const int room = p.wide ? kWideThreads : kTeamThreads, multiple = group_packs(hidden, dtype);
+    if (!gradient && !p.wide && cluster == 1 && p.elems == 16) {
+        const Plan two = deal_rows(p, cluster, tokens, hidden, dtype, streams, false, room, multiple, 2);
+        if (two.even && two.smem <= kSmemOne)
+            return two;
+    }
+    return deal_rows(p, cluster, tokens, hidden, dtype, streams, gradient, room, multiple);
 }
 
 template <int DT, int W, bool kDrop>
@@ -495,15 +658,24 @@ cudaError_t layer_norm_dt(const LayerNormArgs &a, cudaStream_t st)
     const Plan p = layer_norm_plan(a.tokens, a.hidden, a.dtype, streams, false);
     if constexpr (W == 16) {
         if (p.wide)
-            return launch_plan(layer_norm_kernel<DT, W, 16, kWide, kDrop>, a, p, streams, st);
-        if (p.even && p.deal.cluster == 1 && a.w != nullptr && a.b != nullptr && a.x != nullptr &&
-            a.nranks <= 1)
-            return launch_plan(p.elems == 8 ? layer_norm_kernel<DT, W, 8, kPlain, kDrop>
-                                            : layer_norm_kernel<DT, W, 16, kPlain, kDrop>,
-                               a, p, streams, st);
+            return launch_plan(layer_norm_kernel<DT, W, 16, kWide, kDrop, 1>, a, p, streams, st);
+        if (p.even && p.deal.cluster == 1) {
+            const bool plain = a.x != nullptr && a.nranks <= 1;
+            if (plain && p.elems == 8)
+                return launch_plan(layer_norm_kernel<DT, W, 8, kPlain, kDrop, 1>, a, p, streams, st);
+            if (plain && p.rows == 2)
+                return launch_plan(layer_norm_kernel<DT, W, 16, kPlain, kDrop, 2>, a, p, streams, st);
+            if constexpr (kDrop) {
+                if (p.elems == 8)
+                    return launch_plan(layer_norm_kernel<DT, W, 8, kEven, true, 1>, a, p, streams, st);
+                return launch_plan(p.rows == 2 ? layer_norm_kernel<DT, W, 16, kEven, true, 2>
+                                               : layer_norm_kernel<DT, W, 16, kEven, true, 1>,
+                                   a, p, streams, st);
+            }
+        }
     }
-    return launch_plan(p.elems == 8 ? layer_norm_kernel<DT, W, 8, kGeneral, kDrop>
-                                    : layer_norm_kernel<DT, W, 16, kGeneral, kDrop>,
+    return launch_plan(p.elems == 8 ? layer_norm_kernel<DT, W, 8, kGeneral, kDrop, 1>
+                                    : layer_norm_kernel<DT, W, 16, kGeneral, kDrop, 1>,
                        a, p, streams, st);
 }
 
@@ -519,7 +691,7 @@ cudaError_t layer_norm_backward_dt(const LayerNormArgs &a, const Plan &p, cudaSt
 {
     const int streams = kDrop ? 3 : 2;
     if constexpr (W == 16) {
-        if (p.even && p.deal.cluster == 1 && a.w != nullptr && a.dx != nullptr &&
+        if (p.even && p.deal.cluster == 1 && a.dx != nullptr &&
             (!kDrop || (a.dx_out != nullptr && a.dh != nullptr)))
             return launch_plan(p.elems == 8 ? layer_norm_backward_kernel<DT, W, 8, kPlain, kDrop>
                                             : layer_norm_backward_kernel<DT, W, 16, kPlain, kDrop>,

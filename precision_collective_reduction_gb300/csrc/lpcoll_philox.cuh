@@ -13,6 +13,7 @@
 
 namespace lpc {
 
+// Made by whole warps.
 struct Philox {
     uint32_t key0, key1, offset0, offset1, least;
     unsigned long long first_row, groups;
@@ -24,8 +25,10 @@ struct Philox {
             seed = a.rng[0];
             offset = a.rng[1];
         }
-        key0 = static_cast<uint32_t>(seed);
-        key1 = static_cast<uint32_t>(seed >> 32);
+        // the same in every lane: said by a warp-wide OR, it keeps the rounds' keys out
+        // of the lanes' registers
+        key0 = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(seed));
+        key1 = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(seed >> 32));
         offset0 = static_cast<uint32_t>(offset);
         offset1 = static_cast<uint32_t>(offset >> 32);
         least = a.least;
@@ -37,24 +40,40 @@ struct Philox {
     {
         return (first_row + t) * groups;
     }
-    // Bit j: column j of the group is kept.
-    __device__ __forceinline__ uint32_t keep4(unsigned long long group) const
+    // The words of N groups, round by round side by side: their keys are the same,
+    // and one chain of products alone would wait for itself.
+    template <int N>
+    __device__ __forceinline__ void words(const unsigned long long (&group)[N],
+                                          uint32_t (&w)[4 * N]) const
     {
-        uint32_t c0 = static_cast<uint32_t>(group), c1 = static_cast<uint32_t>(group >> 32);
-        uint32_t c2 = offset0, c3 = offset1, k0 = key0, k1 = key1;
+        uint32_t k0 = key0, k1 = key1;
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+            w[4 * g] = static_cast<uint32_t>(group[g]);
+            w[4 * g + 1] = static_cast<uint32_t>(group[g] >> 32);
+            w[4 * g + 2] = offset0;
+            w[4 * g + 3] = offset1;
+        }
 #pragma unroll
         for (int i = 0; i < 10; ++i) {
-            const unsigned long long a = static_cast<unsigned long long>(c0) * 0xD2511F53u;
-            const unsigned long long b = static_cast<unsigned long long>(c2) * 0xCD9E8D57u;
-            c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
-            c1 = static_cast<uint32_t>(b);
-            c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
-            c3 = static_cast<uint32_t>(a);
+#pragma unroll
+            for (int g = 0; g < N; ++g) {
+                uint32_t *const c = w + 4 * g;
+                const unsigned long long a = static_cast<unsigned long long>(c[0]) * 0xD2511F53u;
+                const unsigned long long b = static_cast<unsigned long long>(c[2]) * 0xCD9E8D57u;
+                c[0] = static_cast<uint32_t>(b >> 32) ^ c[1] ^ k0;
+                c[1] = static_cast<uint32_t>(b);
+                c[2] = static_cast<uint32_t>(a >> 32) ^ c[3] ^ k1;
+                c[3] = static_cast<uint32_t>(a);
+            }
             k0 += 0x9E3779B9u;
             k1 += 0xBB67AE85u;
         }
-        return (c0 >= least ? 1u : 0u) | (c1 >= least ? 2u : 0u) | (c2 >= least ? 4u : 0u) |
-               (c3 >= least ? 8u : 0u);
+    }
+    // 0 where a column is dropped, whatever it holds.
+    __device__ __forceinline__ float keep(float x, uint32_t word) const
+    {
+        return word >= least ? x : 0.0f;
     }
 };
 

@@ -527,6 +527,7 @@ struct Plan {
     bool even;    // every thread has all its columns
     bool wide;    // kWide (forward only)
     int ctas;     // CTAs, or clusters of them, that share the rows
+    int rows;     // that a team takes at a time
     size_t smem;  // dynamic shared memory of a CTA
 };
 
@@ -535,20 +536,22 @@ constexpr size_t kSmem[kMaxCtas] = {224 * 1024, 110 * 1024, 72 * 1024};
 constexpr size_t kSmemOne = kSmem[0];
 
 // The rest of a plan whose columns per thread and form are chosen, for rows over
-// `cluster` CTAs. A CTA's part of a row is a multiple of `multiple` accesses;
-// `gradient`: the teams of a CTA add up two sums of every column at the end.
+// `cluster` CTAs. A CTA's part of a row is a multiple of `multiple` accesses, an SM
+// holds `room` threads; `gradient`: the teams of a CTA add up two sums of every
+// column at the end; `rows_of_turn`: rows that a team takes at a time.
 inline Plan deal_rows(Plan p, int cluster, size_t tokens, int hidden, int dtype, int streams,
-                      bool gradient, int multiple)
+                      bool gradient, int room, int multiple = 1, int rows_of_turn = 1)
 {
+    p.rows = rows_of_turn;
+    streams *= rows_of_turn;
     const int width = row_width(hidden, dtype);
     const int kn = width / static_cast<int>(dtype_bytes(dtype));
     Deal &d = p.deal;
     d.cluster = cluster;
     d.packs = round_up(((hidden + kn - 1) / kn + cluster - 1) / cluster, multiple);
     d.threads = round_up((d.packs + p.elems / kn - 1) / (p.elems / kn), 32);
-    const int room = p.wide ? kWideThreads : (p.elems == 8 ? kThreadsOne<8> : kThreadsOne<16>);
     d.groups = cluster > 1 || d.threads * 4 > room ? 1 : room / 2 / d.threads;
-    // one row of each of a CTA's teams, in all streams
+    // the rows that each of a CTA's teams takes at a time, in all streams
     const size_t row =
         static_cast<size_t>(row_part_bytes(width, d.packs, d.threads, p.elems)) * streams;
     while (d.groups > 1 && row * d.groups > kSmem[1])
@@ -559,7 +562,8 @@ inline Plan deal_rows(Plan p, int cluster, size_t tokens, int hidden, int dtype,
     per_sm = per_sm < 1 ? 1 : (per_sm > kMaxCtas ? kMaxCtas : per_sm);
     while (per_sm > 1 && row * d.groups > kSmem[per_sm - 1])
         --per_sm;
-    const size_t steps = (tokens + d.groups - 1) / d.groups;
+    const size_t at_once = static_cast<size_t>(d.groups) * rows_of_turn;
+    const size_t steps = (tokens + at_once - 1) / at_once;
     const size_t most = static_cast<size_t>(kSms) * per_sm / cluster;
     p.ctas = static_cast<int>(steps < most ? steps : most);
     const size_t stage = row * d.groups;
