@@ -12,14 +12,6 @@ namespace lpc {
 namespace {
 
 constexpr int kLanes = 256;  // of a CTA
-#ifndef DR_A
-#define DR_A 1
-#endif
-#ifndef DR_C
-#define DR_C 6
-#endif
-constexpr int kAhead = DR_A;    // pieces that a lane has in flight
-
 // How rows are dealt out: `lanes` lanes of each of `segs` CTAs go through a row in
 // pieces of 16 bytes, `pieces` of them; short rows share a CTA, `rows` of them.
 struct Cut {
@@ -28,7 +20,7 @@ struct Cut {
 };
 
 template <int DT, int W>
-__global__ void __launch_bounds__(kLanes, DR_C)
+__global__ void __launch_bounds__(kLanes, DT == LPCOLL_F32 ? 8 : 6)
 dropout_kernel(const __grid_constant__ LayerNormArgs a, const Cut cut)
 {
     wait_prior_grid();
@@ -49,79 +41,68 @@ dropout_kernel(const __grid_constant__ LayerNormArgs a, const Cut cut)
     const Philox rnd(a.drop, a.hidden);
     if (t >= a.tokens || (cut.segs == 1 && threadIdx.x >= static_cast<unsigned>(cut.lanes * cut.rows)))
         return;
-    const unsigned step = cut.segs * cut.lanes;
     const unsigned long long row = rnd.row(t);
-    const size_t e0 = t * a.hidden;
     const bool drop = a.drop.least != 0;
-    for (; piece < cut.pieces; piece += kAhead * step) {
-        Vec<kN> h[kAhead][kPacks], x[kAhead][kPacks];
-        const auto col = [&](int u, int i) { return (piece + u * step) * kCols + i * kN; };
-        const auto has = [&](int u, int i) {
-            return W == 16 ? (u == 0 || piece + u * step < cut.pieces)
-                           : col(u, i) < static_cast<unsigned>(a.hidden);
+    for (; piece < cut.pieces; piece += cut.segs * cut.lanes) {
+        const unsigned col = piece * kCols;
+        const size_t e0 = t * a.hidden + col;
+        const auto has = [&](int i) {
+            return W == 16 || col + i * kN < static_cast<unsigned>(a.hidden);
         };
+        Vec<kN> h[kPacks], x[kPacks];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-            for (int i = 0; i < kPacks; ++i)
-                if (has(u, i)) {
-                    h[u][i] = load_vec_of<DT, W>(a.h[0], e0 + col(u, i));
-                    if (a.x != nullptr)
-                        x[u][i] = load_vec_of<DT, W>(a.x, e0 + col(u, i));
-                }
+        for (int i = 0; i < kPacks; ++i)
+            if (has(i)) {
+                h[i] = load_vec_of<DT, W>(a.h[0], e0 + i * kN);
+                if (a.x != nullptr)
+                    x[i] = load_vec_of<DT, W>(a.x, e0 + i * kN);
+            }
 #pragma unroll 4
         for (int r = 1; r < a.nranks; ++r)
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-                for (int i = 0; i < kPacks; ++i)
-                    if (has(u, i))
-                        h[u][i] = plus(h[u][i], load_vec_of<DT, W>(a.h[r], e0 + col(u, i)));
-        uint32_t word[kAhead * kCols];
+            for (int i = 0; i < kPacks; ++i)
+                if (has(i))
+                    h[i] = plus(h[i], load_vec_of<DT, W>(a.h[r], e0 + i * kN));
+        uint32_t word[kCols];
         if (drop) {
-            unsigned long long group[kAhead * kGroups];
+            unsigned long long group[kGroups];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-                for (int q = 0; q < kGroups; ++q)
-                    group[u * kGroups + q] = row + (piece + u * step) * kGroups + q;
+            for (int q = 0; q < kGroups; ++q)
+                group[q] = row + piece * kGroups + q;
             rnd.words(group, word);
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
+        for (int i = 0; i < kPacks; ++i) {
+            if (!has(i))
+                continue;
+            Vec<kN> v = h[i];
+            if (a.dx != nullptr)  // gradient: of the residual, dx' itself
+                store_vec_of<DT, W>(a.dx, e0 + i * kN, v);
+            if (a.x_out == nullptr)
+                continue;
+            if (drop) {
+                v = mul(a.drop.scale, v);
 #pragma unroll
-            for (int i = 0; i < kPacks; ++i) {
-                if (!has(u, i))
-                    continue;
-                Vec<kN> v = h[u][i];
-                if (a.dx != nullptr)  // gradient: of the residual, dx' itself
-                    store_vec_of<DT, W>(a.dx, e0 + col(u, i), v);
-                if (a.x_out == nullptr)
-                    continue;
-                if (drop) {
-                    v = mul(a.drop.scale, v);
-#pragma unroll
-                    for (int j = 0; j < kN; ++j)
-                        v.v[j] = rnd.keep(v.v[j], word[u * kCols + i * kN + j]);
-                }
-                if (a.x != nullptr)
-                    v = plus(x[u][i], v);
-                store_vec_of<DT, W>(a.x_out, e0 + col(u, i), v);
+                for (int j = 0; j < kN; ++j)
+                    v.v[j] = rnd.keep(v.v[j], word[i * kN + j]);
             }
+            if (a.x != nullptr)
+                v = plus(x[i], v);
+            store_vec_of<DT, W>(a.x_out, e0 + i * kN, v);
+        }
     }
 }
 
-// A row's lanes have kAhead pieces or more; where there are few rows, more CTAs
-// share one and its lanes have one piece.
+// A CTA of 256 lanes goes through a row, piece after piece; where there are few rows,
+// several CTAs share one.
 template <int DT, int W> cudaError_t dropout_dt(const LayerNormArgs &a, cudaStream_t st)
 {
     const size_t pieces = (a.hidden + Fmt<DT>::kVec - 1) / Fmt<DT>::kVec;
     Cut c;
     c.pieces = static_cast<unsigned>(pieces);
-    const bool few = a.tokens * pieces < static_cast<size_t>(kSms) * 4 * kLanes * kAhead;
-    const size_t lanes = few ? pieces : (pieces + kAhead - 1) / kAhead;
+    const bool few = a.tokens * pieces < static_cast<size_t>(kSms) * 8 * kLanes;
     c.segs = few ? static_cast<unsigned>((pieces + kLanes - 1) / kLanes) : 1;
-    c.lanes = static_cast<int>(lanes < kLanes ? lanes : kLanes);
+    c.lanes = static_cast<int>(pieces < kLanes ? pieces : kLanes);
     c.rows = c.segs > 1 ? 1 : kLanes / c.lanes;
     const size_t ctas = (a.tokens + c.rows - 1) / c.rows * c.segs;
     // whole warps, whose lanes behind the rows' do nothing

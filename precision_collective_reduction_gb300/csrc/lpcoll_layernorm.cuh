@@ -254,6 +254,27 @@ __device__ __forceinline__ float split_sum(const Three &x)
         s += __shfl_xor_sync(kAll, s, m);
     return s;
 }
+// The sums of a row in the gradient.
+struct RowSums {
+    float mean, m2, a, q;
+};
+
+// Two of them side by side.
+__device__ __forceinline__ void split_sums(const Three &x, const Three &y, float &a, float &b)
+{
+    float a1, b1;
+    const float a0 = split_first(x, a1), b0 = split_first(y, b1);
+    float s[2] = {split_second(a0, a1), split_second(b0, b1)};
+#pragma unroll
+    for (int m = 4; m <= 16; m <<= 1) {
+        const float u = __shfl_xor_sync(kAll, s[0], m), v = __shfl_xor_sync(kAll, s[1], m);
+        s[0] += u;
+        s[1] += v;
+    }
+    a = s[0];
+    b = s[1];
+}
+
 // The sum of a thread's values as an accumulator of products with 1.
 template <int N> __device__ __forceinline__ void add_values(Acc<N> &acc, const Vec<N> &a)
 {
@@ -457,9 +478,6 @@ enum GradStream { kGradX = 0, kGradDn = 1, kGradDx = 2 };
 // The sums of a row in the gradient: about the warp's mean the squares m2 and
 // a = sum q (x - mean_w), then q, and the sum of x. A warp leaves them as four floats,
 // lane l < 4 value l; `mine` is that value.
-struct RowSums {
-    float mean, m2, a, q;
-};
 constexpr int kSumOfX = 3;
 
 template <class S>
@@ -520,7 +538,7 @@ __device__ __forceinline__ RowSums team_grad_sums(float mine, float sum, const S
 // A row's x, less the warp's mean, and dn stay in registers in FP32 from the sums to
 // the outputs, as do the weights: reading them again from shared memory costs the
 // conversions again.
-template <int DT, int W, int kElems, int kMode, bool kDrop>
+template <int DT, int W, int kElems, bool kDrop>
 __global__ void __launch_bounds__(kTeamThreads, 1)
 layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int streams)
 {
@@ -529,12 +547,11 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
     __shared__ float4 red[2][kMaxWarps];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    constexpr bool kAlone = kMode == kPlain;
-    const Member<DT, W, kElems, kMode, kAlone> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
-    const Shares<NV, kN, kAlone> share(deal, a.hidden, me.first_warp);
-    const bool given = kDrop && (kMode == kPlain || a.dx_out != nullptr);
-    const bool want_dx = kMode == kPlain || a.dx != nullptr;
-    const bool want_dh = kDrop && (kMode == kPlain || a.dh != nullptr);
+    const Member<DT, W, kElems, kGeneral, false> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
+    const Shares<NV, kN, false> share(deal, a.hidden, me.first_warp);
+    const bool given = kDrop && a.dx_out != nullptr;
+    const bool want_dx = a.dx != nullptr;
+    const bool want_dh = kDrop && a.dh != nullptr;
     const bool drop = want_dh && a.drop.least != 0;
     const Philox rnd(a.drop, a.hidden);
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
@@ -584,7 +601,7 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
         }
         const RowSums s = team_grad_sums(split_sum({{fold(sq), fold(sa), fold(sqs)}}), sum, share,
                                          red[turn], deal, me.first_warp, a.hidden, per_hidden,
-                                         kAlone || deal.cluster == 1);
+                                         deal.cluster == 1);
         Keep<kElems, kN> keep;
         if (drop)
             keep.make(rnd, me, t);
@@ -610,8 +627,132 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
         stage = stage + 1 == deal.stages ? 0 : stage + 1;
     }
     copy_wait(0);
-    if (!kAlone && deal.cluster > 1)
+    if (deal.cluster > 1)
         cluster_barrier();  // no CTA leaves while another reads its sums
+    if (a.partial != nullptr)
+        leave_sums(me, deal, s_w, s_b, a.partial, reinterpret_cast<float *>(ring_smem));
+}
+
+// The gradient of rows that fill their teams (no clusters, every thread has all its
+// columns, nothing left out). A turn of a team joins the sums of its row t, makes
+// those of its next row, which depend on nothing of row t, and writes row t: so the
+// steps of the one fill the waits of the other. With no next row the stage's old
+// values are summed and not used. (One warp more that joins the sums for all, with
+// the sums of a row handed over in shared memory, left 96 registers a thread and was
+// slower: 8192 x 8192 BF16 95 us, 216 with dropout.)
+template <int DT, int W, int kElems, bool kDrop>
+__global__ void __launch_bounds__(kTeamThreads, 1)
+layer_norm_backward_even_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int streams)
+{
+    wait_prior_grid();
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float4 red[2][kMaxWarps];
+    constexpr int kN = Pack<DT, W>::kN;
+    constexpr int NV = kElems / kN;
+    const Member<DT, W, kElems, kPlain, true> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
+    const Shares<NV, kN, true> share(deal, a.hidden, me.first_warp);
+    const bool drop = kDrop && a.drop.least != 0;
+    const Philox rnd(a.drop, a.hidden);
+    const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
+    const int lane = threadIdx.x & 31, warps = deal.threads >> 5;
+    const auto fetch = [&](size_t t, int stage) {
+        if (t < a.tokens) {
+            me.copy(stage, kGradX, a.x, t);
+            me.copy(stage, kGradDn, a.dn_out, t);
+            if (kDrop)
+                me.copy(stage, kGradDx, a.dx_out, t);
+        }
+        copy_commit();
+    };
+    for (int s = 0; s < deal.stages; ++s)
+        fetch(me.t0 + s * me.step, s);
+
+    typename Pack<DT, W>::Raw w[NV];
+    Vec<kN> s_w[NV], s_b[NV];
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        w[c] = a.w != nullptr ? load_pack<DT, W>(a.w, me.col(c)) : all_of<DT, W>(1.0f);
+        s_w[c] = s_b[c] = splat<kN>(0.0f);
+    }
+
+    // this thread's parts of the sums of the row in `stage`
+    const auto add_up = [&](size_t t, int stage) {
+        Acc<kN> total = {};
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+            add_values<kN>(total, me.read(t, stage, kGradX, c));
+        return fold(total);
+    };
+    const auto add_rest = [&](size_t t, int stage, float sum) {
+        const Vec<kN> about = splat<kN>(-(sum * share.inv_own));
+        Acc<kN> sq = {}, sa = {}, sqs = {};
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const Vec<kN> d = plus(me.read(t, stage, kGradX, c), about);
+            const Vec<kN> q = mul(me.read(t, stage, kGradDn, c), unpack<DT, W>(w[c]));
+            add_products(sq, d, d);
+            add_products(sa, q, d);
+            add_values<kN>(sqs, q);
+        }
+        return Three{{fold(sq), fold(sa), fold(sqs)}};
+    };
+
+    int stage = 0, turn = 0;
+    me.ready(deal.stages - 1);
+    float sum = warp_sum(add_up(me.t0, 0));
+    float mine = split_sum(add_rest(me.t0, 0, sum));
+    for (size_t t = me.t0; t < a.tokens; t += me.step, turn ^= 1) {
+        const int after = stage + 1 == deal.stages ? 0 : stage + 1;
+        const size_t t2 = t + me.step;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (warps > 1) {
+            if (lane < 4)
+                reinterpret_cast<float *>(&red[turn][threadIdx.x >> 5])[lane] =
+                    lane == kSumOfX ? sum : mine;
+            __syncwarp();
+            team_barrier(deal);
+            if (lane < warps)
+                v = red[turn][me.first_warp + lane];
+        } else {
+            const RowSums own = spread(sum, mine);
+            if (lane == 0)
+                v = make_float4(own.m2, own.a, own.q, sum);
+        }
+        me.ready(deal.stages - 2);
+        float pair[2] = {v.w, add_up(t2, after)};
+        warp_sums(pair);
+        const float mean = pair[0] * per_hidden;
+        sum = pair[1];
+        float joined;
+        split_sums(moved(v, share, mean), add_rest(t2, after, sum), joined, mine);
+        const RowSums s = spread(mean, joined);
+        Keep<kElems, kN> keep;
+        if (drop)
+            keep.make(rnd, me, t);
+        // D = dx' + r q - r c1 - (x - mean) r c2, with the constants together
+        const float r = inv_rms(s.m2, per_hidden, a.eps);
+        const float c1 = s.q * per_hidden, c2 = r * r * (s.a * per_hidden);
+        const Vec<kN> shift = splat<kN>(-r * s.mean);
+        const Vec<kN> constant = splat<kN>(r * fmaf(c2, s.mean, -c1));
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const Vec<kN> x = me.read(t, stage, kGradX, c);
+            const Vec<kN> dn = me.read(t, stage, kGradDn, c);
+            s_w[c] = fma(fma(r, x, shift), dn, s_w[c]);
+            s_b[c] = plus(s_b[c], dn);
+            Vec<kN> q = constant;
+            if (kDrop)
+                q = plus(q, me.read(t, stage, kGradDx, c));
+            q = fma(r, mul(dn, unpack<DT, W>(w[c])), fma(-(r * c2), x, q));
+            store_vec_of<DT, W>(a.dx, me.elem(t, c), q);
+            if (kDrop)
+                store_vec_of<DT, W>(a.dh, me.elem(t, c),
+                                    drop ? keep.apply(rnd, me, q, a.drop.scale, c) : q);
+        }
+        fetch(t + deal.stages * me.step, stage);
+        stage = after;
+    }
+    copy_wait(0);
     if (a.partial != nullptr)
         leave_sums(me, deal, s_w, s_b, a.partial, reinterpret_cast<float *>(ring_smem));
 }
@@ -642,13 +783,21 @@ Plan layer_norm_plan(size_t tokens, int hidden, int dtype, int streams, bool gra
            (static_cast<size_t>(hidden) * width / kn / cluster + 2048) * streams > kSmemOne)
         cluster *= 2;
     p.elems = !p.wide && (hidden <= 256 || (tokens <= kSms && hidden <= kRow / 2 * cluster)) ? 8 : 16;
-    const int room = p.wide ? kWideThreads : kTeamThreads, multiple = group_packs(hidden, dtype);
-    if (!gradient && !p.wide && cluster == 1 && p.elems == 16) {
-        const Plan two = deal_rows(p, cluster, tokens, hidden, dtype, streams, false, room, multiple, 2);
+    // 8 columns a thread also where they fill the threads and 16 do not
+    if (!p.wide && cluster == 1 && width == 16 && hidden <= kRow / 2 && hidden % 512 != 0 &&
+        hidden % 256 == 0)
+        p.elems = 8;
+    Room room{p.wide ? kWideThreads : kTeamThreads, group_packs(hidden, dtype)};
+    if (gradient) {
+        room.least = 2;
+    } else if (!p.wide && cluster == 1 && p.elems == 16) {
+        Room pair = room;
+        pair.rows = 2;
+        const Plan two = deal_rows(p, cluster, tokens, hidden, dtype, streams, false, pair);
         if (two.even && two.smem <= kSmemOne)
             return two;
     }
-    return deal_rows(p, cluster, tokens, hidden, dtype, streams, gradient, room, multiple);
+    return deal_rows(p, cluster, tokens, hidden, dtype, streams, gradient, room);
 }
 
 template <int DT, int W, bool kDrop>
@@ -693,12 +842,12 @@ cudaError_t layer_norm_backward_dt(const LayerNormArgs &a, const Plan &p, cudaSt
     if constexpr (W == 16) {
         if (p.even && p.deal.cluster == 1 && a.dx != nullptr &&
             (!kDrop || (a.dx_out != nullptr && a.dh != nullptr)))
-            return launch_plan(p.elems == 8 ? layer_norm_backward_kernel<DT, W, 8, kPlain, kDrop>
-                                            : layer_norm_backward_kernel<DT, W, 16, kPlain, kDrop>,
+            return launch_plan(p.elems == 8 ? layer_norm_backward_even_kernel<DT, W, 8, kDrop>
+                                            : layer_norm_backward_even_kernel<DT, W, 16, kDrop>,
                                a, p, streams, st);
     }
-    return launch_plan(p.elems == 8 ? layer_norm_backward_kernel<DT, W, 8, kGeneral, kDrop>
-                                    : layer_norm_backward_kernel<DT, W, 16, kGeneral, kDrop>,
+    return launch_plan(p.elems == 8 ? layer_norm_backward_kernel<DT, W, 8, kDrop>
+                                    : layer_norm_backward_kernel<DT, W, 16, kDrop>,
                        a, p, streams, st);
 }
 

@@ -393,7 +393,7 @@ Plan make_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient)
         !gradient && streams <= 2 && hidden <= kRow && dtype == LPCOLL_BF16;
     p.elems = !p.wide && (hidden <= 256 || tokens <= kSms || light) ? 8 : 16;
     const int room = p.wide ? kWideThreads : (p.elems == 8 ? kThreadsOne<8> : kThreadsOne<16>);
-    return deal_rows(p, cluster, tokens, hidden, dtype, streams, gradient, room);
+    return deal_rows(p, cluster, tokens, hidden, dtype, streams, gradient, Room{room});
 }
 
 Plan backward_plan(size_t tokens, int hidden, int dtype, int gate_kind)

@@ -535,34 +535,41 @@ struct Plan {
 constexpr size_t kSmem[kMaxCtas] = {224 * 1024, 110 * 1024, 72 * 1024};
 constexpr size_t kSmemOne = kSmem[0];
 
+// What deal_rows works with beside the call's sizes.
+struct Room {
+    int threads;       // that an SM holds
+    int multiple = 1;  // accesses that a CTA's part of a row is a multiple of
+    int rows = 1;      // that a team takes at a time
+    int least = 1;     // stages that a team needs
+};
+
 // The rest of a plan whose columns per thread and form are chosen, for rows over
-// `cluster` CTAs. A CTA's part of a row is a multiple of `multiple` accesses, an SM
-// holds `room` threads; `gradient`: the teams of a CTA add up two sums of every
-// column at the end; `rows_of_turn`: rows that a team takes at a time.
+// `cluster` CTAs. `gradient`: the teams of a CTA add up two sums of every column at
+// the end.
 inline Plan deal_rows(Plan p, int cluster, size_t tokens, int hidden, int dtype, int streams,
-                      bool gradient, int room, int multiple = 1, int rows_of_turn = 1)
+                      bool gradient, const Room &room)
 {
-    p.rows = rows_of_turn;
-    streams *= rows_of_turn;
+    p.rows = room.rows;
+    streams *= room.rows;
     const int width = row_width(hidden, dtype);
     const int kn = width / static_cast<int>(dtype_bytes(dtype));
     Deal &d = p.deal;
     d.cluster = cluster;
-    d.packs = round_up(((hidden + kn - 1) / kn + cluster - 1) / cluster, multiple);
+    d.packs = round_up(((hidden + kn - 1) / kn + cluster - 1) / cluster, room.multiple);
     d.threads = round_up((d.packs + p.elems / kn - 1) / (p.elems / kn), 32);
-    d.groups = cluster > 1 || d.threads * 4 > room ? 1 : room / 2 / d.threads;
+    d.groups = cluster > 1 || d.threads * 4 > room.threads ? 1 : room.threads / 2 / d.threads;
     // the rows that each of a CTA's teams takes at a time, in all streams
     const size_t row =
         static_cast<size_t>(row_part_bytes(width, d.packs, d.threads, p.elems)) * streams;
-    while (d.groups > 1 && row * d.groups > kSmem[1])
+    while (d.groups > 1 && row * d.groups * room.least > kSmem[1])
         d.groups /= 2;
     p.even = width == 16 && hidden % kn == 0 && d.packs * cluster * kn == hidden &&
              d.packs % (32 * (p.elems / kn)) == 0;
-    int per_sm = room / (d.threads * d.groups);
+    int per_sm = room.threads / (d.threads * d.groups);
     per_sm = per_sm < 1 ? 1 : (per_sm > kMaxCtas ? kMaxCtas : per_sm);
-    while (per_sm > 1 && row * d.groups > kSmem[per_sm - 1])
+    while (per_sm > 1 && row * d.groups * room.least > kSmem[per_sm - 1])
         --per_sm;
-    const size_t at_once = static_cast<size_t>(d.groups) * rows_of_turn;
+    const size_t at_once = static_cast<size_t>(d.groups) * room.rows;
     const size_t steps = (tokens + at_once - 1) / at_once;
     const size_t most = static_cast<size_t>(kSms) * per_sm / cluster;
     p.ctas = static_cast<int>(steps < most ? steps : most);
