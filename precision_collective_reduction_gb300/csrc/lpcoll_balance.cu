@@ -5,8 +5,8 @@
 //   loss = c E sum_e (n_e / S) (P_e / V),   S = sum_e n_e, V valid tokens
 //   dz_tj = dloss (c E / (S V)) p_tj (n_j - sum_e n_e p_te)
 //
-// One warp per token, its lanes' probabilities added up in registers over the
-// warp's tokens. A CTA adds up its warps in order and leaves one row of sums and
+// 8 to 32 lanes per token, at 8 experts a lane and more, add up its probabilities in
+// registers over their tokens. A CTA adds up its warps in order and leaves one row of sums and
 // counts; the rows meet in one cluster, which adds them in order, so the same call
 // gives the same bits. Few tokens take that cluster alone: its CTAs make the rows
 // too, with a cluster barrier in between.
@@ -22,13 +22,21 @@ constexpr int kWide = 1024;            // threads of a CTA that makes sums
 constexpr int kWarps = kWide / 32;
 constexpr int kJoin = 8;               // CTAs of the cluster that joins the rows
 constexpr int kRows = 8;               // warps whose sums are in shared memory at a time
-constexpr size_t kOneLaunch = 1024;    // tokens that the cluster takes alone
+constexpr size_t kOneLaunch = 512;     // tokens that the cluster takes alone
 
-__device__ __forceinline__ float warp_max(float v)
+// Largest of, and sum over, the G lanes of a token; the same bits in each.
+template <int G> __device__ __forceinline__ float group_largest(float v)
 {
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1)
+    for (int m = G / 2; m >= 1; m >>= 1)
         v = fmaxf(v, __shfl_xor_sync(kAll, v, m));
+    return v;
+}
+template <int G> __device__ __forceinline__ float group_sum(float v)
+{
+#pragma unroll
+    for (int m = G / 2; m >= 1; m >>= 1)
+        v += __shfl_xor_sync(kAll, v, m);
     return v;
 }
 
@@ -37,29 +45,64 @@ __device__ __forceinline__ bool is_valid(const BalanceArgs &a, size_t t)
     return a.valid == nullptr || (LPC_READ_OK(a.valid + t, 1) && a.valid[t] != 0);
 }
 
-// Softmax of a token in place; all zeros where no logit is above -infinity.
-template <int PER> __device__ __forceinline__ void softmax(float (&x)[PER])
+// Softmax of N tokens in place, side by side; all zeros where no logit is above
+// -infinity. kSums: for sums over tokens, with the hardware's 2^x, which moves a term by
+// at most |d| 2^-24 of itself and ends at 2^-126 (32768 x 256 FP32: 16.0 -> 14.6 us); the
+// gradient keeps the digits of small probabilities.
+template <int PER, int G, int N, bool kSums> __device__ __forceinline__ void softmax(float (&x)[N][PER])
 {
-    float m = x[0];
+    float m[N], sum[N];
 #pragma unroll
-    for (int i = 1; i < PER; ++i)
-        m = fmaxf(m, x[i]);
-    m = warp_max(m);
-    // a NaN logit is no maximum, but its term is NaN, and so is the sum
-    if (m == -INFINITY)
-        m = 0.0f;
-    float sum = 0.0f;
+    for (int u = 0; u < N; ++u) {
+        m[u] = x[u][0];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        x[i] = expf(x[i] - m);
-        sum += x[i];
+        for (int i = 1; i < PER; ++i)
+            m[u] = fmaxf(m[u], x[u][i]);
     }
-    sum = warp_sum(sum);
-    const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        x[i] = x[i] * inv;
+    for (int u = 0; u < N; ++u)
+        m[u] = group_largest<G>(m[u]);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        // a NaN logit is no maximum, but its term is NaN, and so is the sum
+        if (m[u] == -INFINITY)
+            m[u] = 0.0f;
+        sum[u] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            x[u][i] = kSums ? exp_term(x[u][i] - m[u]) : expf(x[u][i] - m[u]);
+            sum[u] += x[u][i];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+        sum[u] = group_sum<G>(sum[u]);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const float inv = sum[u] == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum[u]);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            x[u][i] = x[u][i] * inv;
+    }
 }
+
+// Loads the logits of token t if `there`, else -infinity.
+template <int DT, int PER, int G>
+__device__ __forceinline__ void load_token(const BalanceArgs &a, const void *logits, size_t t,
+                                           bool there, int lane, float (&x)[PER])
+{
+    if (there) {
+        load_logits<DT, PER, G>(logits, t, a.experts, lane, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            x[i] = -INFINITY;
+    }
+}
+
+// Tokens that the lanes of a token take at a time, so that their loads and sums do
+// not wait for one another.
+template <int PER> constexpr int kPair = PER <= 8 ? 2 : 1;
 
 // Row `cta` of the workspace: sums [experts], then counts [experts] and the number
 // of valid tokens.
@@ -70,15 +113,18 @@ __device__ __forceinline__ float *sums_row(const BalanceArgs &a, int cta)
 
 struct MakeSmem {
     float part[kRows][LPCOLL_MAX_EXPERTS];
+    float sums[LPCOLL_MAX_EXPERTS];
     int hist[LPCOLL_MAX_EXPERTS];
     int tokens;
 };
 
-// The sums and counts of the tokens of CTA `cta` of `ctas`.
-template <int DT, int PER>
+// The sums and counts of the tokens of CTA `cta` of `ctas`, left in shared memory.
+template <int DT, int PER, int G>
 __device__ __forceinline__ void make_row(const BalanceArgs &a, MakeSmem &sm, int cta, int ctas)
 {
+    constexpr int N = kPair<PER>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int place = lane % G;  // among the token's lanes
     for (int e = tid; e < a.experts; e += kWide)
         sm.hist[e] = 0;
     if (tid == 0)
@@ -89,23 +135,38 @@ __device__ __forceinline__ void make_row(const BalanceArgs &a, MakeSmem &sm, int
     for (int i = 0; i < PER; ++i)
         acc[i] = 0.0f;
     int tokens = 0;
-    const size_t step = static_cast<size_t>(ctas) * kWarps;
-    for (size_t t = static_cast<size_t>(cta) * kWarps + warp; t < a.tokens; t += step) {
-        if (!is_valid(a, t))
-            continue;
-        ++tokens;
-        float x[PER];
-        load_logits<DT, PER>(a.logits, t, a.experts, lane, x);
-        if (lane < a.topk) {
-            const int e = load_i32(a.ids + t * a.topk + lane);
-            if (static_cast<unsigned>(e) < static_cast<unsigned>(a.experts))
-                atomicAdd(&sm.hist[e], 1);
+    const size_t step = static_cast<size_t>(ctas) * (kWide / G);
+    const size_t first = static_cast<size_t>(cta) * (kWide / G);  // of the CTA
+    for (size_t t0 = first; t0 < a.tokens; t0 += N * step) {
+        float x[N][PER];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const size_t t = t0 + u * step + tid / G;
+            const bool there = t < a.tokens && is_valid(a, t);
+            load_token<DT, PER, G>(a, a.logits, t, there, place, x[u]);
+            if (there) {
+                tokens += place == 0 ? 1 : 0;
+                for (int k = place; k < a.topk; k += G) {
+                    const int e = load_i32(a.ids + t * a.topk + k);
+                    if (static_cast<unsigned>(e) < static_cast<unsigned>(a.experts))
+                        atomicAdd(&sm.hist[e], 1);
+                }
+            }
         }
-        softmax(x);
+        softmax<PER, G, N, true>(x);
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                acc[i] += x[u][i];
+    }
+    // the tokens of a warp
+#pragma unroll
+    for (int m = G; m < 32; m <<= 1)
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            acc[i] += x[i];
-    }
+            acc[i] += __shfl_xor_sync(kAll, acc[i], m);
+    tokens = __reduce_add_sync(kAll, tokens);
     if (lane == 0 && tokens != 0)
         atomicAdd(&sm.tokens, tokens);
     float sum = 0.0f;  // of expert tid
@@ -113,8 +174,8 @@ __device__ __forceinline__ void make_row(const BalanceArgs &a, MakeSmem &sm, int
         if (warp >= w0 && warp < w0 + kRows)
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int e = expert_of<DT, PER>(i, lane);
-                if (e < a.experts)
+                const int e = expert_of<DT, PER, G>(i, place);
+                if (lane < G && e < a.experts)
                     sm.part[warp - w0][e] = acc[i];
             }
         __syncthreads();
@@ -124,23 +185,17 @@ __device__ __forceinline__ void make_row(const BalanceArgs &a, MakeSmem &sm, int
                 sum += sm.part[r][tid];
         __syncthreads();
     }
-    float *const row = sums_row(a, cta);
-    int32_t *const counts = reinterpret_cast<int32_t *>(row) + a.experts;
-    if (tid < a.experts) {
-        store_f32(row + tid, sum);
-        store_i32(counts + tid, sm.hist[tid]);
-    }
-    if (tid == 0)
-        store_i32(counts + a.experts, sm.tokens);
+    if (tid < a.experts)
+        sm.sums[tid] = sum;
 }
 
 struct JoinSmem {
     float sums[kWarps][33];
     int counts[kWarps][33];
-    float dot[kWarps];        // sum of n_e P_e, of a warp's experts
-    long long slots[kWarps];  // and of n_e
+    float dot[kWarps];  // sum of n_e P_e, of a warp's experts
+    int slots[kWarps];  // and of n_e
     float cta_dot;
-    long long cta_slots;
+    int cta_slots;
 };
 
 __device__ __forceinline__ unsigned join_rank()
@@ -156,23 +211,59 @@ __device__ __forceinline__ void join_barrier()
                  "barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-template <class T> __device__ __forceinline__ T join_load(const T *p, unsigned rank)
+__device__ __forceinline__ uint32_t join_address(const void *p, unsigned rank)
 {
-    static_assert(sizeof(T) == 4 || sizeof(T) == 8, "one 32- or 64-bit value");
     const uint32_t local = static_cast<uint32_t>(__cvta_generic_to_shared(p));
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-    T v;
-    if constexpr (sizeof(T) == 4) {
-        uint32_t raw;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(raw) : "r"(remote) : "memory");
-        memcpy(&v, &raw, 4);
-    } else {
-        unsigned long long raw;
-        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(raw) : "r"(remote) : "memory");
-        memcpy(&v, &raw, 8);
-    }
+    return remote;
+}
+
+__device__ __forceinline__ float join_load(const float *p, unsigned rank)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(join_address(p, rank)) : "memory");
     return v;
+}
+
+__device__ __forceinline__ int join_load(const int *p, unsigned rank)
+{
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(join_address(p, rank)) : "memory");
+    return v;
+}
+
+// The loss, from each warp's part of sum n_e P_e and sum n_e (in its lane 0). All
+// threads of the cluster come here; the first thread of all has `tokens`.
+__device__ __forceinline__ void write_loss(const BalanceArgs &a, JoinSmem &sm, unsigned rank,
+                                           float dot, int slots, int tokens)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (lane == 0) {
+        sm.dot[warp] = dot;
+        sm.slots[warp] = slots;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        dot = warp_sum(sm.dot[lane]);
+        slots = __reduce_add_sync(kAll, sm.slots[lane]);
+        if (lane == 0) {
+            sm.cta_dot = dot;
+            sm.cta_slots = slots;
+        }
+    }
+    join_barrier();
+    if (rank == 0 && warp == 0) {
+        dot = warp_sum(lane < kJoin ? join_load(&sm.cta_dot, lane) : 0.0f);
+        slots = __reduce_add_sync(kAll, lane < kJoin ? join_load(&sm.cta_slots, lane) : 0);
+        if (lane == 0) {
+            const float of = static_cast<float>(slots) * static_cast<float>(tokens);
+            store_i32(a.counts + a.experts, tokens);
+            store_f32(a.loss, of == 0.0f ? 0.0f
+                                         : __fdiv_rn(a.coef * static_cast<float>(a.experts) * dot, of));
+        }
+    }
+    join_barrier();  // no CTA leaves while its sums are read
 }
 
 // Adds up the rows, 32 experts of a CTA of the cluster at a time: 32 warps take
@@ -182,13 +273,20 @@ __device__ __forceinline__ void join_rows(const BalanceArgs &a, JoinSmem &sm, in
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int E = a.experts;
     const unsigned rank = join_rank();
+    int tokens = 0;
+    if (rank == 0 && warp == 0) {
+#pragma unroll 5
+        for (int r = lane; r < rows; r += 32)
+            tokens += load_i32(reinterpret_cast<const int32_t *>(sums_row(a, r)) + 2 * E);
+        tokens = __reduce_add_sync(kAll, tokens);
+    }
     float dot = 0.0f;
-    long long slots = 0;
+    int slots = 0;
     for (int e0 = static_cast<int>(rank) * 32; e0 < E; e0 += kJoin * 32) {
         float sum = 0.0f;
         int count = 0;
         if (e0 + lane < E) {
-#pragma unroll 10
+#pragma unroll 5
             for (int r = warp; r < rows; r += kWarps) {
                 const float *row = sums_row(a, r) + e0 + lane;
                 sum += load_f32(row);
@@ -208,49 +306,24 @@ __device__ __forceinline__ void join_rows(const BalanceArgs &a, JoinSmem &sm, in
         }
         __syncthreads();
     }
-    if (lane == 0) {
-        sm.dot[warp] = dot;
-        sm.slots[warp] = slots;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        float d = 0.0f;
-        long long s = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            d += sm.dot[w];
-            s += sm.slots[w];
-        }
-        sm.cta_dot = d;
-        sm.cta_slots = s;
-    }
-    join_barrier();
-    if (rank == 0 && warp == 0) {
-        int tokens = 0;
-        for (int r = lane; r < rows; r += 32)
-            tokens += load_i32(reinterpret_cast<const int32_t *>(sums_row(a, r)) + 2 * E);
-        tokens = __reduce_add_sync(kAll, tokens);
-        if (lane == 0) {
-            float d = 0.0f;
-            long long s = 0;
-            for (unsigned c = 0; c < kJoin; ++c) {
-                d += join_load(&sm.cta_dot, c);
-                s += join_load(&sm.cta_slots, c);
-            }
-            const float of = static_cast<float>(s) * static_cast<float>(tokens);
-            store_i32(a.counts + E, tokens);
-            store_f32(a.loss, of == 0.0f ? 0.0f
-                                         : __fdiv_rn(a.coef * static_cast<float>(E) * d, of));
-        }
-    }
-    join_barrier();  // no CTA leaves while its sums are read
+    write_loss(a, sm, rank, dot, slots, tokens);
 }
 
-template <int DT, int PER>
+template <int DT, int PER, int G>
 __global__ void __launch_bounds__(kWide) balance_rows_kernel(const __grid_constant__ BalanceArgs a)
 {
     wait_prior_grid();
     __shared__ MakeSmem sm;
-    make_row<DT, PER>(a, sm, blockIdx.x, gridDim.x);
+    make_row<DT, PER, G>(a, sm, blockIdx.x, gridDim.x);
+    float *const row = sums_row(a, blockIdx.x);
+    int32_t *const counts = reinterpret_cast<int32_t *>(row) + a.experts;
+    const int tid = threadIdx.x;
+    if (tid < a.experts) {
+        store_f32(row + tid, sm.sums[tid]);
+        store_i32(counts + tid, sm.hist[tid]);
+    }
+    if (tid == 0)
+        store_i32(counts + a.experts, sm.tokens);
 }
 
 __global__ void __launch_bounds__(kWide) balance_join_kernel(const __grid_constant__ BalanceArgs a, int rows)
@@ -260,127 +333,164 @@ __global__ void __launch_bounds__(kWide) balance_join_kernel(const __grid_consta
     join_rows(a, sm, rows);
 }
 
-template <int DT, int PER>
+// Few tokens: the CTAs of one cluster make their rows and read them from one another's
+// shared memory, each an eighth of the experts.
+template <int DT, int PER, int G>
 __global__ void __launch_bounds__(kWide) balance_one_kernel(const __grid_constant__ BalanceArgs a)
 {
     wait_prior_grid();
-    __shared__ union {
-        MakeSmem make;
-        JoinSmem join;
-    } sm;
-    make_row<DT, PER>(a, sm.make, blockIdx.x, kJoin);
-    join_barrier();  // the rows are in global memory, and shared memory is free
-    join_rows(a, sm.join, kJoin);
+    __shared__ MakeSmem sm;
+    __shared__ JoinSmem join;
+    make_row<DT, PER, G>(a, sm, blockIdx.x, kJoin);
+    join_barrier();
+    const unsigned rank = join_rank();
+    const int tid = threadIdx.x, each = (a.experts + kJoin - 1) / kJoin;
+    const int e = static_cast<int>(rank) * each + tid;
+    float dot = 0.0f;
+    int slots = 0, tokens = 0;
+    if (tid < each && e < a.experts) {
+        float p[kJoin];
+#pragma unroll
+        for (unsigned c = 0; c < kJoin; ++c) {
+            p[c] = join_load(&sm.sums[e], c);
+            slots += join_load(&sm.hist[e], c);
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (unsigned c = 0; c < kJoin; ++c)
+            sum += p[c];
+        store_f32(a.prob_sums + e, sum);
+        store_i32(a.counts + e, slots);
+        dot = static_cast<float>(slots) * sum;
+    }
+    if (rank == 0 && tid == 0)
+#pragma unroll
+        for (unsigned c = 0; c < kJoin; ++c)
+            tokens += join_load(&sm.tokens, c);
+    // write_loss ends with a barrier of the cluster, behind all of these reads
+    write_loss(a, join, rank, warp_sum(dot), __reduce_add_sync(kAll, slots), tokens);
 }
 
-// Gradient: a warp per token, with the counts of its experts in registers.
-template <int DT, int PER>
+// Gradient: the counts of a lane's experts stay in its registers.
+template <int DT, int PER, int G>
 __global__ void __launch_bounds__(kThreads)
 balance_backward_kernel(const __grid_constant__ BalanceArgs a)
 {
     wait_prior_grid();
+    constexpr int N = kPair<PER>;
     constexpr int R = kRun<DT, PER>;
     constexpr int kEs = kOne<DT>;
     using Raw = typename RunBytes<R * kEs>::Raw;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int place = threadIdx.x % G;
     const int E = a.experts;
     float n[PER], all = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = expert_of<DT, PER>(i, lane);
+        const int e = expert_of<DT, PER, G>(i, place);
         n[i] = e < E ? static_cast<float>(load_i32(a.counts + e)) : 0.0f;
         all += n[i];
     }
-    const float of = warp_sum(all) * static_cast<float>(load_i32(a.counts + E));
+    const float of = group_sum<G>(all) * static_cast<float>(load_i32(a.counts + E));
     const float rate =
         of == 0.0f ? 0.0f
                    : __fdiv_rn(load_f32(a.dloss) * a.coef * static_cast<float>(E), of);
-    const size_t step = static_cast<size_t>(gridDim.x) * kWarpsPerCta;
-    for (size_t t = static_cast<size_t>(blockIdx.x) * kWarpsPerCta + warp; t < a.tokens; t += step) {
-        const bool valid = is_valid(a, t);
-        if (!valid && a.accumulate)
-            continue;
-        float x[PER];
-        if (valid) {
-            load_logits<DT, PER>(a.logits, t, E, lane, x);
-            softmax(x);
-            float mean = 0.0f;
+    const size_t step = static_cast<size_t>(gridDim.x) * (kThreads / G);
+    const size_t first = static_cast<size_t>(blockIdx.x) * (kThreads / G);
+    for (size_t t0 = first; t0 < a.tokens; t0 += N * step) {
+        float x[N][PER];
+        bool there[N], valid[N];
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                mean = fmaf(n[i], x[i], mean);
-            mean = warp_sum(mean);
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                x[i] = of == 0.0f ? 0.0f : rate * x[i] * (n[i] - mean);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                x[i] = 0.0f;
+        for (int u = 0; u < N; ++u) {
+            const size_t t = t0 + u * step + threadIdx.x / G;
+            there[u] = t < a.tokens;
+            valid[u] = there[u] && is_valid(a, t);
+            load_token<DT, PER, G>(a, a.logits, t, valid[u], place, x[u]);
         }
-        if (a.accumulate) {
-            float y[PER];
-            load_logits<DT, PER>(a.dlogits, t, E, lane, y);
+        softmax<PER, G, N, false>(x);
+        float mean[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            mean[u] = 0.0f;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                x[i] += y[i];
+                mean[u] = fmaf(n[i], x[u][i], mean[u]);
         }
-        char *const row = static_cast<char *>(a.dlogits) + t * E * kEs;
 #pragma unroll
-        for (int r = 0; r < PER / R; ++r) {
-            const int e = (r * 32 + lane) * R;
-            typename Pack<DT, kEs>::Raw v[R];
+        for (int u = 0; u < N; ++u)
+            mean[u] = group_sum<G>(mean[u]);
 #pragma unroll
-            for (int j = 0; j < R; ++j) {
-                const float one[1] = {x[r * R + j]};
-                v[j] = narrow_pack<DT, kEs>(one);
+        for (int u = 0; u < N; ++u) {
+            if (!there[u] || (a.accumulate && !valid[u]))
+                continue;
+            const size_t t = t0 + u * step + threadIdx.x / G;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                x[u][i] = of == 0.0f ? 0.0f : rate * x[u][i] * (n[i] - mean[u]);
+            if (a.accumulate) {
+                float y[PER];
+                load_logits<DT, PER, G>(a.dlogits, t, E, place, y);
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    x[u][i] += y[i];
             }
-            if (E % R == 0) {
-                if (e < E && LPC_WRITE_OK(row + e * kEs, R * kEs)) {
-                    Raw raw;
-                    memcpy(&raw, v, sizeof(raw));
-                    *reinterpret_cast<Raw *>(row + e * kEs) = raw;
-                }
-            } else {
+            char *const row = static_cast<char *>(a.dlogits) + t * E * kEs;
 #pragma unroll
-                for (int j = 0; j < R; ++j)
-                    if (e + j < E)
-                        store_pack<DT, kEs>(row, e + j, v[j]);
+            for (int r = 0; r < PER / R; ++r) {
+                const int e = (r * G + place) * R;
+                typename Pack<DT, kEs>::Raw v[R];
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    const float one[1] = {x[u][r * R + j]};
+                    v[j] = narrow_pack<DT, kEs>(one);
+                }
+                if (E % R == 0) {
+                    if (e < E && LPC_WRITE_OK(row + e * kEs, R * kEs)) {
+                        Raw raw;
+                        memcpy(&raw, v, sizeof(raw));
+                        *reinterpret_cast<Raw *>(row + e * kEs) = raw;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < R; ++j)
+                        if (e + j < E)
+                            store_pack<DT, kEs>(row, e + j, v[j]);
+                }
             }
         }
     }
 }
 
-template <int DT, int PER>
+template <int DT, int PER, int G>
 cudaError_t balance_per(const BalanceArgs &a, bool backward, cudaStream_t st)
 {
     if (backward) {
-        const size_t need = (a.tokens + kWarpsPerCta - 1) / kWarpsPerCta;
+        const size_t need = (a.tokens + kThreads / G - 1) / (kThreads / G);
         const size_t most = static_cast<size_t>(kSms) * 8;
-        return launch_kernel_block(balance_backward_kernel<DT, PER>, need < most ? need : most,
+        return launch_kernel_block(balance_backward_kernel<DT, PER, G>, need < most ? need : most,
                                    kThreads, 0, st, a);
     }
     const int rows = balance_rows(a.tokens);
     if (rows == 1)
-        return launch_kernel_cluster(balance_one_kernel<DT, PER>, kJoin, kWide, kJoin, 0, st, a);
+        return launch_kernel_cluster(balance_one_kernel<DT, PER, G>, kJoin, kWide, kJoin, 0, st, a);
     const cudaError_t e =
-        launch_kernel_block(balance_rows_kernel<DT, PER>, rows, kWide, 0, st, a);
+        launch_kernel_block(balance_rows_kernel<DT, PER, G>, rows, kWide, 0, st, a);
     if (e != cudaSuccess)
         return e;
     return launch_kernel_cluster(balance_join_kernel, kJoin, kWide, kJoin, 0, st, a, rows);
 }
 
-// Logits per lane: the smallest power of two that holds the experts.
+// 8 logits a lane, and lanes that hold the experts, up to a warp; then more logits.
 template <int DT> cudaError_t balance_dt(const BalanceArgs &a, bool backward, cudaStream_t st)
 {
     if (a.experts <= 64)
-        return balance_per<DT, 2>(a, backward, st);
+        return balance_per<DT, 8, 8>(a, backward, st);
     if (a.experts <= 128)
-        return balance_per<DT, 4>(a, backward, st);
+        return balance_per<DT, 8, 16>(a, backward, st);
     if (a.experts <= 256)
-        return balance_per<DT, 8>(a, backward, st);
+        return balance_per<DT, 8, 32>(a, backward, st);
     if (a.experts <= 512)
-        return balance_per<DT, 16>(a, backward, st);
-    return balance_per<DT, 32>(a, backward, st);
+        return balance_per<DT, 16, 32>(a, backward, st);
+    return balance_per<DT, 32, 32>(a, backward, st);
 }
 
 }  // namespace
@@ -390,14 +500,14 @@ int balance_rows(size_t tokens)
     if (tokens <= kOneLaunch)
         return 1;
     const size_t need = (tokens + kWarps - 1) / kWarps;
-    const size_t most = static_cast<size_t>(kSms) * 2;
+    const size_t most = kSms;
     return static_cast<int>(need < most ? need : most);
 }
 
 size_t balance_workspace(size_t tokens, int experts)
 {
     const int rows = balance_rows(tokens);
-    return static_cast<size_t>(rows == 1 ? kJoin : rows) * (2 * experts + 1) * sizeof(float);
+    return rows == 1 ? 0 : static_cast<size_t>(rows) * (2 * experts + 1) * sizeof(float);
 }
 
 cudaError_t launch_balance(const BalanceArgs &a, cudaStream_t st)

@@ -18,25 +18,49 @@ namespace lpc {
 
 namespace {
 
+constexpr int kSms = 152;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kLanes = 256;
 
-// How a row is cut: `segs` CTAs of `lanes` lanes with 16 bytes (of the table or of
-// dout) each; short rows share a CTA, `rows` of them.
+// How a row is cut: `lanes` lanes of each of `segs` CTAs go through it in pieces of 16
+// bytes (of the table or of dout), `pieces` of them, `ahead` at a time; short rows
+// share a CTA, `rows` of them.
 struct RowCut {
-    unsigned segs;
+    unsigned segs, pieces;
     int lanes, rows;
 };
 
-RowCut cut(size_t hidden, int dtype)
+RowCut cut(size_t hidden, int dtype, int ahead, int most)
 {
-    const size_t per_lane = 16 / dtype_bytes(dtype);
-    const size_t lanes = (hidden + per_lane - 1) / per_lane;
+    const size_t per_piece = 16 / dtype_bytes(dtype);
+    const size_t pieces = (hidden + per_piece - 1) / per_piece;
+    const size_t lanes = (pieces + ahead - 1) / ahead;
     RowCut r;
-    r.segs = static_cast<unsigned>((lanes + kLanes - 1) / kLanes);
+    r.pieces = static_cast<unsigned>(pieces);
+    r.segs = static_cast<unsigned>((lanes + most - 1) / most);
     r.lanes = static_cast<int>((lanes + r.segs - 1) / r.segs);
-    r.rows = r.segs > 1 ? 1 : kLanes / r.lanes;
+    r.rows = r.segs > 1 ? 1 : most / r.lanes;
     return r;
+}
+
+// The row and the first piece of a thread.
+struct Place {
+    size_t row;
+    unsigned piece;
+    bool idle;  // a lane behind the CTA's rows
+};
+__device__ __forceinline__ Place place_of(const RowCut &c, size_t cta)
+{
+    Place p = {cta, threadIdx.x, threadIdx.x >= static_cast<unsigned>(c.lanes * c.rows)};
+    if (c.segs > 1) {
+        p.row = cta / c.segs;
+        p.piece += static_cast<unsigned>(cta % c.segs) * c.lanes;
+    } else if (c.rows > 1) {
+        const unsigned which = threadIdx.x / c.lanes;
+        p.row = cta * c.rows + which;
+        p.piece -= which * c.lanes;
+    }
+    return p;
 }
 
 // Row of the shard of token t, or -1.
@@ -55,6 +79,8 @@ __device__ __forceinline__ long long row_of(const EmbedArgs &a, size_t t)
     return id >= a.first_id && row < a.vocab ? static_cast<long long>(row) : -1;
 }
 
+constexpr int kPieces = 4;  // that a lane of the forward pass has in flight
+
 template <int DT, int W>
 __global__ void __launch_bounds__(kLanes)
 embed_kernel(const __grid_constant__ EmbedArgs a, const RowCut c)
@@ -63,32 +89,42 @@ embed_kernel(const __grid_constant__ EmbedArgs a, const RowCut c)
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int kCols = Fmt<DT>::kVec;
     constexpr int kPacks = kCols / kN;
-    const int which = static_cast<int>(threadIdx.x) / c.lanes;
-    const size_t t = static_cast<size_t>(blockIdx.x / c.segs) * c.rows + which;
-    const size_t col = (static_cast<size_t>(blockIdx.x % c.segs) * c.lanes +
-                        (static_cast<int>(threadIdx.x) - which * c.lanes)) * kCols;
-    if (t >= a.tokens || col >= a.hidden)
+    const Place p = place_of(c, blockIdx.x);
+    if (p.idle || p.row >= a.tokens)
         return;
-    const long long row = row_of(a, t);
-    typename Pack<DT, W>::Raw raw[kPacks];
+    const long long row = row_of(a, p.row);
+    const unsigned step = c.segs * c.lanes;
+    const size_t to = p.row * a.hidden, from = static_cast<size_t>(row >= 0 ? row : 0) * a.hidden;
+    const bool plain = a.scale == 1.0f;
+    typename Pack<DT, W>::Raw raw[kPieces][kPacks];
+    const auto has = [&](int u, int i) {
+        const unsigned piece = p.piece + u * step;
+        return W == 16 ? piece < c.pieces : piece * kCols + i * kN < a.hidden;
+    };
 #pragma unroll
-    for (int i = 0; i < kPacks; ++i) {
-        raw[i] = {};
-        if (row >= 0 && (W == 16 || col + i * kN < a.hidden))
-            raw[i] = load_pack<DT, W>(a.table, static_cast<size_t>(row) * a.hidden + col + i * kN);
-    }
+    for (int u = 0; u < kPieces; ++u)
 #pragma unroll
-    for (int i = 0; i < kPacks; ++i) {
-        if (W != 16 && col + i * kN >= a.hidden)
-            continue;
-        float x[kN];
-        widen_pack<DT, W>(raw[i], x);
-        if (row >= 0)  // other rows are +0, whatever the scale
+        for (int i = 0; i < kPacks; ++i) {
+            raw[u][i] = {};
+            if (row >= 0 && has(u, i))
+                raw[u][i] = load_pack<DT, W>(a.table, from + (p.piece + u * step) * kCols + i * kN);
+        }
 #pragma unroll
-            for (int j = 0; j < kN; ++j)
-                x[j] = x[j] * a.scale;
-        store_pack<DT, W>(a.out, t * a.hidden + col + i * kN, narrow_pack<DT, W>(x));
-    }
+    for (int u = 0; u < kPieces; ++u)
+#pragma unroll
+        for (int i = 0; i < kPacks; ++i) {
+            if (!has(u, i))
+                continue;
+            if (row >= 0 && !plain) {  // other rows are +0, whatever the scale
+                float x[kN];
+                widen_pack<DT, W>(raw[u][i], x);
+#pragma unroll
+                for (int j = 0; j < kN; ++j)
+                    x[j] = x[j] * a.scale;
+                raw[u][i] = narrow_pack<DT, W>(x);
+            }
+            store_pack<DT, W>(a.out, to + (p.piece + u * step) * kCols + i * kN, raw[u][i]);
+        }
 }
 
 // ---------------------------------------------------------------------------
@@ -132,7 +168,7 @@ SortPlan sort_plan(size_t tokens, size_t vocab)
 struct RadixArgs {
     const int32_t *keys, *order;  // of the pass before; NULL in the first
     int32_t *keys_out, *order_out;
-    int32_t *counts;   // [digits][chunks]
+    int32_t *counts;   // [chunks][digits]
     uint32_t *used;    // bit v: row v has a token
     int tokens, shift, bits, chunks, chunk_len, words;
 };
@@ -166,7 +202,7 @@ radix_count_kernel(const __grid_constant__ EmbedArgs e, const RadixArgs a)
         atomicAdd(&hist[key_of(e, a, static_cast<int>(i)) >> a.shift & (digits - 1)], 1);
     __syncthreads();
     for (int d = threadIdx.x; d < digits; d += kThreads)
-        store_i32(a.counts + static_cast<size_t>(d) * a.chunks + blockIdx.x, hist[d]);
+        store_i32(a.counts + static_cast<size_t>(blockIdx.x) * digits + d, hist[d]);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -197,25 +233,17 @@ radix_place_kernel(const __grid_constant__ EmbedArgs e, const RadixArgs a)
     for (long long i = w_lo + lane; i < w_end; i += 32)
         atomicAdd(&next[warp][key_of(e, a, static_cast<int>(i)) >> a.shift & (digits - 1)], 1);
     if (a.chunks > 1) {
-        // a warp per digit, a lane per chunk
-        constexpr int kSteps = kMaxChunks / 32;
-        for (int d = warp; d < digits; d += kWarpsPerCta) {
+        // a thread per digit, several chunks' counts in flight
+        for (int d = tid; d < digits; d += kThreads) {
             int sum = 0, prior = 0;
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int c = i * 32 + lane;
-                const int v = c < a.chunks
-                                  ? load_i32(a.counts + static_cast<size_t>(d) * a.chunks + c)
-                                  : 0;
+#pragma unroll 16
+            for (int c = 0; c < a.chunks; ++c) {
+                const int v = load_i32(a.counts + static_cast<size_t>(c) * digits + d);
                 sum += v;
                 prior += c < static_cast<int>(blockIdx.x) ? v : 0;
             }
-            sum = __reduce_add_sync(kAll, sum);
-            prior = __reduce_add_sync(kAll, prior);
-            if (lane == 0) {
-                total[d] = sum;
-                before[d] = prior;
-            }
+            total[d] = sum;
+            before[d] = prior;
         }
     }
     __syncthreads();
@@ -282,26 +310,6 @@ radix_place_kernel(const __grid_constant__ EmbedArgs e, const RadixArgs a)
             next[warp][d] += __popc(same);
         __syncwarp();
     }
-}
-
-// ---------------------------------------------------------------------------
-// Sums of the sorted tokens' rows.
-// ---------------------------------------------------------------------------
-
-constexpr int kAhead = 4;        // rows that a lane loads before it adds them
-constexpr int kClearRows = 8;    // rows of the table that a CTA clears
-
-struct SumArgs {
-    const int32_t *keys, *order;
-    const uint32_t *used;
-    float *head, *tail;  // [tiles][hidden]: runs that came from the tile before, that go on
-    int tokens, tile, tiles;
-    size_t sum_ctas;     // the CTAs behind these clear
-};
-
-__device__ __forceinline__ int key_at(const SumArgs &s, long long i)
-{
-    return i >= 0 && i < s.tokens ? load_i32(s.keys + i) : -1;
 }
 
 // Columns of a lane in FP32, kCols of them in the layout of dout's accesses.
@@ -380,6 +388,238 @@ template <int DT, int W> struct LaneCols {
     }
 };
 
+// Zeros into the `rows` rows from v0 on whose bit in `used` is not set: a warp a row
+// where there are enough of them, else a CTA.
+template <int DT, int W>
+__device__ __forceinline__ void clear_rows(const EmbedArgs &a, size_t v0, int rows,
+                                           const uint32_t *used)
+{
+    constexpr int WF = LaneCols<DT, W>::WF;
+    constexpr int kF = WF / 4;
+    const float zero[kF] = {};
+    const int warps = blockDim.x >> 5;
+    const bool narrow = rows >= warps;
+    const int lane = narrow ? threadIdx.x & 31 : threadIdx.x, lanes = narrow ? 32 : blockDim.x;
+    for (int i = narrow ? threadIdx.x >> 5 : 0; i < rows; i += narrow ? warps : 1) {
+        if (v0 + i >= a.vocab || (used[i >> 5] >> (i & 31) & 1u) != 0)
+            continue;
+        float *const row = a.dtable + (v0 + i) * a.hidden;
+#pragma unroll 4
+        for (size_t col = static_cast<size_t>(lane) * kF; col < a.hidden;
+             col += static_cast<size_t>(lanes) * kF)
+            store_pack<LPCOLL_F32, WF>(row, col, narrow_pack<LPCOLL_F32, WF>(zero));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The same sort in one launch, for up to kClusterTokens: a cluster of up to kSortCtas
+// CTAs holds all keys and tokens in its shared memory, each CTA the places [rank n,
+// rank n + n) of the order, and a pass writes them to their next places, in whatever
+// CTA those are. A cluster barrier tells that all counts of a pass are there, another
+// that all of its writes are. A CTA takes 2048 tokens before there is another.
+// ---------------------------------------------------------------------------
+
+constexpr int kSortCtas = 8;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kClusterTokens = 65536;
+
+__device__ __forceinline__ unsigned sort_rank()
+{
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void sort_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\t"
+                 "barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t remote(const void *p, unsigned rank)
+{
+    const uint32_t local = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    uint32_t far;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(local), "r"(rank));
+    return far;
+}
+
+// Clears some rows of the table that no token has; the CTA looks for them in all ids.
+template <int DT, int W>
+__device__ __forceinline__ void clear_unused(const EmbedArgs &e, size_t v0, int rows, int *smem)
+{
+    uint32_t *const used = reinterpret_cast<uint32_t *>(smem);
+    for (int w = threadIdx.x; w * 32 < rows; w += kSortThreads)
+        used[w] = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (size_t t = threadIdx.x; t < e.tokens; t += kSortThreads) {
+        const long long row = row_of(e, t) - static_cast<long long>(v0);
+        if (row >= 0 && row < rows)
+            atomicOr(&used[row >> 5], 1u << (row & 31));
+    }
+    __syncthreads();
+    clear_rows<DT, W>(e, v0, rows, used);
+}
+
+// The first cluster sorts. Meanwhile the CTAs of the others clear `clear` rows of the
+// table each.
+template <int DT, int W>
+__global__ void __launch_bounds__(kSortThreads)
+cluster_sort_kernel(const __grid_constant__ EmbedArgs e, const RadixArgs a, int passes, int log_n,
+                    int ctas, int clear)
+{
+    wait_prior_grid();
+    extern __shared__ int sort_smem[];
+    if (blockIdx.x >= static_cast<unsigned>(ctas)) {
+        clear_unused<DT, W>(e, static_cast<size_t>(blockIdx.x - ctas) * clear, clear, sort_smem);
+        return;
+    }
+    __shared__ int warp_total[kSortWarps];
+    const int n = 1 << log_n, digits = 1 << a.bits;
+    // [2][n] keys, [2][n] tokens, [warps][digits] places, [digits] counts, [digits] firsts
+    int *const keys = sort_smem, *const order = keys + 2 * n;
+    int *const next = order + 2 * n, *const count = next + kSortWarps * digits;
+    int *const first = count + digits;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned rank = sort_rank();
+    const int lo = static_cast<int>(rank) * n;
+    const int mine = max(0, min(n, a.tokens - lo));
+    const int part = n / kSortWarps;  // a multiple of 32
+    const int w_lo = warp * part, w_end = min(w_lo + part, mine);
+    for (int w = static_cast<int>(rank) * kSortThreads + tid; w < a.words; w += ctas * kSortThreads)
+        store_i32(reinterpret_cast<int32_t *>(a.used) + w, 0);
+    for (int i = tid; i < mine; i += kSortThreads) {
+        keys[i] = key_of(e, a, lo + i);
+        order[i] = lo + i;
+    }
+    int from = 0;
+    for (int pass = 0, shift = 0; pass < passes; ++pass, shift += a.bits, from ^= 1) {
+        const int *const key_in = keys + from * n, *const order_in = order + from * n;
+        for (int d = tid; d < kSortWarps * digits; d += kSortThreads)
+            next[d] = 0;
+        __syncthreads();
+        for (int i = w_lo + lane; i < w_end; i += 32)
+            atomicAdd(&next[warp * digits + (key_in[i] >> shift & (digits - 1))], 1);
+        __syncthreads();
+        int sum = 0;
+        if (tid < digits) {
+            int v[kSortWarps];
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w)
+                v[w] = next[w * digits + tid];
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                next[w * digits + tid] = sum;
+                sum += v[w];
+            }
+            count[tid] = sum;
+        }
+        sort_barrier();
+        int total = 0, prior = 0;
+        if (tid < digits) {
+            int v[kSortCtas];
+#pragma unroll
+            for (int c = 0; c < kSortCtas; ++c) {
+                v[c] = 0;
+                if (c < ctas)
+                    asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                                 : "=r"(v[c])
+                                 : "r"(remote(count + tid, c))
+                                 : "memory");
+            }
+#pragma unroll
+            for (int c = 0; c < kSortCtas; ++c) {
+                total += v[c];
+                prior += c < static_cast<int>(rank) ? v[c] : 0;
+            }
+        }
+        // exclusive sum of the totals over the digits
+        int scan = total;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int v = __shfl_up_sync(kAll, scan, m);
+            scan += lane >= m ? v : 0;
+        }
+        if (lane == 31)
+            warp_total[warp] = scan;
+        __syncthreads();
+        if (tid < digits) {
+            int before = scan - total + prior;
+            for (int w = 0; w < warp; ++w)
+                before += warp_total[w];
+            first[tid] = before;
+        }
+        __syncthreads();
+        for (int s0 = w_lo; s0 < w_end; s0 += 32) {
+            const int i = s0 + lane;
+            const bool there = i < w_end;
+            const int key = there ? key_in[i] : -1;
+            const int d = there ? key >> shift & (digits - 1) : -1;
+            const unsigned same = __match_any_sync(kAll, d);
+            if (there) {
+                const int at = first[d] + next[warp * digits + d] +
+                               __popc(same & ((1u << lane) - 1u));
+                const int place = (from ^ 1) * n + (at & (n - 1));
+                const unsigned owner = static_cast<unsigned>(at) >> log_n;
+                asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(remote(keys + place, owner)),
+                             "r"(key)
+                             : "memory");
+                asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(remote(order + place, owner)),
+                             "r"(order_in[i])
+                             : "memory");
+            }
+            __syncwarp();
+            if (there && lane == __ffs(same) - 1)
+                next[warp * digits + d] += __popc(same);
+            __syncwarp();
+        }
+        sort_barrier();
+    }
+    for (int i = tid; i < mine; i += kSortThreads) {
+        const int key = keys[from * n + i];
+        store_i32(a.keys_out + lo + i, key);
+        store_i32(a.order_out + lo + i, order[from * n + i]);
+        // the bits were cleared before the last barrier; one for each run of the CTA
+        if (key < static_cast<int>(e.vocab) && (i == 0 || keys[from * n + i - 1] != key) &&
+            LPC_WRITE_OK(a.used + (key >> 5), 4))
+            atomicOr(a.used + (key >> 5), 1u << (key & 31));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sums of the sorted tokens' rows.
+// ---------------------------------------------------------------------------
+
+constexpr int kAhead = 8;        // rows that a lane loads before it adds them
+constexpr int kMaxTile = 1024;   // sorted tokens of a CTA
+
+struct SumArgs {
+    const int32_t *keys, *order;
+    const uint32_t *used;
+    float *head, *tail;  // [tiles][hidden]: runs that came from the tile before, that go on
+    int tokens, tile, tiles;
+    size_t sum_ctas;     // the others clear
+    unsigned every;      // every so many CTAs one that sums, as long as there are any
+    int clear;           // rows of the table that one of the others clears
+    size_t cleared;      // rows that the sort's launch has cleared
+};
+
+__device__ __forceinline__ int key_at(const SumArgs &s, long long i)
+{
+    return i >= 0 && i < s.tokens ? load_i32(s.keys + i) : -1;
+}
+
+// Rows of the table that a CTA clears: some 64 KB of them, a power of 2 up to 32.
+int rows_to_clear(size_t hidden)
+{
+    int rows = 1;
+    while (rows < 32 && rows * hidden * sizeof(float) < 64 * 1024)
+        rows *= 2;
+    return rows;
+}
+
 template <int DT, int W>
 __global__ void __launch_bounds__(kLanes)
 embed_sums_kernel(const __grid_constant__ EmbedArgs a, const SumArgs s, const RowCut c)
@@ -387,53 +627,56 @@ embed_sums_kernel(const __grid_constant__ EmbedArgs a, const SumArgs s, const Ro
     wait_prior_grid();
     using Cols = LaneCols<DT, W>;
     constexpr int kCols = Cols::kCols;
-    const int which = static_cast<int>(threadIdx.x) / c.lanes;
-    const int lane = static_cast<int>(threadIdx.x) - which * c.lanes;
-    if (blockIdx.x >= s.sum_ctas) {  // clears rows without a token
-        const size_t v0 = (blockIdx.x - s.sum_ctas) * kClearRows;
+    // the CTAs that sum wait for memory, the others keep it busy meanwhile
+    const size_t sums_before = min(s.sum_ctas, (blockIdx.x + static_cast<size_t>(s.every) - 1) / s.every);
+    if (blockIdx.x % s.every != 0 || sums_before == s.sum_ctas) {
+        const size_t v0 = s.cleared + (blockIdx.x - sums_before) * s.clear;
         const uint32_t bits =
-            s.used != nullptr && LPC_READ_OK(s.used + v0 / 32, 4) ? s.used[v0 / 32] : 0u;
-        const float zero[kCols] = {};
-        for (int i = which; i < kClearRows; i += c.rows) {
-            if (v0 + i >= a.vocab || (bits >> ((v0 + i) % 32) & 1u) != 0)
-                continue;
-            for (unsigned seg = 0; seg < c.segs; ++seg) {
-                const Cols cols{(static_cast<size_t>(seg) * c.lanes + lane) * kCols, a.hidden};
-                if (cols.col < a.hidden)
-                    cols.store_f(a.dtable, v0 + i, zero);
-            }
-        }
+            (s.used != nullptr && LPC_READ_OK(s.used + v0 / 32, 4) ? s.used[v0 / 32] : 0u) >>
+            (v0 % 32);
+        clear_rows<DT, W>(a, v0, s.clear, &bits);
         return;
     }
-    const long long tile = static_cast<long long>(blockIdx.x / c.segs) * c.rows + which;
-    const Cols cols{(static_cast<size_t>(blockIdx.x % c.segs) * c.lanes + lane) * kCols, a.hidden};
-    if (tile >= s.tiles || cols.col >= a.hidden)
+    // the keys of the CTA's tiles with one on either side, and the tokens
+    extern __shared__ int keys_smem[];
+    const size_t cta = sums_before;
+    const long long cta_tile = static_cast<long long>(cta / c.segs) * c.rows;
+    const int span = s.tile * c.rows;
+    int *const keys = keys_smem, *const order = keys_smem + span + 2;
+    const long long cta_lo = cta_tile * s.tile;
+    for (int i = threadIdx.x; i < span + 2; i += blockDim.x) {
+        keys[i] = key_at(s, cta_lo + i - 1);
+        if (i < span && cta_lo + i < s.tokens)
+            order[i] = load_i32(s.order + cta_lo + i);
+    }
+    __syncthreads();
+    const Place p = place_of(c, cta);
+    const Cols cols{static_cast<size_t>(p.piece) * kCols, a.hidden};
+    const long long tile = static_cast<long long>(p.row);
+    if (p.idle || tile >= s.tiles || cols.col >= a.hidden)
         return;
     const long long lo = tile * s.tile;
-    const long long end = min(lo + s.tile, static_cast<long long>(s.tokens));
+    const int first = static_cast<int>(lo - cta_lo);  // keys[first + 1] is the tile's first
+    const int n = static_cast<int>(min(static_cast<long long>(s.tile), s.tokens - lo));
     const int vocab = static_cast<int>(a.vocab);
     float acc[kCols] = {};
-    int run = key_at(s, lo);
-    bool started = key_at(s, lo - 1) != run;  // the run begins in this tile
-    for (long long i0 = lo; i0 < end && run != vocab; i0 += kAhead) {
-        int key[kAhead + 1];
+    bool started = keys[first] != keys[first + 1];  // the run begins in this tile
+    for (int i0 = 0; i0 < n && keys[first + 1 + i0] != vocab; i0 += kAhead) {
         typename Pack<DT, W>::Raw raw[kAhead][Cols::kPacks];
 #pragma unroll
-        for (int j = 0; j <= kAhead; ++j)
-            key[j] = key_at(s, i0 + j);
-#pragma unroll
         for (int j = 0; j < kAhead; ++j)
-            if (i0 + j < end && key[j] != vocab)
-                cols.load(a.dout, static_cast<size_t>(load_i32(s.order + i0 + j)), raw[j]);
+            if (i0 + j < n && keys[first + 1 + i0 + j] != vocab)
+                cols.load(a.dout, static_cast<size_t>(order[first + i0 + j]), raw[j]);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            if (i0 + j >= end || key[j] == vocab)
+            const int at = first + 1 + i0 + j;
+            if (i0 + j >= n || keys[at] == vocab)
                 break;
             cols.add(raw[j], acc);
-            const bool ends = key[j + 1] != key[j];
-            if (ends || i0 + j + 1 == end) {
+            const bool ends = keys[at + 1] != keys[at];
+            if (ends || i0 + j + 1 == n) {
                 if (started && ends)
-                    cols.finish(a, static_cast<size_t>(key[j]), acc);
+                    cols.finish(a, static_cast<size_t>(keys[at]), acc);
                 else
                     cols.store_f(started ? s.tail : s.head, static_cast<size_t>(tile), acc);
                 started = true;
@@ -441,7 +684,6 @@ embed_sums_kernel(const __grid_constant__ EmbedArgs a, const SumArgs s, const Ro
                 for (int q = 0; q < kCols; ++q)
                     acc[q] = 0.0f;
             }
-            run = key[j + 1];
         }
     }
 }
@@ -454,26 +696,29 @@ embed_join_kernel(const __grid_constant__ EmbedArgs a, const SumArgs s, const Ro
     wait_prior_grid();
     using Cols = LaneCols<DT, W>;
     constexpr int kCols = Cols::kCols;
-    const int which = static_cast<int>(threadIdx.x) / c.lanes;
-    const int lane = static_cast<int>(threadIdx.x) - which * c.lanes;
-    const long long tile = static_cast<long long>(blockIdx.x / c.segs) * c.rows + which;
-    const Cols cols{(static_cast<size_t>(blockIdx.x % c.segs) * c.lanes + lane) * kCols, a.hidden};
-    if (tile >= s.tiles || cols.col >= a.hidden)
+    const Place p = place_of(c, blockIdx.x);
+    const long long tile = static_cast<long long>(p.row);
+    const Cols cols{static_cast<size_t>(p.piece) * kCols, a.hidden};
+    if (p.idle || tile >= s.tiles || cols.col >= a.hidden)
         return;
     const long long lo = tile * s.tile, next = lo + s.tile;
-    const int run = key_at(s, next - 1);
-    if (next >= s.tokens || run == static_cast<int>(a.vocab) || key_at(s, next) != run)
-        return;  // ends with the tile
-    if (key_at(s, lo) == run && key_at(s, lo - 1) == run)
-        return;  // began before it
-    // the last tile of the run: its first key is the run's, the next tile's is not
-    long long at = tile + 1, above = s.tiles;  // key of tile `at` is the run's, of `above` not
-    while (above - at > 1) {
-        const long long mid = (at + above) / 2;
-        if (key_at(s, mid * s.tile) == run)
-            at = mid;
-        else
-            above = mid;
+    const int run = key_at(s, next - 1), after = key_at(s, next);
+    const int start = key_at(s, lo), before = key_at(s, lo - 1);
+    if (next >= s.tokens || after != run || run == static_cast<int>(a.vocab) ||
+        (start == run && before == run))
+        return;  // ends with the tile, or began before it
+    // the last tile whose first key is the run's: some tiles on at a time
+    long long at = tile + 1;
+    for (bool more = true; more && at + 1 < s.tiles;) {
+        int key[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            key[j] = key_at(s, (at + 1 + j) * s.tile);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            more = more && key[j] == run;
+            at += more ? 1 : 0;
+        }
     }
     float acc[kCols];
     cols.load_f(s.tail, static_cast<size_t>(tile), acc);
@@ -493,14 +738,115 @@ embed_join_kernel(const __grid_constant__ EmbedArgs a, const SumArgs s, const Ro
     cols.finish(a, static_cast<size_t>(run), acc);
 }
 
+// ---------------------------------------------------------------------------
+// Few tokens: one launch, without a sort. A CTA for each token looks through all ids:
+// if an earlier token has the same row it has nothing to do, else it adds up the rows
+// of the tokens that have. Where they are many, kSlices groups of lanes take
+// consecutive parts of that list, and their sums are added in order.
+// ---------------------------------------------------------------------------
+
+constexpr int kFewTokens = 512;
+constexpr int kSlices = 4;
+constexpr int kLongList = 32;
+
+template <int DT, int W>
+__global__ void __launch_bounds__(kLanes)
+embed_few_kernel(const __grid_constant__ EmbedArgs a, int clear)
+{
+    wait_prior_grid();
+    using Cols = LaneCols<DT, W>;
+    constexpr int kCols = Cols::kCols;
+    __shared__ uint32_t same[kFewTokens / 32];  // bit t: token t has this CTA's row
+    __shared__ int list[kFewTokens];
+    __shared__ float part[kLanes][kCols + 1];
+    const int T = static_cast<int>(a.tokens), tid = threadIdx.x, lane = tid & 31;
+    if (blockIdx.x >= a.tokens) {
+        const size_t v0 = (blockIdx.x - a.tokens) * clear;
+        uint32_t bits = 0;
+        for (int t = tid; t < T; t += kLanes) {
+            const long long row = row_of(a, t) - static_cast<long long>(v0);
+            if (row >= 0 && row < clear)
+                bits |= 1u << row;
+        }
+        if (tid == 0)
+            same[0] = 0;
+        __syncthreads();
+        if (bits != 0)
+            atomicOr(&same[0], bits);
+        __syncthreads();
+        clear_rows<DT, W>(a, v0, clear, same);
+        return;
+    }
+    const int mine = static_cast<int>(blockIdx.x);
+    const long long row = row_of(a, mine);
+    if (row < 0)
+        return;
+    bool earlier = false;
+    for (int w = tid >> 5; w * 32 < T; w += kLanes / 32) {
+        const int t = w * 32 + lane;
+        const bool hit = t < T && row_of(a, t) == row;
+        earlier = earlier || (hit && t < mine);
+        const uint32_t bits = __ballot_sync(kAll, hit);
+        if (lane == 0)
+            same[w] = bits;
+    }
+    if (__syncthreads_or(earlier))
+        return;
+    int n = 0;
+    for (int w = 0; w * 32 < T; ++w)
+        n += __popc(same[w]);
+    for (int i = tid; i < n; i += kLanes) {
+        int left = i, w = 0;
+        while (left >= __popc(same[w]))
+            left -= __popc(same[w++]);
+        list[i] = w * 32 + static_cast<int>(__fns(same[w], 0, left + 1));
+    }
+    __syncthreads();
+    const int slices = n > kLongList ? kSlices : 1, lanes = kLanes / slices;
+    const int slice = tid / lanes, place = tid - slice * lanes;
+    const int each = (n + slices - 1) / slices;
+    const int end = min(n, (slice + 1) * each);
+    for (size_t col0 = 0; col0 < a.hidden; col0 += static_cast<size_t>(lanes) * kCols) {
+        const Cols cols{col0 + static_cast<size_t>(place) * kCols, a.hidden};
+        const bool in = cols.col < a.hidden;
+        float acc[kCols] = {};
+        for (int i0 = slice * each; in && i0 < end; i0 += kAhead) {
+            typename Pack<DT, W>::Raw raw[kAhead][Cols::kPacks];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i0 + j < end)
+                    cols.load(a.dout, static_cast<size_t>(list[i0 + j]), raw[j]);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i0 + j < end)
+                    cols.add(raw[j], acc);
+        }
+        if (slices > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < kCols; ++q)
+                part[tid][q] = acc[q];
+            __syncthreads();
+            if (slice == 0)
+                for (int r = 1; r < kSlices; ++r)
+#pragma unroll
+                    for (int q = 0; q < kCols; ++q)
+                        acc[q] += part[r * lanes + place][q];
+        }
+        if (slice == 0 && in)
+            cols.finish(a, static_cast<size_t>(row), acc);
+    }
+}
+
 // Sorted tokens of a tile: few, so that small batches fill the GPU, and more where
 // there are many tokens, so that the partial rows stay few.
 int tile_len(size_t tokens)
 {
-    if (tokens <= 4096)
+    if (tokens <= 8192)
         return 8;
-    const size_t len = (tokens / 4096 + 31) / 32 * 32;
-    return static_cast<int>(len > 32 ? len : 32);
+    size_t len = (tokens / 4096 + 31) / 32 * 32;
+    len = len > 32 ? len : 32;
+    return static_cast<int>(len < kMaxTile ? len : kMaxTile);
 }
 
 size_t aligned(size_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -528,32 +874,82 @@ Scratch scratch(size_t tokens, size_t vocab, size_t hidden)
 
 template <int DT, int W> cudaError_t embed_dt(const EmbedArgs &a, cudaStream_t st)
 {
-    const RowCut c = cut(a.hidden, a.dtype);
+    RowCut c = cut(a.hidden, a.dtype, kPieces, kLanes);
+    if (a.tokens * c.segs < static_cast<size_t>(kSms) * 4 * c.rows)  // few: a piece a lane
+        c = cut(a.hidden, a.dtype, 1, kLanes);
     const size_t ctas = (a.tokens + c.rows - 1) / c.rows * c.segs;
     return launch_kernel_block(embed_kernel<DT, W>, ctas, c.lanes * c.rows, 0, st, a, c);
+}
+
+template <int DT, int W> cudaError_t few_dt(const EmbedArgs &a, cudaStream_t st)
+{
+    const int clear = rows_to_clear(a.hidden);
+    const size_t clear_ctas = a.accumulate ? 0 : (a.vocab + clear - 1) / clear;
+    return launch_kernel_block(embed_few_kernel<DT, W>, a.tokens + clear_ctas, kLanes, 0, st, a,
+                               clear);
+}
+
+// The sort in one launch, and with it the first `cleared` rows of the table cleared
+// where they have no token: as much as the sort takes time for, on the SMs that it
+// leaves free.
+template <int DT, int W>
+cudaError_t cluster_sort_dt(const EmbedArgs &a, const RadixArgs &r, int passes, size_t &cleared,
+                            cudaStream_t st)
+{
+    const size_t free = kSms - kSortCtas;
+    constexpr int kMostRows = 512;
+    int log_n = 11, sorting = 1;
+    while (sorting < kSortCtas && (sorting << log_n) < r.tokens)
+        sorting *= 2;
+    while ((sorting << log_n) < r.tokens)
+        ++log_n;
+    const size_t smem =
+        ((static_cast<size_t>(4) << log_n) + (kSortWarps + 2) * (1u << r.bits)) * sizeof(int);
+    // some 8 us and 0.7 ns a token, at 45 GB/s an SM
+    const size_t bytes = 256 * 1024 + 32 * a.tokens;
+    int rows = kMostRows;
+    while (rows > 1 && rows * a.hidden * sizeof(float) > bytes)
+        rows /= 2;
+    const size_t need = a.accumulate ? 0 : (a.vocab + rows - 1) / rows;
+    // whole clusters
+    const size_t ctas = (need < free ? need : free) / kSortCtas * kSortCtas;
+    cleared = ctas * rows;
+    // always the same value: calls of several threads must not undo each other's
+    const cudaError_t e = cudaFuncSetAttribute(
+        cluster_sort_kernel<DT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    if (e != cudaSuccess)
+        return e;
+    return launch_kernel_cluster(cluster_sort_kernel<DT, W>, sorting + ctas, kSortThreads, sorting,
+                                 smem, st, a, r, passes, log_n, sorting, rows);
 }
 
 template <int DT, int W>
 cudaError_t sums_dt(const EmbedArgs &a, SumArgs s, cudaStream_t st)
 {
-    const RowCut c = cut(a.hidden, a.dtype);
+    RowCut c = cut(a.hidden, a.dtype, 1, kLanes);
+    while (c.rows > 1 && c.rows * s.tile > kMaxTile)
+        c.rows /= 2;
     s.sum_ctas = (static_cast<size_t>(s.tiles) + c.rows - 1) / c.rows * c.segs;
-    const size_t clear = a.accumulate ? 0 : (a.vocab + kClearRows - 1) / kClearRows;
+    s.clear = rows_to_clear(a.hidden);
+    const size_t clear = a.accumulate || s.cleared >= a.vocab
+                             ? 0
+                             : (a.vocab - s.cleared + s.clear - 1) / s.clear;
     if (s.sum_ctas + clear == 0)
         return cudaSuccess;
+    s.every = s.sum_ctas == 0 ? 1 : static_cast<unsigned>((s.sum_ctas + clear) / s.sum_ctas);
+    const size_t smem = (2 * static_cast<size_t>(s.tile) * c.rows + 2) * sizeof(int);
     const cudaError_t e = launch_kernel_block(embed_sums_kernel<DT, W>, s.sum_ctas + clear,
-                                              c.lanes * c.rows, 0, st, a, s, c);
+                                              kLanes, smem, st, a, s, c);
     if (e != cudaSuccess || s.tiles <= 1)
         return e;
-    return launch_kernel_block(embed_join_kernel<DT, W>, s.sum_ctas, c.lanes * c.rows, 0, st, a, s,
-                               c);
+    return launch_kernel_block(embed_join_kernel<DT, W>, s.sum_ctas, kLanes, 0, st, a, s, c);
 }
 
 }  // namespace
 
 size_t embed_workspace(size_t tokens, size_t vocab, size_t hidden)
 {
-    return tokens == 0 ? 0 : scratch(tokens, vocab, hidden).all();
+    return tokens <= kFewTokens ? 0 : scratch(tokens, vocab, hidden).all();
 }
 
 cudaError_t launch_embed(const EmbedArgs &a, cudaStream_t st)
@@ -564,6 +960,8 @@ cudaError_t launch_embed(const EmbedArgs &a, cudaStream_t st)
 cudaError_t launch_embed_backward(const EmbedArgs &a, cudaStream_t st)
 {
     SumArgs s = {};
+    if (a.tokens > 0 && a.tokens <= kFewTokens)
+        return LPC_BY_ROW(few_dt, a.dtype, a.hidden, a, st);
     if (a.tokens > 0) {
         const Scratch w = scratch(a.tokens, a.vocab, a.hidden);
         const SortPlan p = sort_plan(a.tokens, a.vocab);
@@ -585,7 +983,17 @@ cudaError_t launch_embed_backward(const EmbedArgs &a, cudaStream_t st)
         r.bits = p.bits;
         r.chunks = p.chunks;
         r.chunk_len = p.chunk_len;
-        for (int i = 0; i < p.passes; ++i) {
+        if (a.tokens <= kClusterTokens) {
+            r.keys_out = keys[0];
+            r.order_out = order[0];
+            const cudaError_t e =
+                LPC_BY_ROW(cluster_sort_dt, a.dtype, a.hidden, a, r, p.passes, s.cleared, st);
+            if (e != cudaSuccess)
+                return e;
+            r.keys = r.keys_out;
+            r.order = r.order_out;
+        }
+        for (int i = 0; i < p.passes && a.tokens > kClusterTokens; ++i) {
             r.shift = i * p.bits;
             r.keys_out = keys[i & 1];
             r.order_out = order[i & 1];

@@ -699,7 +699,7 @@ int expert_balance(const void *logits, lpcoll_dtype dtype, size_t ntokens, int n
         return LPCOLL_ERR_ARG;
     st = first_error({check_array(logits, ntokens), check_array(ids, ntokens),
                       check_optional(valid), check_ptr(loss), check_ptr(counts),
-                      check_ptr(prob_sums), check_ptr(workspace)});
+                      check_ptr(prob_sums), check_array(workspace, need)});
     if (st != LPCOLL_OK)
         return st;
     debug_begin();

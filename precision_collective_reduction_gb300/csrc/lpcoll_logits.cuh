@@ -1,4 +1,4 @@
-// lpcoll_logits.cuh -- a token's logits, one warp per token: what the router and
+// lpcoll_logits.cuh -- a token's logits, one warp or part of one per token: what the router and
 // the balance loss share. Internal linkage: each translation unit has its own.
 #pragma once
 
@@ -8,15 +8,30 @@ namespace lpc {
 
 namespace {
 
+// 2^x, 2 ulp; results below the normal range are 0.
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A term e^d of a softmax's sum, d <= 0: the rounding of the product moves it
+// by |d| 2^-24 of itself, at most 2^-25 of the sum's largest term.
+__device__ __forceinline__ float exp_term(float d)
+{
+    return exp2_fast(__fmul_rn(d, 1.44269504f));
+}
+
 // The PER experts of a lane come in runs of kRun consecutive ones, run r at
-// (r * 32 + lane) * kRun, so that a run is one access where rows of logits
-// are a multiple of a run.
+// (r * LANES + lane) * kRun for the LANES lanes of a token, so that a run is one
+// access where rows of logits are a multiple of a run.
 template <int DT, int PER> constexpr int kRun = PER < Fmt<DT>::kVec ? PER : Fmt<DT>::kVec;
 
-template <int DT, int PER> __device__ __forceinline__ int expert_of(int i, int lane)
+template <int DT, int PER, int LANES = 32> __device__ __forceinline__ int expert_of(int i, int lane)
 {
     constexpr int R = kRun<DT, PER>;
-    return (i / R * 32 + lane) * R + i % R;
+    return (i / R * LANES + lane) * R + i % R;
 }
 
 template <int BYTES> struct RunBytes;
@@ -31,7 +46,7 @@ template <> struct RunBytes<16> {
 };
 
 // -infinity where there is no expert.
-template <int DT, int PER>
+template <int DT, int PER, int LANES = 32>
 __device__ __forceinline__ void load_logits(const void *logits, size_t t, int experts, int lane,
                                             float (&x)[PER])
 {
@@ -42,7 +57,7 @@ __device__ __forceinline__ void load_logits(const void *logits, size_t t, int ex
     if (experts % R == 0) {
 #pragma unroll
         for (int r = 0; r < PER / R; ++r) {
-            const int e = (r * 32 + lane) * R;
+            const int e = (r * LANES + lane) * R;
             typename Pack<DT, kEs>::Raw v[R];
             if (e < experts && LPC_READ_OK(row + e * kEs, R * kEs)) {
                 const Raw raw = *reinterpret_cast<const Raw *>(row + e * kEs);
@@ -58,7 +73,7 @@ __device__ __forceinline__ void load_logits(const void *logits, size_t t, int ex
     } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = expert_of<DT, PER>(i, lane);
+            const int e = expert_of<DT, PER, LANES>(i, lane);
             float one[1] = {-INFINITY};
             if (e < experts)
                 widen_pack<DT, kEs>(load_pack<DT, kEs>(row, e), one);

@@ -36,21 +36,6 @@ __device__ __forceinline__ float key_logit(uint32_t k)
     return __uint_as_float(k ^ ((k >> 31) != 0 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// 2^x, 2 ulp; results below the normal range are 0.
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// A term e^d of a softmax's sum, d <= 0: the rounding of the product moves it
-// by |d| 2^-24 of itself, at most 2^-25 of the sum's largest term.
-__device__ __forceinline__ float exp_term(float d)
-{
-    return exp2_fast(__fmul_rn(d, 1.44269504f));
-}
-
 // Descending order of v[LO .. LO + N) (Batcher's odd-even merge sort); merge_down
 // does it for the elements R apart, whose halves are in order.
 template <int P, int Q, int PER> __device__ __forceinline__ void order(uint32_t (&v)[PER])

@@ -446,7 +446,8 @@ def some_ids(g, T, V, first, kind):
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("T,V,H", [(1, 1, 1), (1, 100, 4096), (7, 3, 5), (64, 700, 96),
                                    (33, 40, 129), (500, 1000, 66), (2100, 5000, 68),
-                                   (5000, 300, 40), (70, 1024, 2051), (40, 50, 8200)])
+                                   (5000, 300, 40), (70, 1024, 2051), (40, 50, 8200),
+                                   (512, 90, 20), (513, 90, 20), (1100, 60, 12), (9000, 33, 8)])
 @pytest.mark.parametrize("kind", ["mixed", "same", "none"])
 def test_embed(lib, dt, T, V, H, kind):
     g = gen(T, V, H)
@@ -481,10 +482,12 @@ def test_embed(lib, dt, T, V, H, kind):
         assert same(a, b)
 
 
-@pytest.mark.parametrize("V", [511, 512, 1 << 18, (1 << 18) + 1, 3_000_000])
-def test_embed_gradient_of_vocabularies_at_the_sort_digits(lib, V):
-    g = gen(V)
-    T, H = 3000, 4
+@pytest.mark.parametrize("T,V", [(3000, 511), (3000, 512), (3000, 1 << 18), (3000, (1 << 18) + 1),
+                                 (3000, 3_000_000), (8192, 40000), (8193, 40000), (65536, 700),
+                                 (65537, 700), (70001, 300_000)])
+def test_embed_gradient_at_the_sizes_of_the_sort(lib, T, V):
+    g = gen(T, V)
+    H = 4
     ids = g.integers(0, V, size=T)
     ids[:4] = [0, V - 1, V, -1]
     ids[100:400] = V - 1

@@ -85,12 +85,12 @@ def test_residual_dropout_refusals(L):
 
 
 def test_balance_refusals(L):
-    need = L.expert_balance_workspace_bytes(4, 8)
-    assert need > 0 and L.expert_balance_workspace_bytes(4, 0) == 0
+    need = L.expert_balance_workspace_bytes(4000, 8)
+    assert need > 0 and L.expert_balance_workspace_bytes(4000, 0) == 0
     assert L.expert_balance_workspace_bytes(4, 1025) == 0
     assert L.expert_balance_workspace_bytes((1 << 31) - 1, 1024) <= 304 * 2049 * 4
 
-    def f(z=A, dt=0, T=4, E=8, ids=A, K=2, valid=None, coef=0.01, loss=A, counts=A, sums=A, ws=A,
+    def f(z=A, dt=0, T=4000, E=8, ids=A, K=2, valid=None, coef=0.01, loss=A, counts=A, sums=A, ws=A,
           n=need):
         return L.expert_balance(z, dt, T, E, ids, K, valid, coef, loss, counts, sums, ws, n, None)
     assert f(dt=2) == ARG and f(E=0) == ARG and f(E=1025) == ARG and f(K=0) == ARG
@@ -120,11 +120,11 @@ def test_embed_refusals(L):
     assert f(table=None) == ARG and f(ids=None) == ARG and f(out=None) == ARG
     for name in ("table", "ids", "out"):
         assert f(**{name: A + 8}) == ALIGN
-    need = L.token_embed_backward_workspace_bytes(4, 16, 64)
+    need = L.token_embed_backward_workspace_bytes(4000, 16, 64)
     assert need > 0 and L.token_embed_backward_workspace_bytes(0, 16, 64) == 0
     assert L.token_embed_backward_workspace_bytes(1 << 31, 16, 64) == 0
 
-    def g(dout=A, ids=A, index=0, first=0, T=4, V=16, H=64, dt=0, scale=1.0, acc=0, dtable=A,
+    def g(dout=A, ids=A, index=0, first=0, T=4000, V=16, H=64, dt=0, scale=1.0, acc=0, dtable=A,
           ws=A, n=need):
         return L.token_embed_backward(dout, ids, index, first, T, V, H, dt, scale, acc, dtable,
                                       ws, n, None)
