@@ -535,9 +535,6 @@ __device__ __forceinline__ RowSums team_grad_sums(float mine, float sum, const S
     return spread(mean, split_sum(s));
 }
 
-// A row's x, less the warp's mean, and dn stay in registers in FP32 from the sums to
-// the outputs, as do the weights: reading them again from shared memory costs the
-// conversions again.
 template <int DT, int W, int kElems, bool kDrop>
 __global__ void __launch_bounds__(kTeamThreads, 1)
 layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int streams)
@@ -567,36 +564,32 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
     for (int s = 0; s < deal.stages; ++s)
         fetch(me.t0 + s * me.step, s);
 
-    Vec<kN> w[NV], s_w[NV], s_b[NV];
+    typename Pack<DT, W>::Raw w[NV];
+    Vec<kN> s_w[NV], s_b[NV];
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-        w[c] = a.w != nullptr && me.has(c) ? load_vec_of<DT, W>(a.w, me.col(c)) : splat<kN>(1.0f);
+        w[c] = a.w != nullptr && me.has(c) ? load_pack<DT, W>(a.w, me.col(c)) : all_of<DT, W>(1.0f);
         s_w[c] = s_b[c] = splat<kN>(0.0f);
     }
 
     int stage = 0, turn = 0;
     for (size_t t = me.t0; t < a.tokens; t += me.step, turn ^= 1) {
         me.ready(deal.stages - 1);
-        Vec<kN> d[NV], dn[NV];
         Acc<kN> total = {}, sq = {}, sa = {}, sqs = {};
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            if (!me.has(c))
-                continue;
-            d[c] = me.read(t, stage, kGradX, c);
-            dn[c] = me.read(t, stage, kGradDn, c);
-            add_values<kN>(total, d[c]);
-        }
+        for (int c = 0; c < NV; ++c)
+            if (me.has(c))
+                add_values<kN>(total, me.read(t, stage, kGradX, c));
         const float sum = warp_sum(fold(total));
-        const float own = sum * share.inv_own;  // the warp's mean
+        const Vec<kN> about = splat<kN>(-(sum * share.inv_own));  // the warp's mean
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             if (!me.has(c))
                 continue;
-            d[c] = plus(d[c], splat<kN>(-own));
-            const Vec<kN> q = mul(dn[c], w[c]);
-            add_products(sq, d[c], d[c]);
-            add_products(sa, q, d[c]);
+            const Vec<kN> d = plus(me.read(t, stage, kGradX, c), about);
+            const Vec<kN> q = mul(me.read(t, stage, kGradDn, c), unpack<DT, W>(w[c]));
+            add_products(sq, d, d);
+            add_products(sa, q, d);
             add_values<kN>(sqs, q);
         }
         const RowSums s = team_grad_sums(split_sum({{fold(sq), fold(sa), fold(sqs)}}), sum, share,
@@ -607,15 +600,16 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
             keep.make(rnd, me, t);
         const float r = inv_rms(s.m2, per_hidden, a.eps);
         const float c1 = s.q * per_hidden, c2 = r * r * (s.a * per_hidden);
-        const Vec<kN> centre = splat<kN>(own - s.mean);
+        const Vec<kN> centre = splat<kN>(-s.mean);
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             if (!me.has(c))
                 continue;
-            const Vec<kN> x = plus(d[c], centre);
-            s_w[c] = fma(mul(r, x), dn[c], s_w[c]);
-            s_b[c] = plus(s_b[c], dn[c]);
-            Vec<kN> q = fma(-c2, x, fma(dn[c], w[c], splat<kN>(-c1)));
+            const Vec<kN> d = plus(me.read(t, stage, kGradX, c), centre);
+            const Vec<kN> dn = me.read(t, stage, kGradDn, c);
+            s_w[c] = fma(mul(r, d), dn, s_w[c]);
+            s_b[c] = plus(s_b[c], dn);
+            Vec<kN> q = fma(-c2, d, fma(dn, unpack<DT, W>(w[c]), splat<kN>(-c1)));
             q = given ? fma(r, q, me.read(t, stage, kGradDx, c)) : mul(r, q);
             if (want_dx)
                 store_vec_of<DT, W>(a.dx, me.elem(t, c), q);
