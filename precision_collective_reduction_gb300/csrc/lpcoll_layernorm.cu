@@ -7,42 +7,53 @@ namespace lpc {
 
 namespace {
 
-// Column sums of the workspace: a CTA adds 32 columns of one of the two sums.
-// 32 threads per column take every 32nd part, all in flight at once (kPer of
-// them, for as many CTAs per SM), and a warp adds up a column's 32.
-constexpr int kPer = (kSms + 31) / 32;
+// Column sums of the workspace: a CTA adds 32 columns of one of the two sums. Of a
+// part, kVec columns a thread; the CTA's threads take as many parts at once as they
+// can, each thread all of its own with their loads in flight together, and a warp adds
+// up a column's threads. Measured with the stores that leave the parts: 8192 columns of
+// 152 CTAs 14 us with 4-byte accesses and 1024 threads.
+constexpr int kSumThreads = 256;
 
-template <int kPerSm>
-__global__ void __launch_bounds__(1024)
+template <int kVec>
+__global__ void __launch_bounds__(kSumThreads)
 layer_norm_sums_kernel(const float *partial, float *dw, float *db, int hidden, int parts,
                        int column_ctas)
 {
     wait_prior_grid();
-    __shared__ float red[32][33];
+    constexpr int kAcross = 32 / kVec;                // threads of a part's 32 columns
+    constexpr int kDown = kSumThreads / kAcross;      // parts at once
+    constexpr int kSteps = (kMaxCtas * kSms + kDown - 1) / kDown;
+    __shared__ float red[kDown][33];
     const int which = blockIdx.x / column_ctas;
     float *const out = which == 0 ? dw : db;
     if (out == nullptr)
         return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int first = (blockIdx.x % column_ctas) * 32;
-    const float *p = partial + static_cast<size_t>(which) * parts * hidden + first + lane;
-    constexpr int kParts = kPer * kPerSm;
-    float v[kParts];
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) {
-        const int q = i * 32 + warp;
-        v[i] = q < parts && first + lane < hidden ? load_f32(p + static_cast<size_t>(q) * hidden)
-                                                  : 0.0f;
+    const int across = tid % kAcross, down = tid / kAcross;
+    const int col = first + across * kVec;
+    const float *const p = partial + static_cast<size_t>(which) * parts * hidden;
+    Vec<kVec> sum = {};
+#pragma unroll 8
+    for (int i = 0; i < kSteps; ++i) {
+        const int q = i * kDown + down;
+        if (q < parts && col < hidden)
+            sum = plus(sum, load_vec_of<LPCOLL_F32, 4 * kVec>(p, static_cast<size_t>(q) * hidden + col));
     }
-    float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kParts; ++i)
-        sum += v[i];
-    red[warp][lane] = sum;
+    for (int j = 0; j < kVec; ++j)
+        red[down][across * kVec + j] = sum.v[j];
     __syncthreads();
-    sum = warp_sum(red[lane][warp]);
-    if (lane == 0 && first + warp < hidden)
-        store_f32(out + first + warp, sum);
+    for (int c = warp; c < 32; c += kSumThreads / 32) {
+        float v = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kDown; r += 32)
+            if (kDown >= 32 || lane < kDown)
+                v += red[r + (kDown >= 32 ? lane : lane % kDown)][c];
+        v = warp_sum(v);
+        if (lane == 0 && first + c < hidden)
+            store_f32(out + first + c, v);
+    }
 }
 
 }  // namespace
@@ -56,12 +67,9 @@ int layer_norm_parts(size_t tokens, size_t hidden, int dtype, bool dropout)
 
 cudaError_t launch_layer_norm_sums(const LayerNormArgs &a, int parts, cudaStream_t st)
 {
-    static_assert(kMaxCtas == 3, "one kernel per number of CTAs per SM");
     const int ctas = (a.hidden + 31) / 32;
-    const auto kernel = parts <= kSms ? layer_norm_sums_kernel<1>
-                                      : (parts <= 2 * kSms ? layer_norm_sums_kernel<2>
-                                                           : layer_norm_sums_kernel<3>);
-    return launch_kernel_block(kernel, static_cast<size_t>(2) * ctas, 1024, 0, st, a.partial, a.dw,
+    return launch_kernel_block(a.hidden % 4 == 0 ? layer_norm_sums_kernel<4> : layer_norm_sums_kernel<1>,
+                               static_cast<size_t>(2) * ctas, kSumThreads, 0, st, a.partial, a.dw,
                                a.db, a.hidden, parts, ctas);
 }
 

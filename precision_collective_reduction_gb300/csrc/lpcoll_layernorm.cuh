@@ -624,7 +624,7 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
     if (deal.cluster > 1)
         cluster_barrier();  // no CTA leaves while another reads its sums
     if (a.partial != nullptr)
-        leave_sums(me, deal, s_w, s_b, a.partial, reinterpret_cast<float *>(ring_smem));
+        leave_sums<DT, W>(me, deal, s_w, s_b, a.partial, reinterpret_cast<float *>(ring_smem));
 }
 
 // The gradient of rows that fill their teams (no clusters, every thread has all its
@@ -669,32 +669,44 @@ layer_norm_backward_even_kernel(const __grid_constant__ LayerNormArgs a, const D
         s_w[c] = s_b[c] = splat<kN>(0.0f);
     }
 
-    // this thread's parts of the sums of the row in `stage`
-    const auto add_up = [&](size_t t, int stage) {
-        Acc<kN> total = {};
-#pragma unroll
-        for (int c = 0; c < NV; ++c)
-            add_values<kN>(total, me.read(t, stage, kGradX, c));
-        return fold(total);
+    // This thread's parts of the sums of the row in `stage`, in one pass about its
+    // first column x0: with d = x - x0, m = mean d of its n columns,
+    //   sum (x - x0 - m)^2 = sum d^2 - m sum d,  sum q (x - x0 - m) = sum q d - m sum q.
+    // n (x0 - mean)^2 is at most n times those squares, so of their digits no more
+    // are lost than the sum of a row's terms may lose anyway.
+    struct Part {
+        float sum, mean, m2, a, q;
     };
-    const auto add_rest = [&](size_t t, int stage, float sum) {
-        const Vec<kN> about = splat<kN>(-(sum * share.inv_own));
-        Acc<kN> sq = {}, sa = {}, sqs = {};
+    const auto add_up = [&](size_t t, int stage) {
+        Acc<kN> total = {}, sq = {}, sa = {}, sqs = {};
+        float x0 = 0.0f;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-            const Vec<kN> d = plus(me.read(t, stage, kGradX, c), about);
+            const Vec<kN> x = me.read(t, stage, kGradX, c);
+            if (c == 0)
+                x0 = x.v[0];
+            const Vec<kN> d = plus(x, splat<kN>(-x0));
             const Vec<kN> q = mul(me.read(t, stage, kGradDn, c), unpack<DT, W>(w[c]));
+            add_values<kN>(total, d);
             add_products(sq, d, d);
             add_products(sa, q, d);
             add_values<kN>(sqs, q);
         }
-        return Three{{fold(sq), fold(sa), fold(sqs)}};
+        const float sum = fold(total), m = sum * (1.0f / kElems), qs = fold(sqs);
+        return Part{fmaf(static_cast<float>(kElems), x0, sum), x0 + m, fmaf(-m, sum, fold(sq)),
+                    fmaf(-m, qs, fold(sa)), qs};
+    };
+    // The same about the warp's mean.
+    const auto about_warp = [&](const Part &p, float warp_mean) {
+        const float d = p.mean - warp_mean;
+        return Three{{fmaf(kElems * d, d, p.m2), fmaf(d, p.q, p.a), p.q}};
     };
 
     int stage = 0, turn = 0;
     me.ready(deal.stages - 1);
-    float sum = warp_sum(add_up(me.t0, 0));
-    float mine = split_sum(add_rest(me.t0, 0, sum));
+    Part part = add_up(me.t0, 0);
+    float sum = warp_sum(part.sum);
+    float mine = split_sum(about_warp(part, sum * share.inv_own));
     for (size_t t = me.t0; t < a.tokens; t += me.step, turn ^= 1) {
         const int after = stage + 1 == deal.stages ? 0 : stage + 1;
         const size_t t2 = t + me.step;
@@ -713,12 +725,13 @@ layer_norm_backward_even_kernel(const __grid_constant__ LayerNormArgs a, const D
                 v = make_float4(own.m2, own.a, own.q, sum);
         }
         me.ready(deal.stages - 2);
-        float pair[2] = {v.w, add_up(t2, after)};
+        part = add_up(t2, after);
+        float pair[2] = {v.w, part.sum};
         warp_sums(pair);
         const float mean = pair[0] * per_hidden;
         sum = pair[1];
         float joined;
-        split_sums(moved(v, share, mean), add_rest(t2, after, sum), joined, mine);
+        split_sums(moved(v, share, mean), about_warp(part, sum * share.inv_own), joined, mine);
         const RowSums s = spread(mean, joined);
         Keep<kElems, kN> keep;
         if (drop)
@@ -748,7 +761,7 @@ layer_norm_backward_even_kernel(const __grid_constant__ LayerNormArgs a, const D
     }
     copy_wait(0);
     if (a.partial != nullptr)
-        leave_sums(me, deal, s_w, s_b, a.partial, reinterpret_cast<float *>(ring_smem));
+        leave_sums<DT, W>(me, deal, s_w, s_b, a.partial, reinterpret_cast<float *>(ring_smem));
 }
 
 // Accesses that share a group of four columns.

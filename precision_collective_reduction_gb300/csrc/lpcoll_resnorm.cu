@@ -309,7 +309,7 @@ residual_norm_backward_kernel(const __grid_constant__ NormArgs a, const Deal dea
         cluster_barrier();  // no CTA leaves while another reads its sums
 
     if (a.partial != nullptr)
-        leave_sums(me, deal, s_pre, S, a.partial, reinterpret_cast<float *>(ring_smem));
+        leave_sums<DT, W>(me, deal, s_pre, S, a.partial, reinterpret_cast<float *>(ring_smem));
 }
 
 // Column sums of the workspace: a CTA adds 32 columns of one of the two sums.

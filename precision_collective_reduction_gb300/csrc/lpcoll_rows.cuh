@@ -481,12 +481,29 @@ template <int DT, int W, int kElems, int kMode, bool kAlone> struct Member {
             __syncwarp();
     }
 };
+// FP32 values of an access at column `col` of a row of FP32 numbers, in the widest
+// accesses that rows of the access's own width leave aligned.
+template <int DT, int W>
+__device__ __forceinline__ void store_floats(float *row, int col, const Vec<Pack<DT, W>::kN> &x)
+{
+    constexpr int kN = Pack<DT, W>::kN;
+    constexpr int kF = kN < 4 ? kN : 4;
+#pragma unroll
+    for (int j = 0; j < kN; j += kF) {
+        Vec<kF> v;
+#pragma unroll
+        for (int i = 0; i < kF; ++i)
+            v.v[i] = x.v[j + i];
+        store_vec_of<LPCOLL_F32, 4 * kF>(row, col + j, v);
+    }
+}
+
 // Leaves two sums over a CTA's tokens of each of its columns in the workspace,
 // [2][CTAs][hidden]: the teams add theirs in order in shared memory (the rows are
 // done with), then the CTA, or each of a cluster for its columns, writes a row of both.
-template <class M, int kN, int NV>
-__device__ __forceinline__ void leave_sums(const M &me, const Deal &deal, const Vec<kN> (&s0)[NV],
-                                           const Vec<kN> (&s1)[NV], float *partial, float *sums)
+template <int DT, int W, class M, int kN, int NV>
+__device__ __forceinline__ void leave_sums(const M &me, const Deal &deal, Vec<kN> (&s0)[NV],
+                                           Vec<kN> (&s1)[NV], float *partial, float *sums)
 {
     const int H = me.hidden;
     const size_t part = static_cast<size_t>(gridDim.x / deal.cluster) * H;
@@ -499,21 +516,22 @@ __device__ __forceinline__ void leave_sums(const M &me, const Deal &deal, const 
         for (int c = 0; c < NV; ++c) {
             if (!me.has(c))
                 continue;
+            if (deal.groups > 1)
 #pragma unroll
-            for (int j = 0; j < kN; ++j) {
-                const int i = me.col(c) + j;
-                float v0 = s0[c].v[j], v1 = s1[c].v[j];
-                if (g > 0) {
-                    v0 = sums[2 * i] + v0;
-                    v1 = sums[2 * i + 1] + v1;
+                for (int j = 0; j < kN; ++j) {
+                    const int i = me.col(c) + j;
+                    if (g > 0) {
+                        s0[c].v[j] = sums[2 * i] + s0[c].v[j];
+                        s1[c].v[j] = sums[2 * i + 1] + s1[c].v[j];
+                    }
+                    if (g + 1 < deal.groups) {
+                        sums[2 * i] = s0[c].v[j];
+                        sums[2 * i + 1] = s1[c].v[j];
+                    }
                 }
-                if (g + 1 < deal.groups) {
-                    sums[2 * i] = v0;
-                    sums[2 * i + 1] = v1;
-                } else {
-                    store_f32(out + i, v0);
-                    store_f32(out + part + i, v1);
-                }
+            if (g + 1 == deal.groups) {
+                store_floats<DT, W>(out, me.col(c), s0[c]);
+                store_floats<DT, W>(out + part, me.col(c), s1[c]);
             }
         }
     }
