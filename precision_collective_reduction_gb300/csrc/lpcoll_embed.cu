@@ -739,7 +739,8 @@ embed_join_kernel(const __grid_constant__ EmbedArgs a, const SumArgs s, const Ro
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: one launch, without a sort. A CTA for each token looks through all ids:
+// Few tokens: one launch, without a sort. A CTA for each token (and kLanes pieces of
+// its row) looks through all ids:
 // if an earlier token has the same row it has nothing to do, else it adds up the rows
 // of the tokens that have. Where they are many, kSlices groups of lanes take
 // consecutive parts of that list, and their sums are added in order.
@@ -751,7 +752,7 @@ constexpr int kLongList = 32;
 
 template <int DT, int W>
 __global__ void __launch_bounds__(kLanes)
-embed_few_kernel(const __grid_constant__ EmbedArgs a, int clear)
+embed_few_kernel(const __grid_constant__ EmbedArgs a, unsigned segs, int clear)
 {
     wait_prior_grid();
     using Cols = LaneCols<DT, W>;
@@ -760,8 +761,9 @@ embed_few_kernel(const __grid_constant__ EmbedArgs a, int clear)
     __shared__ int list[kFewTokens];
     __shared__ float part[kLanes][kCols + 1];
     const int T = static_cast<int>(a.tokens), tid = threadIdx.x, lane = tid & 31;
-    if (blockIdx.x >= a.tokens) {
-        const size_t v0 = (blockIdx.x - a.tokens) * clear;
+    const size_t sum_ctas = a.tokens * segs;
+    if (blockIdx.x >= sum_ctas) {
+        const size_t v0 = (blockIdx.x - sum_ctas) * clear;
         uint32_t bits = 0;
         for (int t = tid; t < T; t += kLanes) {
             const long long row = row_of(a, t) - static_cast<long long>(v0);
@@ -777,7 +779,7 @@ embed_few_kernel(const __grid_constant__ EmbedArgs a, int clear)
         clear_rows<DT, W>(a, v0, clear, same);
         return;
     }
-    const int mine = static_cast<int>(blockIdx.x);
+    const int mine = static_cast<int>(blockIdx.x / segs);
     const long long row = row_of(a, mine);
     if (row < 0)
         return;
@@ -806,7 +808,9 @@ embed_few_kernel(const __grid_constant__ EmbedArgs a, int clear)
     const int slice = tid / lanes, place = tid - slice * lanes;
     const int each = (n + slices - 1) / slices;
     const int end = min(n, (slice + 1) * each);
-    for (size_t col0 = 0; col0 < a.hidden; col0 += static_cast<size_t>(lanes) * kCols) {
+    const size_t seg_lo = static_cast<size_t>(blockIdx.x % segs) * kLanes * kCols;
+    const size_t seg_end = min(a.hidden, seg_lo + kLanes * kCols);
+    for (size_t col0 = seg_lo; col0 < seg_end; col0 += static_cast<size_t>(lanes) * kCols) {
         const Cols cols{col0 + static_cast<size_t>(place) * kCols, a.hidden};
         const bool in = cols.col < a.hidden;
         float acc[kCols] = {};
@@ -885,8 +889,10 @@ template <int DT, int W> cudaError_t few_dt(const EmbedArgs &a, cudaStream_t st)
 {
     const int clear = rows_to_clear(a.hidden);
     const size_t clear_ctas = a.accumulate ? 0 : (a.vocab + clear - 1) / clear;
-    return launch_kernel_block(embed_few_kernel<DT, W>, a.tokens + clear_ctas, kLanes, 0, st, a,
-                               clear);
+    const size_t seg = static_cast<size_t>(kLanes) * Fmt<DT>::kVec;
+    const unsigned segs = static_cast<unsigned>((a.hidden + seg - 1) / seg);
+    return launch_kernel_block(embed_few_kernel<DT, W>, a.tokens * segs + clear_ctas, kLanes, 0, st,
+                               a, segs, clear);
 }
 
 // The sort in one launch, and with it the first `cleared` rows of the table cleared
