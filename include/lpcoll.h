@@ -317,11 +317,12 @@ int dda_flat_sim_noalloc(const void *const *in, void *const *out, int nranks,
  *   - checks come in the order above; sizes are checked with the dtype
  *     (LPCOLL_ERR_ARG), and an array of no elements may be NULL;
  *   - any hidden size works; rows of a multiple of 16 bytes are the fast ones;
- *   - resources: CTAs of up to 1024 threads and, for residual_norm and its
- *     gradient, up to 224 KB of dynamic shared memory and clusters of up to 8
- *     CTAs, which wait for one another (and for nobody else). All copies have
- *     completed when a kernel does.
- * Limits: rows, slots < 2^31; ntokens * ceil(hidden / 256) < 2^30.
+ *   - resources: CTAs of up to 1024 threads and, for the norms, their gradients
+ *     and token_embed_backward, up to 224 KB of dynamic shared memory and, for
+ *     these and expert_balance, clusters of up to 8 CTAs, which wait for one
+ *     another (and for nobody else). All copies have completed when a kernel does.
+ * Limits: rows, slots < 2^31; ntokens * ceil(hidden / 256) < 2^30; hidden <= 2^30
+ * in token_embed, its gradient and residual_dropout without a norm.
  * ------------------------------------------------------------------------ */
 #define LPCOLL_MAX_EXPERTS 1024
 #define LPCOLL_MAX_TOPK 32
@@ -570,7 +571,8 @@ typedef enum { LPCOLL_I32 = 0, LPCOLL_I64 = 1 } lpcoll_index;
 /* Rows of a shard of a vocabulary: out[t] = scale * table[ids[t] - first_id], and
  * +0 where ids[t] is outside [first_id, first_id + vocab): the ids of other
  * shards (whose results an allreduce adds) and padding.
- *   table  [vocab][hidden] of dtype      out  [ntokens][hidden] of dtype
+ *   table  [vocab][hidden] of dtype
+ *   out    [ntokens][hidden] of dtype, not the table
  *   ids    [ntokens] of index's type     vocab < 2^31                       */
 int token_embed(const void *table, size_t vocab, const void *ids, lpcoll_index index,
                 int64_t first_id, size_t ntokens, size_t hidden, lpcoll_dtype dtype,

@@ -11,6 +11,8 @@ namespace lpc {
 namespace {
 
 constexpr size_t kMaxIndex = 0x7FFFFFFF;  // rows and slots are counted in int32
+// columns of calls that LPCOLL_MAX_HIDDEN does not limit: counted in int32 too
+constexpr size_t kMaxHidden = static_cast<size_t>(1) << 30;
 
 // A pointer to `count` elements; none are needed for an empty array.
 int check_array(const void *p, size_t count) { return count == 0 ? LPCOLL_OK : check_ptr(p); }
@@ -76,7 +78,7 @@ size_t layer_norm_workspace(size_t ntokens, size_t hidden, int dtype, bool dropo
 // Sizes of residual_dropout without a norm: CTAs along every token's row.
 int check_dropout(float p, size_t ntokens, size_t hidden, int dtype)
 {
-    if (bad_dtype(dtype) || !(p >= 0.0f && p < 1.0f))
+    if (bad_dtype(dtype) || !(p >= 0.0f && p < 1.0f) || hidden > kMaxHidden)
         return LPCOLL_ERR_ARG;
     return check_rows(ntokens, 1, 0, hidden, dtype);
 }
@@ -94,7 +96,7 @@ DropArgs drop_args(const uint64_t *rng, float p, size_t first_row)
 
 int check_embed(size_t ntokens, size_t vocab, size_t hidden, int dtype, int index)
 {
-    if (index != LPCOLL_I32 && index != LPCOLL_I64)
+    if ((index != LPCOLL_I32 && index != LPCOLL_I64) || hidden > kMaxHidden)
         return LPCOLL_ERR_ARG;
     return check_rows(ntokens, 1, vocab, hidden, dtype);
 }

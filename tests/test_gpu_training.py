@@ -128,6 +128,43 @@ def test_layer_norm(lib, dt, T, H, has_w, has_b):
     assert same(x, y)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H", [(700, 256), (307, 768), (1001, 512), (331, 8192), (40, 2048),
+                                 (459, 1280), (310, 6144), (170, 12288), (153, 16384)])
+def test_norms_of_rows_that_fill_their_teams(lib, dt, T, H):
+    # every form of the kernels for such rows: two at a time and a last one alone, teams
+    # that share a CTA, clusters, rows of 1024 threads
+    g = gen(T, H, 9)
+    x, dn, dxo = (dev(stream_like(g, T, H), dt) for _ in range(3))
+    w, b = dev(1 + 0.3 * g.normal(size=H), dt), dev(g.normal(size=H), dt)
+    out = Out()
+    y, dx, dh, xo, n = (out(T, H, dtype=DT[dt]) for _ in range(5))
+    dw, db = out(H), out(H)
+    pcr.layer_norm(x, y, w=w, b=b, eps=EPS)
+    within(y, ref.layer_norm(f64(x), f64(w), f64(b), EPS, dt), "out")
+    pcr.layer_norm_backward(dn, x, dx, w=w, eps=EPS, dw=dw, db=db)
+    want = ref.layer_norm_backward(f64(dn), f64(x), f64(w), EPS, dt)
+    for name, t in dict(dx=dx, dw=dw, db=db).items():
+        within(t, want[name], name)
+    p, rng = 0.3, words(T, H)
+    keep = ref.kept(T, H, T, H, p)
+    pcr.residual_dropout_backward(dxo, dn, x, dx, dh, rng, p, w=w, eps=EPS, dw=dw, db=db)
+    want = ref.layer_norm_backward(f64(dn), f64(x), f64(w), EPS, dt, f64(dxo),
+                                   keep / (1 - float(np.float32(p))))
+    for name, t in dict(dx=dx, dh=dh, dw=dw, db=db).items():
+        within(t, want[name], name)
+    for ranks in (1, 2, 16) if H <= 2048 else (1, 9):
+        hs = [dev(g.normal(size=(T, H)), dt) for _ in range(ranks)]
+        for res in (x, None):
+            pcr.residual_dropout(hs, res, xo, rng, p, n_out=n, w=w, b=b, eps=EPS)
+            want = ref.residual_dropout([f64(t) for t in hs], f64(res), keep, p, f64(w), f64(b),
+                                        EPS, dt, True)
+            within(xo, want[0], "x_out")
+            within(n, want[1], "n_out")
+    torch.cuda.synchronize()
+    assert out.intact()
+
+
 def test_layer_norm_of_rows_far_from_zero(lib):
     # values 1000 and one ulp's multiples: the squares about 0 would leave nothing
     g = gen(3)
@@ -603,3 +640,55 @@ def test_binding_refusals():
         pcr.token_embed(f, torch.zeros(3, dtype=torch.int64, device="cuda"), f)
     with pytest.raises(TypeError):
         pcr.token_embed_backward(f, torch.zeros(4, dtype=torch.int64, device="cuda"), b16)
+
+
+# -- calls at the same time -----------------------------------------------------
+
+def test_calls_of_two_threads_on_their_own_streams():
+    # each thread's results are those of the calls one after the other
+    import threading
+    T, H, V, E = 1500, 320, 700, 24
+
+    def inputs(i):
+        r = torch.Generator(device="cuda").manual_seed(i)
+        x, d = (torch.randn(T, H, device="cuda", generator=r) for _ in range(2))
+        return dict(x=x, d=d, ids=torch.randint(0, V, (T,), device="cuda", generator=r),
+                    z=torch.randn(T, E, device="cuda", generator=r),
+                    k=torch.randint(0, E, (T, 2), device="cuda", generator=r).int(),
+                    rng=words(i, 1))
+
+    def run(s):
+        o = [torch.empty(T, H, device="cuda") for _ in range(5)]
+        dw, db, dt_ = (torch.empty(H, device="cuda"), torch.empty(H, device="cuda"),
+                       torch.empty(V, H, device="cuda"))
+        loss, n, sums = (torch.empty(1, device="cuda"),
+                         torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+                         torch.empty(E, device="cuda"))
+        for _ in range(10):
+            pcr.residual_dropout(s["x"], s["d"], o[0], s["rng"], 0.2, n_out=o[1])
+            pcr.residual_dropout_backward(s["d"], s["x"], o[0], o[2], o[3], s["rng"], 0.2, dw=dw, db=db)
+            pcr.layer_norm_backward(o[2], o[0], o[4], dw=dw)
+            pcr.token_embed_backward(o[4], s["ids"], dt_)
+            pcr.expert_balance(s["z"], s["k"], loss, n, sums)
+        return [*o, dw, db, dt_, loss, n, sums]
+    sets = [inputs(i) for i in range(3)]
+    want = [run(s) for s in sets]
+    torch.cuda.synchronize()
+    got, errors = [None] * 3, []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                got[i] = run(sets[i])
+            stream.synchronize()
+        except Exception as e:  # reported by the main thread
+            errors.append(repr(e))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=120)
+    assert not errors, errors
+    for a, b in zip(got, want):
+        assert all(same(x, y) for x, y in zip(a, b))

@@ -59,6 +59,7 @@ def test_residual_dropout_refusals(L):
     assert f(dt=2) == ARG and f(n=0) == ARG and f(n=17) == ARG
     assert f(eps=0.0) == ARG and f(H=16385) == UNSUP
     assert f(T=1 << 31) == ARG and f(T=1 << 30, H=4096, no=None) == ARG
+    assert f(T=1, H=(1 << 30) + 1, no=None) == ARG
     assert f(T=0, h=None, rng=None, xo=None) == OK and f(H=0, h=None) == OK
     assert f(h=None) == ARG and f(h=B.ptr_array([A, None])) == RANK
     assert f(rng=None) == ARG and f(xo=None) == ARG
@@ -116,6 +117,7 @@ def test_embed_refusals(L):
         return L.token_embed(table, V, ids, index, first, T, H, dt, scale, out, None)
     assert f(dt=2) == ARG and f(index=2) == ARG and f(index=-1) == ARG
     assert f(T=1 << 31) == ARG and f(V=1 << 31) == ARG and f(T=1 << 30, H=4096) == ARG
+    assert f(T=1, H=(1 << 30) + 1) == ARG
     assert f(T=0, table=None, ids=None, out=None) == OK and f(H=0, table=None) == OK
     assert f(table=None) == ARG and f(ids=None) == ARG and f(out=None) == ARG
     for name in ("table", "ids", "out"):
