@@ -12,16 +12,17 @@ namespace {
 // can, each thread all of its own with their loads in flight together, and a warp adds
 // up a column's threads. Measured with the stores that leave the parts: 8192 columns of
 // 152 CTAs 14 us with 4-byte accesses and 1024 threads.
-constexpr int kSumThreads = 256;
+template <int kVec> constexpr int kSumThreads = kVec == 4 ? 256 : 1024;
 
 template <int kVec>
-__global__ void __launch_bounds__(kSumThreads)
+__global__ void __launch_bounds__(kSumThreads<kVec>)
 layer_norm_sums_kernel(const float *partial, float *dw, float *db, int hidden, int parts,
                        int column_ctas)
 {
     wait_prior_grid();
     constexpr int kAcross = 32 / kVec;                // threads of a part's 32 columns
-    constexpr int kDown = kSumThreads / kAcross;      // parts at once
+    constexpr int kDown = kSumThreads<kVec> / kAcross;  // parts at once
+    static_assert(kDown == 32, "a warp adds up a column");
     constexpr int kSteps = (kMaxCtas * kSms + kDown - 1) / kDown;
     __shared__ float red[kDown][33];
     const int which = blockIdx.x / column_ctas;
@@ -33,26 +34,25 @@ layer_norm_sums_kernel(const float *partial, float *dw, float *db, int hidden, i
     const int across = tid % kAcross, down = tid / kAcross;
     const int col = first + across * kVec;
     const float *const p = partial + static_cast<size_t>(which) * parts * hidden;
-    Vec<kVec> sum = {};
-#pragma unroll 8
+    Vec<kVec> v[kSteps], sum = {};
+#pragma unroll
     for (int i = 0; i < kSteps; ++i) {
         const int q = i * kDown + down;
+        v[i] = {};
         if (q < parts && col < hidden)
-            sum = plus(sum, load_vec_of<LPCOLL_F32, 4 * kVec>(p, static_cast<size_t>(q) * hidden + col));
+            v[i] = load_vec_of<LPCOLL_F32, 4 * kVec>(p, static_cast<size_t>(q) * hidden + col);
     }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+        sum = plus(sum, v[i]);
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
         red[down][across * kVec + j] = sum.v[j];
     __syncthreads();
-    for (int c = warp; c < 32; c += kSumThreads / 32) {
-        float v = 0.0f;
-#pragma unroll
-        for (int r = 0; r < kDown; r += 32)
-            if (kDown >= 32 || lane < kDown)
-                v += red[r + (kDown >= 32 ? lane : lane % kDown)][c];
-        v = warp_sum(v);
+    for (int c = warp; c < 32; c += kSumThreads<kVec> / 32) {
+        const float all = warp_sum(red[lane][c]);
         if (lane == 0 && first + c < hidden)
-            store_f32(out + first + c, v);
+            store_f32(out + first + c, all);
     }
 }
 
@@ -68,9 +68,11 @@ int layer_norm_parts(size_t tokens, size_t hidden, int dtype, bool dropout)
 cudaError_t launch_layer_norm_sums(const LayerNormArgs &a, int parts, cudaStream_t st)
 {
     const int ctas = (a.hidden + 31) / 32;
-    return launch_kernel_block(a.hidden % 4 == 0 ? layer_norm_sums_kernel<4> : layer_norm_sums_kernel<1>,
-                               static_cast<size_t>(2) * ctas, kSumThreads, 0, st, a.partial, a.dw,
-                               a.db, a.hidden, parts, ctas);
+    if (a.hidden % 4 == 0)
+        return launch_kernel_block(layer_norm_sums_kernel<4>, static_cast<size_t>(2) * ctas,
+                                   kSumThreads<4>, 0, st, a.partial, a.dw, a.db, a.hidden, parts, ctas);
+    return launch_kernel_block(layer_norm_sums_kernel<1>, static_cast<size_t>(2) * ctas,
+                               kSumThreads<1>, 0, st, a.partial, a.dw, a.db, a.hidden, parts, ctas);
 }
 
 cudaError_t launch_layer_norm(const LayerNormArgs &a, cudaStream_t st)
