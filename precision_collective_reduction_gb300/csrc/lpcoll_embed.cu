@@ -707,33 +707,28 @@ embed_join_kernel(const __grid_constant__ EmbedArgs a, const SumArgs s, const Ro
     if (next >= s.tokens || after != run || run == static_cast<int>(a.vocab) ||
         (start == run && before == run))
         return;  // ends with the tile, or began before it
-    // the last tile whose first key is the run's: some tiles on at a time
-    long long at = tile + 1;
-    for (bool more = true; more && at + 1 < s.tiles;) {
+    // the next tiles' partial rows together with their first keys, some at a time, up to
+    // the first key that is not the run's (what stands in that tile's row is not used)
+    float acc[kCols];
+    cols.load_f(s.tail, static_cast<size_t>(tile), acc);
+    bool more = true;
+    for (long long i = tile + 1; more && i < s.tiles; i += kAhead) {
+        float v[kAhead][kCols];
         int key[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            key[j] = key_at(s, (at + 1 + j) * s.tile);
+        for (int j = 0; j < kAhead; ++j) {
+            key[j] = key_at(s, (i + j) * s.tile);
+            if (i + j < s.tiles)
+                cols.load_f(s.head, static_cast<size_t>(i + j), v[j]);
+        }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             more = more && key[j] == run;
-            at += more ? 1 : 0;
-        }
-    }
-    float acc[kCols];
-    cols.load_f(s.tail, static_cast<size_t>(tile), acc);
-    for (long long i = tile + 1; i <= at; i += kAhead) {
-        float v[kAhead][kCols];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (i + j <= at)
-                cols.load_f(s.head, static_cast<size_t>(i + j), v[j]);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (i + j <= at)
+            if (more)
 #pragma unroll
                 for (int q = 0; q < kCols; ++q)
                     acc[q] += v[j][q];
+        }
     }
     cols.finish(a, static_cast<size_t>(run), acc);
 }
