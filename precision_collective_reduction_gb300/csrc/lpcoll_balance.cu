@@ -8,8 +8,14 @@
 // 8 to 32 lanes per token, at 8 experts a lane and more, add up its probabilities in
 // registers over their tokens. A CTA adds up its warps in order and leaves one row of sums and
 // counts; the rows meet in one cluster, which adds them in order, so the same call
-// gives the same bits. Few tokens take that cluster alone: its CTAs make the rows
-// too, with a cluster barrier in between.
+// gives the same bits. Few tokens take that cluster alone: its CTAs read one another's
+// rows from shared memory.
+//
+// Measured on one GB300, 32768 tokens of 256 FP32 logits (5.1 us of bytes): 14.6 us, some
+// 9 for the rows (57% issue active: exponentials and the two warp-wide steps of a softmax)
+// and 5 for the cluster (latency); the gradient 12.1 us (9.9). 512 tokens of 64 BF16: 5.8 us
+// in one launch (latency). Two CTAs of rows per SM 18.6 us, a warp per token for 64 experts
+// 12.8 instead of 9.1 (32768 tokens), the next tokens' logits ahead 15.5 (spills).
 #include "lpcoll_logits.cuh"
 
 namespace lpc {

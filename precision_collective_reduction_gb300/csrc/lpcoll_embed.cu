@@ -9,9 +9,17 @@
 // tokens), then goes through the sorted tokens in tiles: a run of equal rows that
 // lies in one tile is added up in registers and written once; runs over several
 // tiles leave one partial row per tile in the workspace, which a last launch adds
-// in order. So frequent tokens are shared out over many CTAs without atomics, and
-// the same call gives the same bits. Rows of the table without a token are
-// cleared by CTAs of the same launch.
+// in order. So frequent tokens are shared out over many CTAs without atomics on
+// floating-point values, and the same call gives the same bits. Rows of the table
+// without a token are cleared by other CTAs of the sort's and the sums' launches, which
+// keep DRAM busy while those wait for memory.
+//
+// Measured on one GB300 (bytes at the copy rate in brackets): the rows of 16384 tokens of
+// 8192 BF16 from one of four shards 49 us (46), from a whole table 70; in one piece of 16
+// bytes a lane and CTAs of 4 KB 76. The gradient of 16384 tokens into 32000 x 8192: 226 us
+// (194), of them the sort 14-20, which clears 144 MB meanwhile, the sums 195, the last launch
+// 6; with a sort of four launches, the clearing behind the sums and 4 rows in flight a lane
+// 295. 777 tokens into 4001 x 1025 FP32: 13 us (2.5), the latencies of three launches.
 #include "lpcoll_layers.cuh"
 
 namespace lpc {

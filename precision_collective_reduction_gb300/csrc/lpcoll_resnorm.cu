@@ -26,8 +26,8 @@
 // (bytes at the copy rate: 238 and 119).
 //
 // Measured on one GB300, BF16: 16384 x 8192 forward 161 us (6.7 TB/s, DRAM), the
-// gradient of 8192 x 8192 131 us (6.1 TB/s; a team's phases between barriers), 32
-// x 8192 of 8 ranks 5.9 us (latency).
+// gradient of 8192 x 8192 124 us (6.5 TB/s; a team's phases between barriers), 32
+// x 8192 of 8 ranks 5.7 us (latency).
 #include "lpcoll_rows.cuh"
 
 namespace lpc {
