@@ -29,7 +29,8 @@ SOURCES = ["lpcoll_api.cu", "lpcoll_codec.cu", "lpcoll_dda_f32.cu",
            "lpcoll_gather.cu", "lpcoll_variants.cu", "lpcoll_host.cu",
            "lpcoll_noalloc.cu", "lpcoll_layers_api.cu", "lpcoll_route.cu",
            "lpcoll_experts.cu", "lpcoll_resnorm.cu", "lpcoll_layernorm.cu",
-           "lpcoll_dropnorm.cu", "lpcoll_dropout.cu", "lpcoll_balance.cu", "lpcoll_embed.cu"]
+           "lpcoll_dropnorm.cu", "lpcoll_dropnorm_backward.cu", "lpcoll_dropout.cu",
+           "lpcoll_balance.cu", "lpcoll_embed.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -fmad=false / -prec-div=true / -ftz=false back up the explicit __f*_rn
 # intrinsics: every float operation of the kernels is one IEEE operation.

@@ -1,6 +1,6 @@
 // lpcoll_layernorm.cuh -- kernels of layer_norm and of residual_dropout with its
-// norm, and of their gradients, compiled in lpcoll_layernorm.cu and
-// lpcoll_dropnorm.cu.
+// norm, and of their gradients, compiled in lpcoll_layernorm.cu,
+// lpcoll_dropnorm.cu and lpcoll_dropnorm_backward.cu.
 //
 //   x' = x                                         (layer_norm)
 //   x' = x + d(sum_r h_r),  d(h) = kept ? h / (1 - p) : 0   (residual_dropout)
@@ -314,6 +314,33 @@ constexpr int kTeamThreads = 512;  // most threads of a CTA but kWide's
 // Forms of the kernels beside rows.cuh's: kEven has all its columns as kPlain has,
 // but any number of ranks, and the residual or not.
 constexpr int kEven = kWide + 1;
+// kRagged: rows of any length in teams without a cluster. All warps but a team's last have
+// all their columns; the steps that go through the columns exist with and without the
+// question, and a warp takes its own.
+constexpr int kRagged = kEven + 1;
+
+struct Full {
+    static constexpr bool kAll = true;
+};
+struct Partial {
+    static constexpr bool kAll = false;
+};
+
+// step(Full) where the warp has all of its columns, else step(Partial).
+template <int kMode, class Step>
+__device__ __forceinline__ void for_columns(bool full, const Step &step)
+{
+    if constexpr (kMode == kPlain || kMode == kEven) {
+        step(Full{});
+    } else if constexpr (kMode == kRagged) {
+        if (full)
+            step(Full{});
+        else
+            step(Partial{});
+    } else {
+        step(Partial{});
+    }
+}
 
 // A team takes R rows at a time: with two, the steps of one fill the waits of the
 // other, and one barrier serves both. Streams of a row: x if there is one, then the
@@ -326,9 +353,10 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int 
     extern __shared__ uint4 ring_smem[];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    constexpr bool kAlone = kMode == kPlain || kMode == kEven;
+    constexpr bool kAlone = kMode == kPlain || kMode == kEven || kMode == kRagged;
+    constexpr int kHas = kMode == kPlain || kMode == kEven ? kPlain : (kMode == kWide ? kWide : kGeneral);
     __shared__ float2 red[2][R][kMaxWarps];
-    const Member<DT, W, kElems, kAlone ? kPlain : kMode, kAlone> me(deal, a, streams * R, reinterpret_cast<char *>(ring_smem));
+    const Member<DT, W, kElems, kHas, kAlone> me(deal, a, streams * R, reinterpret_cast<char *>(ring_smem));
     const Shares<NV, kN, kAlone> share(deal, a.hidden, me.first_warp);
     const bool given = kMode == kPlain || !kDrop || a.x != nullptr;
     const int h0 = given ? 1 : 0, nranks = !kDrop ? 0 : (kMode == kPlain ? 1 : a.nranks);
@@ -336,6 +364,7 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int 
     const Philox rnd(a.drop, a.hidden);
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
     const int lane = threadIdx.x & 31, warps = deal.threads >> 5;
+    const bool full = __all_sync(kAll, me.has(NV - 1));
     const auto fetch = [&](size_t t, int stage) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -373,50 +402,54 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int 
         me.ready(deal.stages - 1);
         Vec<kN> v[R][NV];
         float sum[R], sq[R];
+        for_columns<kMode>(full, [&](auto all) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const size_t row = t + i * me.step;
-            Keep<kElems, kN> keep;
-            if (drop)
-                keep.make(rnd, me, row);
-            Acc<kN> total = {};
+            for (int i = 0; i < R; ++i) {
+                const size_t row = t + i * me.step;
+                Keep<kElems, kN> keep;
+                if (drop)
+                    keep.make(rnd, me, row);
+                Acc<kN> total = {};
 #pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                if (!me.has(c))
-                    continue;
-                if constexpr (kDrop) {
-                    Vec<kN> h = me.read(row, stage, i * streams + h0, c);
+                for (int c = 0; c < NV; ++c) {
+                    if (!decltype(all)::kAll && !me.has(c))
+                        continue;
+                    if constexpr (kDrop) {
+                        Vec<kN> h = me.read(row, stage, i * streams + h0, c);
 #pragma unroll 4
-                    for (int r = 1; r < nranks; ++r)
-                        h = plus(h, me.read(row, stage, i * streams + h0 + r, c));
-                    if (drop)
-                        h = keep.apply(rnd, me, h, a.drop.scale, c);
-                    v[i][c] = given ? plus(me.read(row, stage, i * streams, c), h) : h;
-                    if (R == 1 || row < a.tokens)
-                        store_vec_of<DT, W>(a.x_out, me.elem(row, c), v[i][c]);
-                } else {
-                    v[i][c] = me.read(row, stage, i, c);
+                        for (int r = 1; r < nranks; ++r)
+                            h = plus(h, me.read(row, stage, i * streams + h0 + r, c));
+                        if (drop)
+                            h = keep.apply(rnd, me, h, a.drop.scale, c);
+                        v[i][c] = given ? plus(me.read(row, stage, i * streams, c), h) : h;
+                        if (R == 1 || row < a.tokens)
+                            store_vec_of<DT, W>(a.x_out, me.elem(row, c), v[i][c]);
+                    } else {
+                        v[i][c] = me.read(row, stage, i, c);
+                    }
+                    add_values<kN>(total, v[i][c]);
                 }
-                add_values<kN>(total, v[i][c]);
+                sum[i] = fold(total);
             }
-            sum[i] = fold(total);
-        }
+        });
         fetch(t + deal.stages * R * me.step, stage);
         stage = stage + 1 == deal.stages ? 0 : stage + 1;
         warp_sums(sum);
+        for_columns<kMode>(full, [&](auto all) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const Vec<kN> about = splat<kN>(-(sum[i] * share.inv_own));
-            Acc<kN> squares = {};
+            for (int i = 0; i < R; ++i) {
+                const Vec<kN> about = splat<kN>(-(sum[i] * share.inv_own));
+                Acc<kN> squares = {};
 #pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                if (!me.has(c))
-                    continue;
-                const Vec<kN> d = plus(v[i][c], about);
-                add_products(squares, d, d);
+                for (int c = 0; c < NV; ++c) {
+                    if (!decltype(all)::kAll && !me.has(c))
+                        continue;
+                    const Vec<kN> d = plus(v[i][c], about);
+                    add_products(squares, d, d);
+                }
+                sq[i] = fold(squares);
             }
-            sq[i] = fold(squares);
-        }
+        });
         warp_sums(sq);
         float mean[R], m2[R];
         if constexpr (kAlone) {
@@ -451,27 +484,29 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int 
             team_moments(sum[0], sq[0], share, red[turn][0], deal, me.first_warp, a.hidden,
                          per_hidden, deal.cluster == 1, mean[0], m2[0]);
         }
+        for_columns<kMode>(full, [&](auto all) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const size_t row = t + i * me.step;
-            if (R > 1 && row >= a.tokens)
-                break;
-            const float r = inv_rms(m2[i], per_hidden, a.eps);
-            const Vec<kN> centre = splat<kN>(-mean[i]);
+            for (int i = 0; i < R; ++i) {
+                const size_t row = t + i * me.step;
+                if (R > 1 && row >= a.tokens)
+                    break;
+                const float r = inv_rms(m2[i], per_hidden, a.eps);
+                const Vec<kN> centre = splat<kN>(-mean[i]);
 #pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                if (!me.has(c))
-                    continue;
-                const Vec<kN> n = mul(r, plus(v[i][c], centre));
-                if constexpr (kMode == kWide) {
-                    weights(c);
-                    store_vec_of<DT, W>(a.n_out, me.elem(row, c),
-                                        fma(n, unpack<DT, W>(w[c]), unpack<DT, W>(b[c])));
-                } else {
-                    store_vec_of<DT, W>(a.n_out, me.elem(row, c), fma(n, wide_w[c], wide_b[c]));
+                for (int c = 0; c < NV; ++c) {
+                    if (!decltype(all)::kAll && !me.has(c))
+                        continue;
+                    const Vec<kN> n = mul(r, plus(v[i][c], centre));
+                    if constexpr (kMode == kWide) {
+                        weights(c);
+                        store_vec_of<DT, W>(a.n_out, me.elem(row, c),
+                                            fma(n, unpack<DT, W>(w[c]), unpack<DT, W>(b[c])));
+                    } else {
+                        store_vec_of<DT, W>(a.n_out, me.elem(row, c), fma(n, wide_w[c], wide_b[c]));
+                    }
                 }
             }
-        }
+        });
     }
     copy_wait(0);
     if (!kAlone && deal.cluster > 1)
@@ -506,23 +541,16 @@ __device__ __forceinline__ RowSums spread(float mean, float mine)
 }
 
 template <class S>
-__device__ __forceinline__ RowSums team_grad_sums(float mine, float sum, const S &share,
-                                                  float4 *red, const Deal &deal, int first_warp,
-                                                  int hidden, float per_hidden, bool alone)
+__device__ __forceinline__ RowSums cluster_grad_sums(float mine, float sum, const S &share,
+                                                     float4 *red, const Deal &deal, int hidden,
+                                                     float per_hidden)
 {
     const int lane = threadIdx.x & 31, warps = deal.threads >> 5;
-    if (warps == 1 && alone)
-        return spread(sum * share.inv_own, mine);
     if (lane < 4)
         reinterpret_cast<float *>(red + (threadIdx.x >> 5))[lane] = lane == kSumOfX ? sum : mine;
     __syncwarp();
-    team_barrier(deal);
+    cluster_barrier();
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (alone) {
-        const float4 v = lane < warps ? red[first_warp + lane] : zero;
-        const float mean = warp_sum(v.w) * per_hidden;
-        return spread(mean, split_sum(moved(v, share, mean)));
-    }
     float4 v[kMaxCluster];
     float all = 0.0f;
 #pragma unroll
@@ -547,6 +575,7 @@ __device__ __forceinline__ RowSums team_grad_sums(float mine, float sum, const S
     return spread(mean, split_sum(s));
 }
 
+// The gradient of rows over a cluster of CTAs.
 template <int DT, int W, int kElems, bool kDrop>
 __global__ void __launch_bounds__(kTeamThreads, 1)
 layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int streams)
@@ -604,9 +633,8 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
             add_products(sa, q, d);
             add_values<kN>(sqs, q);
         }
-        const RowSums s = team_grad_sums(split_sum({{fold(sq), fold(sa), fold(sqs)}}), sum, share,
-                                         red[turn], deal, me.first_warp, a.hidden, per_hidden,
-                                         deal.cluster == 1);
+        const RowSums s = cluster_grad_sums(split_sum({{fold(sq), fold(sa), fold(sqs)}}), sum, share,
+                                            red[turn], deal, a.hidden, per_hidden);
         Keep<kElems, kN> keep;
         if (drop)
             keep.make(rnd, me, t);
@@ -633,39 +661,50 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
         stage = stage + 1 == deal.stages ? 0 : stage + 1;
     }
     copy_wait(0);
-    if (deal.cluster > 1)
-        cluster_barrier();  // no CTA leaves while another reads its sums
+    cluster_barrier();  // no CTA leaves while another reads its sums
     if (a.partial != nullptr)
         leave_sums<DT, W>(me, deal, s_w, s_b, a.partial, reinterpret_cast<float *>(ring_smem));
 }
 
-// The gradient of rows that fill their teams (no clusters, every thread has all its
-// columns, nothing left out). A turn of a team joins the sums of its row t, makes
+// The gradient without clusters (kPlain: every thread has all its columns, and nothing is
+// left out; kRagged). A turn of a team joins the sums of its row t, makes
 // those of its next row, which depend on nothing of row t, and writes row t: so the
 // steps of the one fill the waits of the other. With no next row the stage's old
 // values are summed and not used. (One warp more that joins the sums for all, with
 // the sums of a row handed over in shared memory, left 96 registers a thread and was
 // slower: 8192 x 8192 BF16 95 us, 216 with dropout.)
-template <int DT, int W, int kElems, bool kDrop>
+template <int DT, int W, int kElems, int kMode, bool kDrop>
 __global__ void __launch_bounds__(kTeamThreads, 1)
-layer_norm_backward_even_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int streams)
+layer_norm_backward_team_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int streams)
 {
     wait_prior_grid();
     extern __shared__ uint4 ring_smem[];
     __shared__ float4 red[2][kMaxWarps];
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
-    const Member<DT, W, kElems, kPlain, true> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
+    constexpr int kHas = kMode == kRagged ? kGeneral : kPlain;
+    const Member<DT, W, kElems, kHas, true> me(deal, a, streams, reinterpret_cast<char *>(ring_smem));
     const Shares<NV, kN, true> share(deal, a.hidden, me.first_warp);
-    const bool drop = kDrop && a.drop.least != 0;
+    const bool given = kDrop && (kMode == kPlain || a.dx_out != nullptr);
+    const bool want_dx = kMode == kPlain || a.dx != nullptr;
+    const bool want_dh = kDrop && (kMode == kPlain || a.dh != nullptr);
+    const bool drop = want_dh && a.drop.least != 0;
     const Philox rnd(a.drop, a.hidden);
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
     const int lane = threadIdx.x & 31, warps = deal.threads >> 5;
+    const bool full = __all_sync(kAll, me.has(NV - 1));
+    // columns of this thread
+    int own = 0;
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+        own += me.has(c) ? kN : 0;
+    const float n = kMode == kPlain ? static_cast<float>(kElems) : static_cast<float>(own);
+    const float inv_n = kMode == kPlain ? 1.0f / kElems : share.inverse(n);
     const auto fetch = [&](size_t t, int stage) {
         if (t < a.tokens) {
             me.copy(stage, kGradX, a.x, t);
             me.copy(stage, kGradDn, a.dn_out, t);
-            if (kDrop)
+            if (given)
                 me.copy(stage, kGradDx, a.dx_out, t);
         }
         copy_commit();
@@ -677,7 +716,7 @@ layer_norm_backward_even_kernel(const __grid_constant__ LayerNormArgs a, const D
     Vec<kN> s_w[NV], s_b[NV];
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-        w[c] = a.w != nullptr ? load_pack<DT, W>(a.w, me.col(c)) : all_of<DT, W>(1.0f);
+        w[c] = a.w != nullptr && me.has(c) ? load_pack<DT, W>(a.w, me.col(c)) : all_of<DT, W>(1.0f);
         s_w[c] = s_b[c] = splat<kN>(0.0f);
     }
 
@@ -692,26 +731,29 @@ layer_norm_backward_even_kernel(const __grid_constant__ LayerNormArgs a, const D
     const auto add_up = [&](size_t t, int stage) {
         Acc<kN> total = {}, sq = {}, sa = {}, sqs = {};
         float x0 = 0.0f;
+        for_columns<kMode>(full, [&](auto all) {
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            const Vec<kN> x = me.read(t, stage, kGradX, c);
-            if (c == 0)
-                x0 = x.v[0];
-            const Vec<kN> d = plus(x, splat<kN>(-x0));
-            const Vec<kN> q = mul(me.read(t, stage, kGradDn, c), unpack<DT, W>(w[c]));
-            add_values<kN>(total, d);
-            add_products(sq, d, d);
-            add_products(sa, q, d);
-            add_values<kN>(sqs, q);
-        }
-        const float sum = fold(total), m = sum * (1.0f / kElems), qs = fold(sqs);
-        return Part{fmaf(static_cast<float>(kElems), x0, sum), x0 + m, fmaf(-m, sum, fold(sq)),
-                    fmaf(-m, qs, fold(sa)), qs};
+            for (int c = 0; c < NV; ++c) {
+                if (!decltype(all)::kAll && !me.has(c))
+                    continue;
+                const Vec<kN> x = me.read(t, stage, kGradX, c);
+                if (c == 0)
+                    x0 = x.v[0];
+                const Vec<kN> d = plus(x, splat<kN>(-x0));
+                const Vec<kN> q = mul(me.read(t, stage, kGradDn, c), unpack<DT, W>(w[c]));
+                add_values<kN>(total, d);
+                add_products(sq, d, d);
+                add_products(sa, q, d);
+                add_values<kN>(sqs, q);
+            }
+        });
+        const float sum = fold(total), m = sum * inv_n, qs = fold(sqs);
+        return Part{fmaf(n, x0, sum), x0 + m, fmaf(-m, sum, fold(sq)), fmaf(-m, qs, fold(sa)), qs};
     };
     // The same about the warp's mean.
     const auto about_warp = [&](const Part &p, float warp_mean) {
         const float d = p.mean - warp_mean;
-        return Three{{fmaf(kElems * d, d, p.m2), fmaf(d, p.q, p.a), p.q}};
+        return Three{{fmaf(n * d, d, p.m2), fmaf(d, p.q, p.a), p.q}};
     };
 
     int stage = 0, turn = 0;
@@ -753,21 +795,26 @@ layer_norm_backward_even_kernel(const __grid_constant__ LayerNormArgs a, const D
         const float c1 = s.q * per_hidden, c2 = r * r * (s.a * per_hidden);
         const Vec<kN> shift = splat<kN>(-r * s.mean);
         const Vec<kN> constant = splat<kN>(r * fmaf(c2, s.mean, -c1));
+        for_columns<kMode>(full, [&](auto all) {
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            const Vec<kN> x = me.read(t, stage, kGradX, c);
-            const Vec<kN> dn = me.read(t, stage, kGradDn, c);
-            s_w[c] = fma(fma(r, x, shift), dn, s_w[c]);
-            s_b[c] = plus(s_b[c], dn);
-            Vec<kN> q = constant;
-            if (kDrop)
-                q = plus(q, me.read(t, stage, kGradDx, c));
-            q = fma(r, mul(dn, unpack<DT, W>(w[c])), fma(-(r * c2), x, q));
-            store_vec_of<DT, W>(a.dx, me.elem(t, c), q);
-            if (kDrop)
-                store_vec_of<DT, W>(a.dh, me.elem(t, c),
-                                    drop ? keep.apply(rnd, me, q, a.drop.scale, c) : q);
-        }
+            for (int c = 0; c < NV; ++c) {
+                if (!decltype(all)::kAll && !me.has(c))
+                    continue;
+                const Vec<kN> x = me.read(t, stage, kGradX, c);
+                const Vec<kN> dn = me.read(t, stage, kGradDn, c);
+                s_w[c] = fma(fma(r, x, shift), dn, s_w[c]);
+                s_b[c] = plus(s_b[c], dn);
+                Vec<kN> q = constant;
+                if (given)
+                    q = plus(q, me.read(t, stage, kGradDx, c));
+                q = fma(r, mul(dn, unpack<DT, W>(w[c])), fma(-(r * c2), x, q));
+                if (want_dx)
+                    store_vec_of<DT, W>(a.dx, me.elem(t, c), q);
+                if (want_dh)
+                    store_vec_of<DT, W>(a.dh, me.elem(t, c),
+                                        drop ? keep.apply(rnd, me, q, a.drop.scale, c) : q);
+            }
+        });
         fetch(t + deal.stages * me.step, stage);
         stage = after;
     }
@@ -789,9 +836,11 @@ inline int group_packs(int hidden, int dtype)
 template <int DT, bool kDrop> constexpr int kShortRows = DT == LPCOLL_BF16 && !kDrop ? 4 : 2;
 
 // Rows that fill their teams may be taken several at a time, `short_rows` where a thread
-// has 8 columns.
+// has 8 columns; with `ragged` others two at a time (layer_norm of 4096 x 4097 BF16 40 ->
+// 32 us; with dropout, whose ranks and words leave no registers for a second row, one at
+// a time is faster: 4 ranks of 4096 x 4100 72 us, 84 with two).
 Plan layer_norm_plan(size_t tokens, int hidden, int dtype, int streams, bool gradient,
-                     int short_rows = 1)
+                     int short_rows = 1, bool ragged = false)
 {
     const int width = row_width(hidden, dtype);
     const int kn = width / static_cast<int>(dtype_bytes(dtype));
@@ -817,11 +866,15 @@ Plan layer_norm_plan(size_t tokens, int hidden, int dtype, int streams, bool gra
     if (gradient) {
         room.least = 2;
     } else if (!p.wide && cluster == 1 && tokens > kSms) {
-        Room pair = room;
-        pair.rows = p.elems == 8 ? short_rows : 2;
-        const Plan two = deal_rows(p, cluster, tokens, hidden, dtype, streams, false, pair);
-        if (two.even && two.smem <= kSmemOne)
-            return two;
+        Room some = room;
+        some.rows = p.elems == 8 ? short_rows : 2;
+        Plan several = deal_rows(p, cluster, tokens, hidden, dtype, streams, false, some);
+        if (!several.even && some.rows != 2) {
+            some.rows = 2;
+            several = deal_rows(p, cluster, tokens, hidden, dtype, streams, false, some);
+        }
+        if ((several.even || ragged) && several.smem <= kSmemOne)
+            return several;
     }
     return deal_rows(p, cluster, tokens, hidden, dtype, streams, gradient, room);
 }
@@ -831,7 +884,7 @@ cudaError_t layer_norm_dt(const LayerNormArgs &a, cudaStream_t st)
 {
     const int streams = a.nranks + (a.x != nullptr ? 1 : 0);
     constexpr int kShort = kShortRows<DT, kDrop>;
-    const Plan p = layer_norm_plan(a.tokens, a.hidden, a.dtype, streams, false, kShort);
+    const Plan p = layer_norm_plan(a.tokens, a.hidden, a.dtype, streams, false, kShort, !kDrop);
     if constexpr (W == 16) {
         if (p.wide)
             return launch_plan(layer_norm_kernel<DT, W, 16, kWide, kDrop, 1>, a, p, streams, st);
@@ -854,6 +907,12 @@ cudaError_t layer_norm_dt(const LayerNormArgs &a, cudaStream_t st)
             }
         }
     }
+    if constexpr (!kDrop) {
+        if (p.rows == 2)
+            return launch_plan(p.elems == 8 ? layer_norm_kernel<DT, W, 8, kRagged, false, 2>
+                                            : layer_norm_kernel<DT, W, 16, kRagged, false, 2>,
+                               a, p, streams, st);
+    }
     return launch_plan(p.elems == 8 ? layer_norm_kernel<DT, W, 8, kGeneral, kDrop, 1>
                                     : layer_norm_kernel<DT, W, 16, kGeneral, kDrop, 1>,
                        a, p, streams, st);
@@ -870,15 +929,18 @@ template <int DT, int W, bool kDrop>
 cudaError_t layer_norm_backward_dt(const LayerNormArgs &a, const Plan &p, cudaStream_t st)
 {
     const int streams = kDrop ? 3 : 2;
+    if (p.deal.cluster > 1)
+        return launch_plan(p.elems == 8 ? layer_norm_backward_kernel<DT, W, 8, kDrop>
+                                        : layer_norm_backward_kernel<DT, W, 16, kDrop>,
+                           a, p, streams, st);
     if constexpr (W == 16) {
-        if (p.even && p.deal.cluster == 1 && a.dx != nullptr &&
-            (!kDrop || (a.dx_out != nullptr && a.dh != nullptr)))
-            return launch_plan(p.elems == 8 ? layer_norm_backward_even_kernel<DT, W, 8, kDrop>
-                                            : layer_norm_backward_even_kernel<DT, W, 16, kDrop>,
+        if (p.even && a.dx != nullptr && (!kDrop || (a.dx_out != nullptr && a.dh != nullptr)))
+            return launch_plan(p.elems == 8 ? layer_norm_backward_team_kernel<DT, W, 8, kPlain, kDrop>
+                                            : layer_norm_backward_team_kernel<DT, W, 16, kPlain, kDrop>,
                                a, p, streams, st);
     }
-    return launch_plan(p.elems == 8 ? layer_norm_backward_kernel<DT, W, 8, kDrop>
-                                    : layer_norm_backward_kernel<DT, W, 16, kDrop>,
+    return launch_plan(p.elems == 8 ? layer_norm_backward_team_kernel<DT, W, 8, kRagged, kDrop>
+                                    : layer_norm_backward_team_kernel<DT, W, 16, kRagged, kDrop>,
                        a, p, streams, st);
 }
 
