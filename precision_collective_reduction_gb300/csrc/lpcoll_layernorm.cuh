@@ -309,11 +309,11 @@ template <int DT, int W> __device__ __forceinline__ typename Pack<DT, W>::Raw al
     return narrow_pack<DT, W>(x);
 }
 
-constexpr int kTeamThreads = 512;  // most threads of a CTA but kWide's
+constexpr int kTeamThreads = 512;  // most threads of a CTA
 
 // Forms of the kernels beside rows.cuh's: kEven has all its columns as kPlain has,
 // but any number of ranks, and the residual or not.
-constexpr int kEven = kWide + 1;
+constexpr int kEven = kWide + 1;  // (kWide is residual_norm's)
 // kRagged: rows of any length in teams without a cluster. All warps but a team's last have
 // all their columns; the steps that go through the columns exist with and without the
 // question, and a warp takes its own.
@@ -346,7 +346,7 @@ __device__ __forceinline__ void for_columns(bool full, const Step &step)
 // other, and one barrier serves both. Streams of a row: x if there is one, then the
 // ranks' h.
 template <int DT, int W, int kElems, int kMode, bool kDrop, int R>
-__global__ void __launch_bounds__(kMode == kWide ? kWideThreads : kTeamThreads, 1)
+__global__ void __launch_bounds__(kTeamThreads, 1)
 layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int streams)
 {
     wait_prior_grid();
@@ -354,7 +354,7 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int 
     constexpr int kN = Pack<DT, W>::kN;
     constexpr int NV = kElems / kN;
     constexpr bool kAlone = kMode == kPlain || kMode == kEven || kMode == kRagged;
-    constexpr int kHas = kMode == kPlain || kMode == kEven ? kPlain : (kMode == kWide ? kWide : kGeneral);
+    constexpr int kHas = kMode == kPlain || kMode == kEven ? kPlain : kGeneral;
     __shared__ float2 red[2][R][kMaxWarps];
     const Member<DT, W, kElems, kHas, kAlone> me(deal, a, streams * R, reinterpret_cast<char *>(ring_smem));
     const Shares<NV, kN, kAlone> share(deal, a.hidden, me.first_warp);
@@ -381,20 +381,11 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int 
     for (int s = 0; s < deal.stages; ++s)
         fetch(me.t0 + s * R * me.step, s);
 
-    // In FP32 where they stay in registers for many rows.
-    typename Pack<DT, W>::Raw w[NV], b[NV];
-    Vec<kN> wide_w[NV], wide_b[NV];
-    const auto weights = [&](int c) {
-        w[c] = a.w != nullptr && me.has(c) ? load_pack<DT, W>(a.w, me.col(c)) : all_of<DT, W>(1.0f);
-        b[c] = a.b != nullptr && me.has(c) ? load_pack<DT, W>(a.b, me.col(c)) : all_of<DT, W>(0.0f);
-    };
-    if constexpr (kMode != kWide) {
+    Vec<kN> w[NV], b[NV];
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            weights(c);
-            wide_w[c] = unpack<DT, W>(w[c]);
-            wide_b[c] = unpack<DT, W>(b[c]);
-        }
+    for (int c = 0; c < NV; ++c) {
+        w[c] = a.w != nullptr && me.has(c) ? load_vec_of<DT, W>(a.w, me.col(c)) : splat<kN>(1.0f);
+        b[c] = a.b != nullptr && me.has(c) ? load_vec_of<DT, W>(a.b, me.col(c)) : splat<kN>(0.0f);
     }
 
     int stage = 0, turn = 0;
@@ -497,13 +488,7 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int 
                     if (!decltype(all)::kAll && !me.has(c))
                         continue;
                     const Vec<kN> n = mul(r, plus(v[i][c], centre));
-                    if constexpr (kMode == kWide) {
-                        weights(c);
-                        store_vec_of<DT, W>(a.n_out, me.elem(row, c),
-                                            fma(n, unpack<DT, W>(w[c]), unpack<DT, W>(b[c])));
-                    } else {
-                        store_vec_of<DT, W>(a.n_out, me.elem(row, c), fma(n, wide_w[c], wide_b[c]));
-                    }
+                    store_vec_of<DT, W>(a.n_out, me.elem(row, c), fma(n, w[c], b[c]));
                 }
             }
         });
@@ -844,35 +829,34 @@ Plan layer_norm_plan(size_t tokens, int hidden, int dtype, int streams, bool gra
 {
     const int width = row_width(hidden, dtype);
     const int kn = width / static_cast<int>(dtype_bytes(dtype));
-    constexpr int kRow = 16 * kTeamThreads;  // columns of the largest CTA but kWide's
+    constexpr int kRow = 16 * kTeamThreads;
     Plan p;
-    p.wide = !gradient && tokens > kSms && hidden > kRow && width == 16 &&
-             static_cast<size_t>(hidden) * width / kn * streams <= kSmemOne;
-    int cluster = hidden > kRow && !p.wide ? 2 : 1;
+    p.wide = false;
+    // rows above 8192 columns in one CTA all the same, at 24 or 32 columns a thread, if
+    // their copies fit (2048 x 12288 BF16, norm, with dropout, and their gradients: 19, 50,
+    // 39 and 75 us; in a CTA of 1024 threads that reads its weights for every row 26 and 62,
+    // over a cluster of two 82 and 110)
+    const int least = gradient ? 2 : 1;
+    const bool longer = hidden > kRow && tokens > kSms && width == 16 &&
+                        least * streams * static_cast<size_t>(hidden) * dtype_bytes(dtype) <= kSmemOne;
+    int cluster = hidden > kRow && !longer ? 2 : 1;
     // few tokens: a row over up to 8 CTAs, while there are SMs left and a CTA
     // keeps two warps
     while (cluster < kMaxCluster && tokens * cluster * 2 <= kSms && hidden >= 512 * cluster * 2)
         cluster *= 2;
     // many ranks: until a row of all streams fits the shared memory
-    while (!p.wide && cluster < kMaxCluster &&
+    while (!longer && cluster < kMaxCluster &&
            (static_cast<size_t>(hidden) * width / kn / cluster + 2048) * streams > kSmemOne)
         cluster *= 2;
-    p.elems = !p.wide && (hidden <= 256 || (tokens <= kSms && hidden <= kRow / 2 * cluster)) ? 8 : 16;
+    p.elems = hidden <= 256 || (tokens <= kSms && hidden <= kRow / 2 * cluster) ? 8 : 16;
+    if (longer)
+        p.elems = hidden <= 24 * kTeamThreads ? 24 : 32;
     // 8 columns a thread also where they fill the threads and 16 do not
-    if (!p.wide && cluster == 1 && width == 16 && hidden <= kRow / 2 && hidden % 512 != 0 &&
-        hidden % 256 == 0)
+    if (cluster == 1 && width == 16 && hidden <= kRow / 2 && hidden % 512 != 0 && hidden % 256 == 0)
         p.elems = 8;
-    Room room{p.wide ? kWideThreads : kTeamThreads, group_packs(hidden, dtype)};
-    if (gradient) {
-        room.least = 2;
-        // rows above 8192 columns in one CTA all the same, at 24 or 32 columns a thread
-        // (2048 x 12288 BF16: 39 us, 82 with a cluster of two; with dropout 75, 110)
-        if (hidden > kRow && tokens > kSms && width == 16 &&
-            2 * streams * static_cast<size_t>(hidden) * dtype_bytes(dtype) <= kSmemOne) {
-            cluster = 1;
-            p.elems = hidden <= 24 * kTeamThreads ? 24 : 32;
-        }
-    } else if (!p.wide && cluster == 1 && tokens > kSms) {
+    Room room{kTeamThreads, group_packs(hidden, dtype)};
+    room.least = least;
+    if (!gradient && cluster == 1 && tokens > kSms && !longer) {
         Room some = room;
         some.rows = p.elems == 8 ? short_rows : 2;
         Plan several = deal_rows(p, cluster, tokens, hidden, dtype, streams, false, some);
@@ -893,8 +877,10 @@ cudaError_t layer_norm_dt(const LayerNormArgs &a, cudaStream_t st)
     constexpr int kShort = kShortRows<DT, kDrop>;
     const Plan p = layer_norm_plan(a.tokens, a.hidden, a.dtype, streams, false, kShort, !kDrop);
     if constexpr (W == 16) {
-        if (p.wide)
-            return launch_plan(layer_norm_kernel<DT, W, 16, kWide, kDrop, 1>, a, p, streams, st);
+        if (p.elems > 16)
+            return launch_plan(p.elems == 24 ? layer_norm_kernel<DT, W, 24, kRagged, kDrop, 1>
+                                             : layer_norm_kernel<DT, W, 32, kRagged, kDrop, 1>,
+                               a, p, streams, st);
         if (p.even && p.deal.cluster == 1) {
             const bool plain = a.x != nullptr && a.nranks <= 1;
             if (plain && p.elems == 8)

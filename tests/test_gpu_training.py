@@ -130,10 +130,11 @@ def test_layer_norm(lib, dt, T, H, has_w, has_b):
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("T,H", [(700, 256), (307, 768), (1001, 512), (331, 8192), (40, 2048),
-                                 (459, 1280), (310, 6144), (170, 12288), (153, 16384)])
-def test_norms_of_rows_that_fill_their_teams(lib, dt, T, H):
-    # every form of the kernels for such rows: two at a time and a last one alone, teams
-    # that share a CTA, clusters, rows of 1024 threads
+                                 (459, 1280), (310, 6144), (170, 12288), (153, 16384),
+                                 (154, 9001), (320, 4100), (609, 300)])
+def test_norms_of_many_rows(lib, dt, T, H):
+    # every form of the kernels for more rows than SMs: several at a time and a last one
+    # alone, teams that share a CTA, clusters, long rows, lanes without columns
     g = gen(T, H, 9)
     x, dn, dxo = (dev(stream_like(g, T, H), dt) for _ in range(3))
     w, b = dev(1 + 0.3 * g.normal(size=H), dt), dev(g.normal(size=H), dt)
