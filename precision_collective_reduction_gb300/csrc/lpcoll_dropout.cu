@@ -46,7 +46,7 @@ dropout_kernel(const __grid_constant__ LayerNormArgs a, const Cut cut)
         t = t * cut.rows + which;
         piece -= which * cut.lanes;
     }
-    const Philox rnd(a.drop, a.hidden);
+    const Philox rnd(a.drop, a.hidden, false);
     if (t >= a.tokens || threadIdx.x >= static_cast<unsigned>(cut.lanes * cut.rows))
         return;
     const unsigned long long row = rnd.row(t);

@@ -361,7 +361,7 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Deal deal, int 
     const bool given = kMode == kPlain || !kDrop || a.x != nullptr;
     const int h0 = given ? 1 : 0, nranks = !kDrop ? 0 : (kMode == kPlain ? 1 : a.nranks);
     const bool drop = kDrop && a.drop.least != 0;
-    const Philox rnd(a.drop, a.hidden);
+    const Philox rnd(a.drop, a.hidden, true);
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
     const int lane = threadIdx.x & 31, warps = deal.threads >> 5;
     const bool full = __all_sync(kAll, me.has(NV - 1));
@@ -576,7 +576,7 @@ layer_norm_backward_kernel(const __grid_constant__ LayerNormArgs a, const Deal d
     const bool want_dx = a.dx != nullptr;
     const bool want_dh = kDrop && a.dh != nullptr;
     const bool drop = want_dh && a.drop.least != 0;
-    const Philox rnd(a.drop, a.hidden);
+    const Philox rnd(a.drop, a.hidden, true);
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
     const auto fetch = [&](size_t t, int stage) {
         if (t < a.tokens) {
@@ -674,7 +674,7 @@ layer_norm_backward_team_kernel(const __grid_constant__ LayerNormArgs a, const D
     const bool want_dx = kMode == kPlain || a.dx != nullptr;
     const bool want_dh = kDrop && (kMode == kPlain || a.dh != nullptr);
     const bool drop = want_dh && a.drop.least != 0;
-    const Philox rnd(a.drop, a.hidden);
+    const Philox rnd(a.drop, a.hidden, true);
     const float per_hidden = __fdiv_rn(1.0f, static_cast<float>(a.hidden));
     const int lane = threadIdx.x & 31, warps = deal.threads >> 5;
     const bool full = __all_sync(kAll, me.has(NV - 1));
