@@ -26,8 +26,8 @@
 // layer_norm 45 us (40), one row at a time 51, also as two CTAs an SM at 64 registers. Its
 // gradient 77 us (59), of which 6 are the launch that adds up the sums over tokens; while
 // that took 14, this form took 84, one row after the other 94, with all of a row's values
-// in registers 91, with 8 or 32 columns a thread 109 or 148. residual_dropout 104 us (79)
-// and 92 with p = 0, its gradient 137 (99) and 121: the generator's products do not all fit
+// in registers 91, with 8 or 32 columns a thread 109 or 148. residual_dropout 100 us (79)
+// and 92 with p = 0, its gradient 134 (99) and 121: the generator's products do not all fit
 // under the copies. FP32, 8192 rows of 4096: 47 us (40), 73 (59), 92 (79), 115 (99).
 #pragma once
 
@@ -905,6 +905,14 @@ cudaError_t layer_norm_dt(const LayerNormArgs &a, cudaStream_t st)
             return launch_plan(p.elems == 8 ? layer_norm_kernel<DT, W, 8, kRagged, false, 2>
                                             : layer_norm_kernel<DT, W, 16, kRagged, false, 2>,
                                a, p, streams, st);
+    }
+    // Accesses of 2 or 4 columns: 8192 x 2050 BF16 63 -> 52 us, 8192 x 4100 FP32 110 -> 101.
+    // Of 8 columns equal. Of one column, whose words are handed round, slower where there
+    // is little else to do (4096 x 4097 BF16 114 us, 121), with 4 ranks 183 -> 165.
+    constexpr int kN = Pack<DT, W>::kN;
+    if constexpr (kDrop && kN < 8) {
+        if (p.elems == 16 && p.deal.cluster == 1 && (kN > 1 || a.nranks > 1))
+            return launch_plan(layer_norm_kernel<DT, W, 16, kRagged, true, 1>, a, p, streams, st);
     }
     return launch_plan(p.elems == 8 ? layer_norm_kernel<DT, W, 8, kGeneral, kDrop, 1>
                                     : layer_norm_kernel<DT, W, 16, kGeneral, kDrop, 1>,

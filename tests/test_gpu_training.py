@@ -131,7 +131,7 @@ def test_layer_norm(lib, dt, T, H, has_w, has_b):
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("T,H", [(700, 256), (307, 768), (1001, 512), (331, 8192), (40, 2048),
                                  (459, 1280), (310, 6144), (170, 12288), (153, 16384),
-                                 (154, 9001), (320, 4100), (609, 300)])
+                                 (154, 9001), (320, 4100), (609, 300), (320, 4098), (175, 4099)])
 def test_norms_of_many_rows(lib, dt, T, H):
     # every form of the kernels for more rows than SMs: several at a time and a last one
     # alone, teams that share a CTA, clusters, long rows, lanes without columns
@@ -290,6 +290,27 @@ def test_dropped_values_are_not_read_into_the_result(lib, dt, H):
         outs.append((xo, n, plain, dh))
     for a, b in zip(*outs):
         assert torch.isfinite(a).all() and same(a, b)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [50, 4097, 4098, 4100, 8200])
+@pytest.mark.parametrize("tokens", [4, 160])
+def test_all_bits_of_the_counters(lib, dt, H, tokens):
+    # seeds and offsets with both halves, rows whose counters pass 2^32 and 2^64
+    groups, p = (H + 3) // 4, 0.4
+    assert groups & groups - 1
+    one = torch.ones(tokens, H, device="cuda").to(DT[dt])
+    for seed, offset, power in ((0x123456789, -7, 32), (-9, (5 << 40) + 3, 64), (1 << 62, 0, 32)):
+        first = (1 << power) // groups - 1  # the second row passes the power
+        keep = ref.kept(tokens, H, seed, offset, p, first)
+        rng = words(seed, offset)
+        for norm in (False, True):
+            xo, n, dh = (torch.empty_like(one) for _ in range(3))
+            pcr.residual_dropout(one, None, xo, rng, p, n_out=n if norm else None, first_row=first)
+            assert np.array_equal(f64(xo) != 0, keep)
+            pcr.residual_dropout_backward(one, torch.zeros_like(one) if norm else None,
+                                          xo if norm else None, None, dh, rng, p, first_row=first)
+            assert np.array_equal(f64(dh) != 0, keep)
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
