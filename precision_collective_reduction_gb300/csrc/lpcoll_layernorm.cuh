@@ -24,7 +24,7 @@
 // sums beside the last row's outputs in the gradient, fill one another's waits. Measured
 // on one GB300, 8192 rows of 8192 columns of BF16 (bytes at the copy rate in brackets):
 // layer_norm 45 us (40), one row at a time 51, also as two CTAs an SM at 64 registers. Its
-// gradient 77 us (59), of which 6 are the launch that adds up the sums over tokens; while
+// gradient 76 us (59), of which 6 are the launch that adds up the sums over tokens; while
 // that took 14, this form took 84, one row after the other 94, with all of a row's values
 // in registers 91, with 8 or 32 columns a thread 109 or 148. residual_dropout 100 us (79)
 // and 92 with p = 0, its gradient 134 (99) and 121: the generator's products do not all fit
