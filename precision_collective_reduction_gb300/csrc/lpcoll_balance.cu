@@ -431,7 +431,8 @@ balance_backward_kernel(const __grid_constant__ BalanceArgs a)
             const size_t t = t0 + u * step + threadIdx.x / G;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                x[u][i] = of == 0.0f ? 0.0f : rate * x[u][i] * (n[i] - mean[u]);
+                // padding is 0 beside an infinite rate too
+                x[u][i] = of == 0.0f || !valid[u] ? 0.0f : rate * x[u][i] * (n[i] - mean[u]);
             if (a.accumulate) {
                 float y[PER];
                 load_logits<DT, PER, G>(a.dlogits, t, E, place, y);
