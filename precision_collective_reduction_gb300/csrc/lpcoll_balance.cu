@@ -11,11 +11,12 @@
 // gives the same bits. Few tokens take that cluster alone: its CTAs read one another's
 // rows from shared memory.
 //
-// Measured on one GB300, 32768 tokens of 256 FP32 logits (5.1 us of bytes): 14.6 us, some
-// 9 for the rows (57% issue active: exponentials and the two warp-wide steps of a softmax)
-// and 5 for the cluster (latency); the gradient 12.1 us (9.9). 512 tokens of 64 BF16: 5.8 us
-// in one launch (latency). Two CTAs of rows per SM 18.6 us, a warp per token for 64 experts
-// 12.8 instead of 9.1 (32768 tokens), the next tokens' logits ahead 15.5 (spills).
+// Measured on one GB300, 32768 tokens of 256 FP32 logits (5.1 us of bytes): 16.0 us, some
+// 11 for the rows (exponentials and the two warp-wide steps of a softmax) and 5 for the
+// cluster (latency); the gradient 12.2 us (9.9). 512 tokens of 64 BF16: 5.9 us in one launch
+// (latency). Tried with the hardware's 2^x, which took 14.6 us at the first size but loses
+// digits of small probabilities: two CTAs of rows per SM 18.6 us, a warp per token for 64
+// experts 12.8 instead of 9.1 (32768 tokens), the next tokens' logits ahead 15.5 (spills).
 #include "lpcoll_logits.cuh"
 
 namespace lpc {
@@ -52,10 +53,9 @@ __device__ __forceinline__ bool is_valid(const BalanceArgs &a, size_t t)
 }
 
 // Softmax of N tokens in place, side by side; all zeros where no logit is above
-// -infinity. kSums: for sums over tokens, with the hardware's 2^x, which moves a term by
-// at most |d| 2^-24 of itself and ends at 2^-126 (32768 x 256 FP32: 16.0 -> 14.6 us); the
-// gradient keeps the digits of small probabilities.
-template <int PER, int G, int N, bool kSums> __device__ __forceinline__ void softmax(float (&x)[N][PER])
+// -infinity. The same for the loss and its gradient, with expf: small probabilities have
+// all their digits.
+template <int PER, int G, int N> __device__ __forceinline__ void softmax(float (&x)[N][PER])
 {
     float m[N], sum[N];
 #pragma unroll
@@ -76,7 +76,7 @@ template <int PER, int G, int N, bool kSums> __device__ __forceinline__ void sof
         sum[u] = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            x[u][i] = kSums ? exp_term(x[u][i] - m[u]) : expf(x[u][i] - m[u]);
+            x[u][i] = expf(x[u][i] - m[u]);
             sum[u] += x[u][i];
         }
     }
@@ -159,7 +159,7 @@ __device__ __forceinline__ void make_row(const BalanceArgs &a, MakeSmem &sm, int
                 }
             }
         }
-        softmax<PER, G, N, true>(x);
+        softmax<PER, G, N>(x);
 #pragma unroll
         for (int u = 0; u < N; ++u)
 #pragma unroll
@@ -412,7 +412,7 @@ balance_backward_kernel(const __grid_constant__ BalanceArgs a)
             valid[u] = there[u] && is_valid(a, t);
             load_token<DT, PER, G>(a, a.logits, t, valid[u], place, x[u]);
         }
-        softmax<PER, G, N, false>(x);
+        softmax<PER, G, N>(x);
         float mean[N];
 #pragma unroll
         for (int u = 0; u < N; ++u) {

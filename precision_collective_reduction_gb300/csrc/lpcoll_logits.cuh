@@ -8,21 +8,6 @@ namespace lpc {
 
 namespace {
 
-// 2^x, 2 ulp; results below the normal range are 0.
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// A term e^d of a softmax's sum, d <= 0: the rounding of the product moves it
-// by |d| 2^-24 of itself, at most 2^-25 of the sum's largest term.
-__device__ __forceinline__ float exp_term(float d)
-{
-    return exp2_fast(__fmul_rn(d, 1.44269504f));
-}
-
 // The PER experts of a lane come in runs of kRun consecutive ones, run r at
 // (r * LANES + lane) * kRun for the LANES lanes of a token, so that a run is one
 // access where rows of logits are a multiple of a run.

@@ -23,6 +23,23 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 // Keys up to this one are "no expert": -infinity, a choice taken, padding.
 constexpr uint32_t kKeyNone = 0x007FFFFFu;
 
+// 2^x, 2 ulp; results below the normal range are 0.
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A term e^d of a softmax's sum, d <= 0. The constant is 0.224 2^-24 of itself off and
+// the product rounds by up to 2^-24 of itself, which moves a term by up to 1.224 |d| 2^-24
+// of itself, beside the 2 ulp of 2^x. Of the sum, whose largest term is 1, that is at most
+// 1.224 |d| e^d 2^-24 <= 0.45 2^-24 a term: enough for a sum, not for a probability.
+__device__ __forceinline__ float exp_term(float d)
+{
+    return exp2_fast(__fmul_rn(d, 1.44269504f));
+}
+
 // Order-preserving key of a logit: -0 equals +0, and every NaN is the largest
 // key, since an addition returns all of them as 0x7FFFFFFF.
 __device__ __forceinline__ uint32_t logit_key(float x)
