@@ -775,24 +775,21 @@ layer_norm_backward_team_kernel(const __grid_constant__ LayerNormArgs a, const D
         Keep<kElems, kN> keep;
         if (drop)
             keep.make(rnd, me, t);
-        // D = dx' + r q - r c1 - (x - mean) r c2, with the constants together
+        // x - mean first: a mean that is large beside the spread costs no digits but its own
         const float r = inv_rms(s.m2, per_hidden, a.eps);
         const float c1 = s.q * per_hidden, c2 = r * r * (s.a * per_hidden);
-        const Vec<kN> shift = splat<kN>(-r * s.mean);
-        const Vec<kN> constant = splat<kN>(r * fmaf(c2, s.mean, -c1));
+        const Vec<kN> centre = splat<kN>(-s.mean);
         for_columns<kMode>(full, [&](auto all) {
 #pragma unroll
             for (int c = 0; c < NV; ++c) {
                 if (!decltype(all)::kAll && !me.has(c))
                     continue;
-                const Vec<kN> x = me.read(t, stage, kGradX, c);
+                const Vec<kN> d = plus(me.read(t, stage, kGradX, c), centre);
                 const Vec<kN> dn = me.read(t, stage, kGradDn, c);
-                s_w[c] = fma(fma(r, x, shift), dn, s_w[c]);
+                s_w[c] = fma(mul(r, d), dn, s_w[c]);
                 s_b[c] = plus(s_b[c], dn);
-                Vec<kN> q = constant;
-                if (given)
-                    q = plus(q, me.read(t, stage, kGradDx, c));
-                q = fma(r, mul(dn, unpack<DT, W>(w[c])), fma(-(r * c2), x, q));
+                Vec<kN> q = fma(-c2, d, fma(dn, unpack<DT, W>(w[c]), splat<kN>(-c1)));
+                q = given ? fma(r, q, me.read(t, stage, kGradDx, c)) : mul(r, q);
                 if (want_dx)
                     store_vec_of<DT, W>(a.dx, me.elem(t, c), q);
                 if (want_dh)
