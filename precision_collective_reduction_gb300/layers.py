@@ -572,6 +572,13 @@ def _ids(ids, dev):
     return _ptr(ids, "ids", torch.int32, (T,), dev), 0, T
 
 
+def _first_id(first_id):
+    # ctypes would take it modulo 2^64, where it stands for other ids
+    if not -(1 << 63) <= first_id < 1 << 63:
+        raise ValueError("first_id must be a 64-bit number")
+    return first_id
+
+
 def token_embed(table, ids, out, first_id=0, scale=1.0, stream=None):
     """Rows of a shard of a vocabulary: table [V, H] holds the ids first_id ..
     first_id + V - 1; out [T, H] = scale * table[ids - first_id], and zeros for
@@ -581,8 +588,8 @@ def token_embed(table, ids, out, first_id=0, scale=1.0, stream=None):
     V, H = _shape(table, 2, "table")
     tp = _ptr(table, "table", table.dtype, (V, H), dev)
     op = _ptr(out, "out", table.dtype, (T, H), dev)
-    B._check(B.lib().token_embed(tp, V, ip, index, first_id, T, H, _code(table), scale, op,
-                                 _stream(stream, dev)), "token_embed")
+    B._check(B.lib().token_embed(tp, V, ip, index, _first_id(first_id), T, H, _code(table), scale,
+                                 op, _stream(stream, dev)), "token_embed")
     return out
 
 
@@ -605,7 +612,7 @@ def token_embed_backward(dout, ids, dtable, first_id=0, scale=1.0, accumulate=Fa
     st = _stream(stream, dev)
     need = L.token_embed_backward_workspace_bytes(T, V, H)
     wp, wn, _keep = _scratch(workspace, need, st, dev)
-    B._check(L.token_embed_backward(gp, ip, index, first_id, T, V, H, _code(dout), scale,
-                                    1 if accumulate else 0, tp, wp, wn, st),
+    B._check(L.token_embed_backward(gp, ip, index, _first_id(first_id), T, V, H, _code(dout),
+                                    scale, 1 if accumulate else 0, tp, wp, wn, st),
              "token_embed_backward")
     return dtable

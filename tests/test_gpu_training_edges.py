@@ -146,3 +146,16 @@ def test_norm_gradients_of_rows_far_from_zero(lib, dt, T, H, dropout):
         check()
         pcr.layer_norm_backward(dn, xd, None, eps=eps, dw=dw, db=db)
     check()
+
+
+# -- embedding: ids of the shard --------------------------------------------------
+
+@pytest.mark.parametrize("first", [1 << 63, -(1 << 63) - 1, 1 << 64])
+def test_first_ids_that_are_no_64_bit_numbers_are_refused(first):
+    # taken modulo 2^64 they would stand for other ids
+    table, ids = torch.ones(4, 8, device="cuda"), torch.tensor([0, -(1 << 63)], device="cuda")
+    out, d = torch.empty(2, 8, device="cuda"), torch.empty(4, 8, device="cuda")
+    with pytest.raises(ValueError):
+        pcr.token_embed(table, ids, out, first_id=first)
+    with pytest.raises(ValueError):
+        pcr.token_embed_backward(out, ids, d, first_id=first)
