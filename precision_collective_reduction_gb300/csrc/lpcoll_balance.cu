@@ -195,14 +195,24 @@ __device__ __forceinline__ void make_row(const BalanceArgs &a, MakeSmem &sm, int
         sm.sums[tid] = sum;
 }
 
-struct JoinSmem {
-    float sums[kWarps][33];
-    int counts[kWarps][33];
+// What the CTAs of a cluster make the loss from.
+struct LossSmem {
     float dot[kWarps];  // sum of n_e P_e, of a warp's experts
     int slots[kWarps];  // and of n_e
     float cta_dot;
     int cta_slots;
 };
+
+struct JoinSmem {
+    float sums[kWarps][33];
+    int counts[kWarps][33];
+    LossSmem loss;
+};
+
+// A kernel has 48 KB of static shared memory for certain.
+constexpr size_t kStaticSmem = 48 * 1024;
+static_assert(sizeof(MakeSmem) + sizeof(LossSmem) <= kStaticSmem, "balance_one_kernel's");
+static_assert(sizeof(JoinSmem) <= kStaticSmem, "balance_join_kernel's");
 
 __device__ __forceinline__ unsigned join_rank()
 {
@@ -241,7 +251,7 @@ __device__ __forceinline__ int join_load(const int *p, unsigned rank)
 
 // The loss, from each warp's part of sum n_e P_e and sum n_e (in its lane 0). All
 // threads of the cluster come here; the first thread of all has `tokens`.
-__device__ __forceinline__ void write_loss(const BalanceArgs &a, JoinSmem &sm, unsigned rank,
+__device__ __forceinline__ void write_loss(const BalanceArgs &a, LossSmem &sm, unsigned rank,
                                            float dot, int slots, int tokens)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -312,7 +322,7 @@ __device__ __forceinline__ void join_rows(const BalanceArgs &a, JoinSmem &sm, in
         }
         __syncthreads();
     }
-    write_loss(a, sm, rank, dot, slots, tokens);
+    write_loss(a, sm.loss, rank, dot, slots, tokens);
 }
 
 template <int DT, int PER, int G>
@@ -346,7 +356,7 @@ __global__ void __launch_bounds__(kWide) balance_one_kernel(const __grid_constan
 {
     wait_prior_grid();
     __shared__ MakeSmem sm;
-    __shared__ JoinSmem join;
+    __shared__ LossSmem of_loss;
     make_row<DT, PER, G>(a, sm, blockIdx.x, kJoin);
     join_barrier();
     const unsigned rank = join_rank();
@@ -374,7 +384,7 @@ __global__ void __launch_bounds__(kWide) balance_one_kernel(const __grid_constan
         for (unsigned c = 0; c < kJoin; ++c)
             tokens += join_load(&sm.tokens, c);
     // write_loss ends with a barrier of the cluster, behind all of these reads
-    write_loss(a, join, rank, warp_sum(dot), __reduce_add_sync(kAll, slots), tokens);
+    write_loss(a, of_loss, rank, warp_sum(dot), __reduce_add_sync(kAll, slots), tokens);
 }
 
 // Gradient: the counts of a lane's experts stay in its registers.
