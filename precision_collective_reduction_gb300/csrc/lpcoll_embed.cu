@@ -137,24 +137,21 @@ embed_kernel(const __grid_constant__ EmbedArgs a, const RowCut c)
 
 // ---------------------------------------------------------------------------
 // Tokens sorted by row: a radix sort of (row, token), digits of up to kDigitBits
-// bits, each pass a stable counting sort. The tokens are cut into chunks, one CTA
-// each; with more than one, a first launch counts the digits of every chunk, and a
-// CTA of the second adds up the counts of the chunks before its own. Tokens
-// without a row have the key `vocab` and come last.
+// bits, each pass a stable counting sort. Here, for more than kClusterTokens, the
+// tokens are cut into chunks, one CTA each: a first launch counts the digits of every
+// chunk, and a CTA of the second adds up the counts of the chunks before its own.
+// Tokens without a row have the key `vocab` and come last.
 // ---------------------------------------------------------------------------
 
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 constexpr int kMaxChunks = 128;
-constexpr int kOneChunk = 2048;  // tokens that one CTA sorts in one launch a pass
-constexpr int kMinChunk = 512;
 
 struct SortPlan {
     int passes, bits;  // bits of a digit
-    int chunks, chunk_len;
 };
 
-SortPlan sort_plan(size_t tokens, size_t vocab)
+SortPlan sort_plan(size_t vocab)
 {
     int key_bits = 1;
     while (key_bits < 32 && (vocab >> key_bits) != 0)
@@ -162,16 +159,16 @@ SortPlan sort_plan(size_t tokens, size_t vocab)
     SortPlan p;
     p.passes = (key_bits + kDigitBits - 1) / kDigitBits;
     p.bits = (key_bits + p.passes - 1) / p.passes;
-    size_t len = kOneChunk;
-    if (tokens > kOneChunk) {
-        const size_t even = (tokens + kMaxChunks - 1) / kMaxChunks;
-        len = (even + kThreads - 1) / kThreads * kThreads;
-        len = len > kMinChunk ? len : kMinChunk;
-    }
-    p.chunk_len = static_cast<int>(len);
-    p.chunks = tokens == 0 ? 1 : static_cast<int>((tokens + len - 1) / len);
     return p;
 }
+
+// Tokens of a chunk, and chunks.
+size_t chunk_len(size_t tokens)
+{
+    const size_t even = (tokens + kMaxChunks - 1) / kMaxChunks;
+    return (even + kThreads - 1) / kThreads * kThreads;
+}
+size_t chunks_of(size_t tokens) { return (tokens + chunk_len(tokens) - 1) / chunk_len(tokens); }
 
 struct RadixArgs {
     const int32_t *keys, *order;  // of the pass before; NULL in the first
@@ -228,9 +225,6 @@ radix_place_kernel(const __grid_constant__ EmbedArgs e, const RadixArgs a)
 #pragma unroll
         for (int w = 0; w < kWarpsPerCta; ++w)
             next[w][d] = 0;
-    if (a.keys == nullptr && a.chunks == 1)
-        for (int w = tid; w < a.words; w += kThreads)
-            store_i32(reinterpret_cast<int32_t *>(a.used) + w, 0);
     __syncthreads();
 
     const long long lo = static_cast<long long>(blockIdx.x) * a.chunk_len;
@@ -240,19 +234,17 @@ radix_place_kernel(const __grid_constant__ EmbedArgs e, const RadixArgs a)
     const long long w_end = min(w_lo + part, end);
     for (long long i = w_lo + lane; i < w_end; i += 32)
         atomicAdd(&next[warp][key_of(e, a, static_cast<int>(i)) >> a.shift & (digits - 1)], 1);
-    if (a.chunks > 1) {
-        // a thread per digit, several chunks' counts in flight
-        for (int d = tid; d < digits; d += kThreads) {
-            int sum = 0, prior = 0;
+    // a thread per digit, several chunks' counts in flight
+    for (int d = tid; d < digits; d += kThreads) {
+        int sum = 0, prior = 0;
 #pragma unroll 16
-            for (int c = 0; c < a.chunks; ++c) {
-                const int v = load_i32(a.counts + static_cast<size_t>(c) * digits + d);
-                sum += v;
-                prior += c < static_cast<int>(blockIdx.x) ? v : 0;
-            }
-            total[d] = sum;
-            before[d] = prior;
+        for (int c = 0; c < a.chunks; ++c) {
+            const int v = load_i32(a.counts + static_cast<size_t>(c) * digits + d);
+            sum += v;
+            prior += c < static_cast<int>(blockIdx.x) ? v : 0;
         }
+        total[d] = sum;
+        before[d] = prior;
     }
     __syncthreads();
     // places of the warps' tokens, from the digit's first of this chunk on
@@ -263,10 +255,6 @@ radix_place_kernel(const __grid_constant__ EmbedArgs e, const RadixArgs a)
             const int v = next[w][d];
             next[w][d] = run;
             run += v;
-        }
-        if (a.chunks == 1) {
-            total[d] = run;
-            before[d] = 0;
         }
     }
     __syncthreads();
@@ -858,12 +846,13 @@ int tile_len(size_t tokens)
 
 size_t aligned(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
-// The workspace: keys and order twice, the digits' counts, the used rows' bits, and
-// the partial rows.
+// The workspace: keys and order, twice and with the digits' counts where the sort goes
+// through memory, the used rows' bits, and the partial rows.
 struct Scratch {
     size_t keys, counts, used, partial;  // bytes of one
     size_t words, tiles;
-    size_t all() const { return 4 * keys + counts + used + 2 * partial; }
+    int copies;  // of keys and order
+    size_t all() const { return 2 * copies * keys + counts + used + 2 * partial; }
 };
 
 Scratch scratch(size_t tokens, size_t vocab, size_t hidden)
@@ -872,8 +861,8 @@ Scratch scratch(size_t tokens, size_t vocab, size_t hidden)
     s.words = (vocab + 31) / 32;
     s.tiles = (tokens + tile_len(tokens) - 1) / tile_len(tokens);
     s.keys = aligned(tokens * sizeof(int32_t));
-    s.counts = aligned(static_cast<size_t>(kDigits) * sort_plan(tokens, vocab).chunks *
-                       sizeof(int32_t));
+    s.copies = tokens > kClusterTokens ? 2 : 1;
+    s.counts = tokens > kClusterTokens ? aligned(kDigits * chunks_of(tokens) * sizeof(int32_t)) : 0;
     s.used = aligned(s.words * sizeof(uint32_t));
     s.partial = aligned(s.tiles * hidden * sizeof(float));
     return s;
@@ -914,7 +903,7 @@ cudaError_t cluster_sort_dt(const EmbedArgs &a, const RadixArgs &r, int passes, 
         ++log_n;
     const size_t smem =
         ((static_cast<size_t>(4) << log_n) + (kSortWarps + 2) * (1u << r.bits)) * sizeof(int);
-    // some 8 us and 0.7 ns a token, at 45 GB/s an SM
+    // some 6 us and 0.7 ns a token, at 45 GB/s an SM
     const size_t bytes = 256 * 1024 + 32 * a.tokens;
     int rows = kMostRows;
     while (rows > 1 && rows * a.hidden * sizeof(float) > bytes)
@@ -973,10 +962,10 @@ cudaError_t launch_embed_backward(const EmbedArgs &a, cudaStream_t st)
         return LPC_BY_ROW(few_dt, a.dtype, a.hidden, a, st);
     if (a.tokens > 0) {
         const Scratch w = scratch(a.tokens, a.vocab, a.hidden);
-        const SortPlan p = sort_plan(a.tokens, a.vocab);
+        const SortPlan p = sort_plan(a.vocab);
         char *at = static_cast<char *>(a.workspace);
-        int32_t *keys[2], *order[2];
-        for (int i = 0; i < 2; ++i) {
+        int32_t *keys[2] = {}, *order[2] = {};
+        for (int i = 0; i < w.copies; ++i) {
             keys[i] = reinterpret_cast<int32_t *>(at);
             order[i] = reinterpret_cast<int32_t *>(at + w.keys);
             at += 2 * w.keys;
@@ -990,8 +979,8 @@ cudaError_t launch_embed_backward(const EmbedArgs &a, cudaStream_t st)
         r.tokens = static_cast<int>(a.tokens);
         r.words = static_cast<int>(w.words);
         r.bits = p.bits;
-        r.chunks = p.chunks;
-        r.chunk_len = p.chunk_len;
+        r.chunks = static_cast<int>(chunks_of(a.tokens));
+        r.chunk_len = static_cast<int>(chunk_len(a.tokens));
         if (a.tokens <= kClusterTokens) {
             r.keys_out = keys[0];
             r.order_out = order[0];
@@ -1006,14 +995,9 @@ cudaError_t launch_embed_backward(const EmbedArgs &a, cudaStream_t st)
             r.shift = i * p.bits;
             r.keys_out = keys[i & 1];
             r.order_out = order[i & 1];
-            if (p.chunks > 1) {
-                const cudaError_t e =
-                    launch_kernel_block(radix_count_kernel, p.chunks, kThreads, 0, st, a, r);
-                if (e != cudaSuccess)
-                    return e;
-            }
-            const cudaError_t e =
-                launch_kernel_block(radix_place_kernel, p.chunks, kThreads, 0, st, a, r);
+            cudaError_t e = launch_kernel_block(radix_count_kernel, r.chunks, kThreads, 0, st, a, r);
+            if (e == cudaSuccess)
+                e = launch_kernel_block(radix_place_kernel, r.chunks, kThreads, 0, st, a, r);
             if (e != cudaSuccess)
                 return e;
             r.keys = r.keys_out;
