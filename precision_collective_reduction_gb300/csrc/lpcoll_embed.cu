@@ -731,18 +731,19 @@ embed_join_kernel(const __grid_constant__ EmbedArgs a, const SumArgs s, const Ro
 
 // ---------------------------------------------------------------------------
 // Few tokens: one launch, without a sort. A CTA for each token (and kLanes pieces of
-// its row) looks through all ids:
-// if an earlier token has the same row it has nothing to do, else it adds up the rows
-// of the tokens that have. Where they are many, kSlices groups of lanes take
-// consecutive parts of that list, and their sums are added in order.
+// its row) looks through all ids: if an earlier token has the same row it has nothing to
+// do, else it adds up the rows of the tokens that have. (Long lists in four parts, by as
+// many groups of lanes, were slower: 512 tokens of 1024 FP32 with 64 tokens a row 8.4 us
+// where one list takes 6.6, all of one row of 4096 BF16 42.1 and 41.1.) Two CTAs an SM
+// leave the registers for all of a lane's rows in flight: 100 tokens into 8000 x 1024 BF16
+// 6.3 us, 7.1 with the compiler's own choice, though 512 into 8000 x 8192, which are mostly
+// clearing, 49.7 and 45.7.
 // ---------------------------------------------------------------------------
 
 constexpr int kFewTokens = 512;
-constexpr int kSlices = 4;
-constexpr int kLongList = 32;
 
 template <int DT, int W>
-__global__ void __launch_bounds__(kLanes)
+__global__ void __launch_bounds__(kLanes, 2)
 embed_few_kernel(const __grid_constant__ EmbedArgs a, unsigned segs, int clear)
 {
     wait_prior_grid();
@@ -750,7 +751,6 @@ embed_few_kernel(const __grid_constant__ EmbedArgs a, unsigned segs, int clear)
     constexpr int kCols = Cols::kCols;
     __shared__ uint32_t same[kFewTokens / 32];  // bit t: token t has this CTA's row
     __shared__ int list[kFewTokens];
-    __shared__ float part[kLanes][kCols + 1];
     const int T = static_cast<int>(a.tokens), tid = threadIdx.x, lane = tid & 31;
     const size_t sum_ctas = a.tokens * segs;
     if (blockIdx.x >= sum_ctas) {
@@ -795,42 +795,22 @@ embed_few_kernel(const __grid_constant__ EmbedArgs a, unsigned segs, int clear)
         list[i] = w * 32 + static_cast<int>(__fns(same[w], 0, left + 1));
     }
     __syncthreads();
-    const int slices = n > kLongList ? kSlices : 1, lanes = kLanes / slices;
-    const int slice = tid / lanes, place = tid - slice * lanes;
-    const int each = (n + slices - 1) / slices;
-    const int end = min(n, (slice + 1) * each);
-    const size_t seg_lo = static_cast<size_t>(blockIdx.x % segs) * kLanes * kCols;
-    const size_t seg_end = min(a.hidden, seg_lo + kLanes * kCols);
-    for (size_t col0 = seg_lo; col0 < seg_end; col0 += static_cast<size_t>(lanes) * kCols) {
-        const Cols cols{col0 + static_cast<size_t>(place) * kCols, a.hidden};
-        const bool in = cols.col < a.hidden;
-        float acc[kCols] = {};
-        for (int i0 = slice * each; in && i0 < end; i0 += kAhead) {
-            typename Pack<DT, W>::Raw raw[kAhead][Cols::kPacks];
+    const Cols cols{(static_cast<size_t>(blockIdx.x % segs) * kLanes + tid) * kCols, a.hidden};
+    if (cols.col >= a.hidden)
+        return;
+    float acc[kCols] = {};
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+        typename Pack<DT, W>::Raw raw[kAhead][Cols::kPacks];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (i0 + j < end)
-                    cols.load(a.dout, static_cast<size_t>(list[i0 + j]), raw[j]);
+        for (int j = 0; j < kAhead; ++j)
+            if (i0 + j < n)
+                cols.load(a.dout, static_cast<size_t>(list[i0 + j]), raw[j]);
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (i0 + j < end)
-                    cols.add(raw[j], acc);
-        }
-        if (slices > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int q = 0; q < kCols; ++q)
-                part[tid][q] = acc[q];
-            __syncthreads();
-            if (slice == 0)
-                for (int r = 1; r < kSlices; ++r)
-#pragma unroll
-                    for (int q = 0; q < kCols; ++q)
-                        acc[q] += part[r * lanes + place][q];
-        }
-        if (slice == 0 && in)
-            cols.finish(a, static_cast<size_t>(row), acc);
+        for (int j = 0; j < kAhead; ++j)
+            if (i0 + j < n)
+                cols.add(raw[j], acc);
     }
+    cols.finish(a, static_cast<size_t>(row), acc);
 }
 
 // Sorted tokens of a tile: few, so that small batches fill the GPU, and more where
