@@ -12,9 +12,10 @@
 // rows from shared memory.
 //
 // Measured on one GB300, 32768 tokens of 256 FP32 logits (5.1 us of bytes): 16.0 us, some
-// 11 for the rows (exponentials and the two warp-wide steps of a softmax) and 5 for the
-// cluster (latency); the gradient 12.2 us (9.9). 512 tokens of 64 BF16: 5.9 us in one launch
-// (latency). Tried with the hardware's 2^x, which took 14.6 us at the first size but loses
+// 11 for the rows (62% issue active at half of the warps: exponentials and the two warp-wide
+// steps of a softmax) and 5 for the cluster (latency); the gradient 12.1 us (9.9). 512 tokens
+// of 64 BF16: 5.9 us in one launch (latency). 8192 tokens of 1024 FP32: 24.4 us (5.0), with 32
+// logits and 32 sums a lane, which spill at 64 registers, and 152 rows of 2049 numbers. Tried with the hardware's 2^x, which took 14.6 us at the first size but loses
 // digits of small probabilities: two CTAs of rows per SM 18.6 us, a warp per token for 64
 // experts 12.8 instead of 9.1 (32768 tokens), the next tokens' logits ahead 15.5 (spills).
 #include "lpcoll_logits.cuh"
@@ -29,7 +30,9 @@ constexpr int kWide = 1024;            // threads of a CTA that makes sums
 constexpr int kWarps = kWide / 32;
 constexpr int kJoin = 8;               // CTAs of the cluster that joins the rows
 constexpr int kRows = 8;               // warps whose sums are in shared memory at a time
-constexpr size_t kOneLaunch = 512;     // tokens that the cluster takes alone
+// Tokens that the cluster takes alone: 512 of 64 BF16 6.6 us, two launches 7.5; of 256 FP32
+// 7.2 and 7.5, 1024 of them 9.5 and 7.5; 512 of 1000 17 and 16.
+constexpr size_t kOneLaunch = 512;
 
 // Largest of, and sum over, the G lanes of a token; the same bits in each.
 template <int G> __device__ __forceinline__ float group_largest(float v)

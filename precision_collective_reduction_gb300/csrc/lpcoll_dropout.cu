@@ -10,7 +10,7 @@
 // (measured: 0.165 SM clocks a column), 38 us of 8192 x 8192 columns on a GB300, beside
 // some 15 other instructions a column. FP32 hides them behind its bytes: 8192 x 4096
 // with residual 59 us (floor 59). BF16 has half the bytes: 8192 x 8192 with
-// residual 77 us (floor 59), its gradient 72 (floor 40): 70% of the issue slots. Six
+// residual 76 us (floor 59), its gradient 72 (floor 40): 70% of the issue slots. Six
 // CTAs of 256 lanes an SM at 40 registers (8 at 32 in FP32) were faster than 4 and 5
 // without spills; two pieces in flight and the next piece's loads ahead were not.
 #include "lpcoll_layernorm.cuh"

@@ -15,8 +15,9 @@
 // keep DRAM busy while those wait for memory.
 //
 // Measured on one GB300 (bytes at the copy rate in brackets): the rows of 16384 tokens of
-// 8192 BF16 from one of four shards 49 us (46), from a whole table 70; in one piece of 16
-// bytes a lane and CTAs of 4 KB 76. The gradient of 16384 tokens into 32000 x 8192: 226 us
+// 8192 BF16 from one of four shards 49 us (46), from a whole table 70 (63: 201 MB are read
+// for 157 MB of distinct rows, which do not all stay in L2 beside the outputs); in one
+// piece of 16 bytes a lane and CTAs of 4 KB 76. The gradient of 16384 tokens into 32000 x 8192: 226 us
 // (194), of them the sort 14-20, which clears 144 MB meanwhile, the sums 195, the last launch
 // 6; with a sort of four launches, the clearing behind the sums and 4 rows in flight a lane
 // 295. 777 tokens into 4001 x 1025 FP32: 13 us (2.5), the latencies of three launches.
@@ -143,9 +144,9 @@ embed_kernel(const __grid_constant__ EmbedArgs a, const RowCut c)
 // Tokens without a row have the key `vocab` and come last.
 // ---------------------------------------------------------------------------
 
-constexpr int kDigitBits = 9;
+constexpr int kDigitBits = 9;  // 10^6 tokens into 128000 rows: 262 us, with 8 (a pass more) 287
 constexpr int kDigits = 1 << kDigitBits;
-constexpr int kMaxChunks = 128;
+constexpr int kMaxChunks = 128;  // 300000 tokens of 512 BF16: 166 us, with 64 176, with 256 185
 
 struct SortPlan {
     int passes, bits;  // bits of a digit
@@ -418,6 +419,9 @@ __device__ __forceinline__ void clear_rows(const EmbedArgs &a, size_t v0, int ro
 constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+// As many as the shared memory of 8 CTAs holds. Against the launches through memory: 8192
+// tokens into 32000 x 2048 BF16 64 us and 68, 16384 into 128000 x 1024 108 and 118, 32768
+// into 32000 x 4096 155 and 160, 65536 into 32000 x 1024 90 and 87.
 constexpr int kClusterTokens = 65536;
 
 __device__ __forceinline__ unsigned sort_rank()
@@ -607,7 +611,9 @@ __device__ __forceinline__ int key_at(const SumArgs &s, long long i)
     return i >= 0 && i < s.tokens ? load_i32(s.keys + i) : -1;
 }
 
-// Rows of the table that a CTA clears: some 64 KB of them, a power of 2 up to 32.
+// Rows of the table that a CTA clears: some 64 KB of them, a power of 2 up to 32. (200
+// tokens into 8000 x 1024 6.9 us, with 16 KB 10.7, with 256 KB 8.4; 8192 into 32000 x 2048
+// 64, 70 and 67.)
 int rows_to_clear(size_t hidden)
 {
     int rows = 1;
@@ -740,6 +746,8 @@ embed_join_kernel(const __grid_constant__ EmbedArgs a, const SumArgs s, const Ro
 // clearing, 49.7 and 45.7.
 // ---------------------------------------------------------------------------
 
+// Against the sort and its launches: 200 tokens into 8000 x 1024 BF16 6.9 us and 12.4, 512
+// 9.5 and 13.2, 900 13.8 and 14.1; into 8000 x 8192 512 50 and 48, 900 69 and 51.
 constexpr int kFewTokens = 512;
 
 template <int DT, int W>
@@ -814,7 +822,10 @@ embed_few_kernel(const __grid_constant__ EmbedArgs a, unsigned segs, int clear)
 }
 
 // Sorted tokens of a tile: few, so that small batches fill the GPU, and more where
-// there are many tokens, so that the partial rows stay few.
+// there are many tokens, so that the partial rows stay few. 900 tokens into 8000 x 1024
+// BF16 14.1 us, with 16 15.6, with 32 19.7, though 8192 into 4000 x 2048, twice a row,
+// 35, 30 and 28; 16384 into 128000 x 1024 108 with 32, 105 with 16, 114 with 64, 32768 into
+// 32000 x 4096 155, 166 and 156.
 int tile_len(size_t tokens)
 {
     if (tokens <= 8192)
@@ -883,7 +894,8 @@ cudaError_t cluster_sort_dt(const EmbedArgs &a, const RadixArgs &r, int passes, 
         ++log_n;
     const size_t smem =
         ((static_cast<size_t>(4) << log_n) + (kSortWarps + 2) * (1u << r.bits)) * sizeof(int);
-    // some 6 us and 0.7 ns a token, at 45 GB/s an SM
+    // some 6 us and 0.7 ns a token, at 45 GB/s an SM (2000 tokens into 8000 x 1024 BF16
+    // 17.8 us, with half of it 20.1; 16384 into 128000 x 1024 108, with twice as much 114)
     const size_t bytes = 256 * 1024 + 32 * a.tokens;
     int rows = kMostRows;
     while (rows > 1 && rows * a.hidden * sizeof(float) > bytes)

@@ -24,11 +24,11 @@
 // sums beside the last row's outputs in the gradient, fill one another's waits. Measured
 // on one GB300, 8192 rows of 8192 columns of BF16 (bytes at the copy rate in brackets):
 // layer_norm 45 us (40), one row at a time 51, also as two CTAs an SM at 64 registers. Its
-// gradient 76 us (59), of which 6 are the launch that adds up the sums over tokens; while
+// gradient 77 us (59), of which 6 are the launch that adds up the sums over tokens; while
 // that took 14, this form took 84, one row after the other 94, with all of a row's values
 // in registers 91, with 8 or 32 columns a thread 109 or 148. residual_dropout 100 us (79)
-// and 92 with p = 0, its gradient 134 (99) and 121: the generator's products do not all fit
-// under the copies. FP32, 8192 rows of 4096: 47 us (40), 73 (59), 92 (79), 115 (99).
+// and 92 with p = 0, its gradient 133 (99) and 122: the generator's products do not all fit
+// under the copies. FP32, 8192 rows of 4096: 48 us (40), 71 (59), 93 (79), 113 (99).
 #pragma once
 
 #include "lpcoll_philox.cuh"
@@ -830,8 +830,8 @@ Plan layer_norm_plan(size_t tokens, int hidden, int dtype, int streams, bool gra
     Plan p;
     p.wide = false;
     // rows above 8192 columns in one CTA all the same, at 24 or 32 columns a thread, if
-    // their copies fit (2048 x 12288 BF16, norm, with dropout, and their gradients: 19, 50,
-    // 39 and 75 us; in a CTA of 1024 threads that reads its weights for every row 26 and 62,
+    // their copies fit (2048 x 12288 BF16, norm, with dropout, and their gradients: 20, 50,
+    // 40 and 72 us; in a CTA of 1024 threads that reads its weights for every row 26 and 62,
     // over a cluster of two 82 and 110)
     const int least = gradient ? 2 : 1;
     const bool longer = hidden > kRow && tokens > kSms && width == 16 &&
