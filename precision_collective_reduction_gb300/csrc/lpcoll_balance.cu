@@ -15,9 +15,10 @@
 // 11 for the rows (62% issue active at half of the warps: exponentials and the two warp-wide
 // steps of a softmax) and 5 for the cluster (latency); the gradient 12.1 us (9.9). 512 tokens
 // of 64 BF16: 5.9 us in one launch (latency). 8192 tokens of 1024 FP32: 24.4 us (5.0), with 32
-// logits and 32 sums a lane, which spill at 64 registers, and 152 rows of 2049 numbers. Tried with the hardware's 2^x, which took 14.6 us at the first size but loses
-// digits of small probabilities: two CTAs of rows per SM 18.6 us, a warp per token for 64
-// experts 12.8 instead of 9.1 (32768 tokens), the next tokens' logits ahead 15.5 (spills).
+// logits and 32 sums a lane, which spill at 64 registers, and 152 rows of 2049 numbers. Tried
+// with the hardware's 2^x, which took 14.6 us at the first size but loses digits of small
+// probabilities: two CTAs of rows per SM 18.6 us, a warp per token for 64 experts 12.8 instead
+// of 9.1 (32768 tokens), the next tokens' logits ahead 15.5 (spills).
 #include "lpcoll_logits.cuh"
 
 namespace lpc {
