@@ -18,6 +18,7 @@ who wants the memory back passes a workspace).
 """
 import contextlib
 import ctypes
+import operator
 import threading
 import warnings
 
@@ -574,6 +575,7 @@ def _ids(ids, dev):
 
 def _first_id(first_id):
     # ctypes would take it modulo 2^64, where it stands for other ids
+    first_id = operator.index(first_id)
     if not -(1 << 63) <= first_id < 1 << 63:
         raise ValueError("first_id must be a 64-bit number")
     return first_id

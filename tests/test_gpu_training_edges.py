@@ -159,3 +159,16 @@ def test_first_ids_that_are_no_64_bit_numbers_are_refused(first):
         pcr.token_embed(table, ids, out, first_id=first)
     with pytest.raises(ValueError):
         pcr.token_embed_backward(out, ids, d, first_id=first)
+
+
+@pytest.mark.parametrize("kind", [int, np.int64, np.int32, torch.tensor])
+def test_first_ids_of_every_integer_type(kind):
+    table = torch.randn(4, 8, device="cuda")
+    ids = torch.tensor([7, 9, 10, 11], device="cuda")
+    out, d = torch.empty(4, 8, device="cuda"), torch.empty(4, 8, device="cuda")
+    pcr.token_embed(table, ids, out, first_id=kind(7))
+    assert same(out[:3], table[[0, 2, 3]]) and not out[3].any()
+    pcr.token_embed_backward(table, ids, d, first_id=kind(7))
+    assert same(d[[0, 2, 3]], table[:3]) and not d[1].any()
+    with pytest.raises(TypeError):
+        pcr.token_embed(table, ids, out, first_id=7.0)
